@@ -58,7 +58,9 @@ typedef enum {
   TA_ERR_UNSUPPORTED = -2,   /* valid but not built (e.g. d not in {64,128})  */
   TA_ERR_WORKSPACE = -3,     /* workspace too small                           */
   TA_ERR_CUDA = -4,          /* a CUDA runtime / driver call failed           */
-  TA_ERR_TIMEOUT = -5        /* a kernel's bounded wait ran out (device side) */
+  TA_ERR_TIMEOUT = -5,       /* a kernel's bounded wait ran out (device side) */
+  TA_ERR_BAD_INDEX = -6      /* a length or page number read on the device is
+                                out of range (tiered_attn_cache.h)            */
 } ta_status;
 
 typedef enum {

@@ -16,3 +16,8 @@ from .binding import (  # noqa: F401
     workspace_bytes,
 )
 from .binding import LIB_PATH  # noqa: F401
+from .cache import (  # noqa: F401
+    TA_CACHE_BF16, TA_CACHE_FP8, TA_ERR_BAD_INDEX, PagedCache, alloc_cache_workspace, cache_append,
+    cache_decode, cache_select, cache_sparse, cache_workspace_bytes, init_cache_workspace,
+    make_cache, make_cache_params,
+)

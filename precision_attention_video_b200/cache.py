@@ -1,0 +1,305 @@
+"""Cached attention: a paged key-value cache with its append, decode, page
+choice and sparse attention (the C ABI of include/tiered_attn_cache.h).
+
+Argument marshalling only, as in ``binding``: the operators run in the
+library's CUDA kernels, the caller owns every buffer.  Strides come from the
+tensors of each call, sizes from the parameters::
+
+    p = pav.make_cache_params(n_pages=P, page_size=64, H=32, Hkv=8, d=128, S=S, T=T,
+                              max_pages=W, n_select=16, rot_dim=128)
+    ws = pav.alloc_cache_workspace(p, "cuda")
+    cache = pav.make_cache(p, "cuda")
+    pav.cache_append(p, cache, K, V, table, lens, ws, cu=cu, cos=cos, sin=sin, Q=Q, Q_out=Q)
+    pav.cache_select(p, cache, Q, table, lens, ws, sel, cu=cu)
+    pav.cache_sparse(p, cache, Q, sel, table, lens, ws, O, cu=cu)
+"""
+
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import binding as _b
+from .binding import TieredAttnError, _check
+
+TA_ERR_BAD_INDEX = -6
+TA_CACHE_BF16, TA_CACHE_FP8 = 0, 1
+
+_i32, _i64, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
+
+
+class ta_cache_params(ctypes.Structure):
+    _fields_ = [(n, _i32) for n in (
+        "n_pages", "page_size", "H", "Hkv", "d", "format", "S", "T", "max_pages", "n_select",
+        "n_first", "n_recent", "rot_dim", "rot_interleaved", "rot_rows")] + [
+        ("softmax_scale", ctypes.c_float)] + [(n, _i64) for n in (
+            "stride_page", "stride_head", "stride_slot", "stride_table", "stride_k_t",
+            "stride_k_h", "stride_v_t", "stride_v_h", "stride_q_t", "stride_q_h", "stride_o_t",
+            "stride_o_h")]
+
+
+class ta_cache(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("k", "v", "k_scale", "v_scale", "k_mean")]
+
+
+_P = ctypes.POINTER(ta_cache_params)
+_C = ctypes.POINTER(ta_cache)
+_SIGS = {
+    "tiered_attn_cache_workspace_bytes": (ctypes.c_size_t, [_P]),
+    "tiered_attn_cache_init": (ctypes.c_int, [_vp, ctypes.c_size_t, _vp]),
+    "tiered_attn_cache_append": (ctypes.c_int, [_P, _C] + [_vp] * 11 + [ctypes.c_size_t, _vp]),
+    "tiered_attn_cache_decode": (ctypes.c_int, [_P, _C] + [_vp] * 6 + [ctypes.c_size_t, _vp]),
+    "tiered_attn_cache_select": (ctypes.c_int, [_P, _C] + [_vp] * 6 + [ctypes.c_size_t, _vp]),
+    "tiered_attn_cache_sparse": (ctypes.c_int, [_P, _C] + [_vp] * 8 + [ctypes.c_size_t, _vp]),
+}
+_fns = {}
+
+
+def _fn(name):
+    f = _fns.get(name)
+    if f is None:
+        f = getattr(_b.lib(), name)
+        f.restype, f.argtypes = _SIGS[name]
+        _fns[name] = f
+    return f
+
+
+def make_cache_params(*, n_pages: int, page_size: int, H: int, Hkv: int, d: int, S: int, T: int,
+                      max_pages: int, format: int = TA_CACHE_BF16, n_select: int = 0,
+                      n_first: int = 1, n_recent: int = 1, rot_dim: int = 0,
+                      rot_interleaved: int = 0, softmax_scale: float = 0.0) -> ta_cache_params:
+    """Sizes of a cache and of a step: S sequences with T new tokens in all
+    (the buffers' rows), at most max_pages pages each."""
+    p = ta_cache_params()
+    p.n_pages, p.page_size, p.H, p.Hkv, p.d, p.format = n_pages, page_size, H, Hkv, d, format
+    p.S, p.T, p.max_pages = S, T, max_pages
+    p.n_select, p.n_first, p.n_recent = n_select, n_first, n_recent
+    p.rot_dim, p.rot_interleaved, p.softmax_scale = rot_dim, rot_interleaved, softmax_scale
+    return p
+
+
+class PagedCache:
+    """The cache's tensors, each on one CUDA device: ``k`` and ``v`` bf16 or
+    float8_e4m3fn [n_pages, Hkv, page_size, d] (any order of the outer three
+    dimensions in memory), ``k_scale`` and ``v_scale`` f32 [n_pages, Hkv,
+    page_size] for FP8, ``k_mean`` f32 [n_pages, Hkv, d] where pages are
+    chosen.  ``k`` and ``v`` may be None for a cache that is only chosen from."""
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "k_mean", "_c", "_strides", "_shape", "_fmt",
+                 "_dev")
+
+    def __init__(self, k, v, k_scale=None, v_scale=None, k_mean=None):
+        some = k if k is not None else k_mean
+        if some is None:
+            raise ValueError("PagedCache: neither keys nor means")
+        self._dev = some.get_device()
+        self._fmt, self._shape, self._strides = None, None, (0, 0, 0)
+        if k is not None:
+            if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+                raise TypeError(f"k: expected torch.bfloat16 or torch.float8_e4m3fn, got {k.dtype}")
+            if not isinstance(v, torch.Tensor) or v.dtype != k.dtype:
+                raise TypeError("v: expected a tensor of k's type")
+            if k.dim() != 4 or v.shape != k.shape or v.stride() != k.stride() or k.stride(3) != 1:
+                raise ValueError("k, v: expected [n_pages, Hkv, page_size, d] with equal strides, "
+                                 "d contiguous")
+            self._fmt = TA_CACHE_FP8 if k.dtype == torch.float8_e4m3fn else TA_CACHE_BF16
+            self._shape, self._strides = tuple(k.shape), k.stride()[:3]
+            if self._fmt == TA_CACHE_FP8:
+                for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+                    _plain(name, t, torch.float32, self._shape[:3], self._dev)
+        if k_mean is not None:
+            if k_mean.dim() != 3:
+                raise ValueError("k_mean: expected [n_pages, Hkv, d]")
+            want = tuple(k_mean.shape) if k is None else (*self._shape[:2], self._shape[3])
+            _plain("k_mean", k_mean, torch.float32, want, self._dev)
+        for name, t in (("k", k), ("v", v)):
+            if t is not None and t.get_device() != self._dev:
+                raise ValueError(f"{name}: not on the cache's device")
+        self.k, self.v, self.k_scale, self.v_scale, self.k_mean = k, v, k_scale, v_scale, k_mean
+        self._c = ta_cache(*(t.data_ptr() if t is not None else None
+                             for t in (k, v, k_scale, v_scale, k_mean)))
+
+
+def make_cache(p: ta_cache_params, device="cuda", layout: str = "hnd",
+               means: bool = True) -> PagedCache:
+    """A new cache for ``p``: zeroed pages, head-major ("hnd": [n_pages, Hkv,
+    page_size, d]) or token-major ("nhd": [n_pages, page_size, Hkv, d])."""
+    if layout not in ("hnd", "nhd"):
+        raise ValueError(f"layout: expected 'hnd' or 'nhd', got {layout!r}")
+    fp8 = p.format == TA_CACHE_FP8
+    dt = torch.float8_e4m3fn if fp8 else torch.bfloat16
+    a, b = (p.Hkv, p.page_size) if layout == "hnd" else (p.page_size, p.Hkv)
+
+    def codes():
+        x = torch.zeros((p.n_pages, a, b, p.d), dtype=torch.uint8 if fp8 else dt, device=device)
+        x = x.view(dt) if fp8 else x
+        return x if layout == "hnd" else x.transpose(1, 2)
+
+    def scales():
+        return torch.ones((p.n_pages, p.Hkv, p.page_size), device=device) if fp8 else None
+
+    return PagedCache(codes(), codes(), scales(), scales(),
+                      torch.zeros((p.n_pages, p.Hkv, p.d), device=device) if means else None)
+
+
+def cache_workspace_bytes(p: ta_cache_params) -> int:
+    return int(_fn("tiered_attn_cache_workspace_bytes")(ctypes.byref(p)))
+
+
+def alloc_cache_workspace(p: ta_cache_params, device="cuda") -> torch.Tensor:
+    """A workspace for every cached-attention call with ``p``, ready for use
+    on the current stream."""
+    n = cache_workspace_bytes(p)
+    if n == 0:
+        raise TieredAttnError("tiered_attn_cache_workspace_bytes", _b.TA_ERR_INVALID_ARG)
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    with torch.cuda.device(ws.device):
+        init_cache_workspace(ws)
+    return ws
+
+
+def init_cache_workspace(ws: torch.Tensor, stream=None) -> None:
+    """Clear a workspace: before its first use, and to forget its status."""
+    _check("tiered_attn_cache_init", _fn("tiered_attn_cache_init")(
+        _b._ws(ws), ws.numel(), _b._stream(stream)))
+
+
+def _plain(name, t, dtype, shape, dev) -> int:
+    """Pointer of a contiguous tensor of this type and shape on device `dev`."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: expected a tensor on device {dev}, got one on {t.device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor of shape {tuple(shape)}, got "
+                         f"{tuple(t.shape)} with strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _rows(name, t, shape, dev) -> int:
+    """Pointer of a bf16 [rows, heads, d] tensor, d contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: expected a tensor on device {dev}, got one on {t.device}")
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
+    if t.shape != shape or t.stride(2) != 1:
+        raise ValueError(f"{name}: expected shape {tuple(shape)} with the last dimension "
+                         f"contiguous, got {tuple(t.shape)} with strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _begin(p, cache, table, lens, ws, cu, kv: bool):
+    """Checks shared by every call; (a copy of p with the cache's strides,
+    device, pointers of table, lens, cu, ws)."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    if cache._dev < 0:
+        raise ValueError("cache: expected CUDA tensors")
+    if cache._dev != dev:
+        raise ValueError(f"cache: on cuda:{cache._dev}, but the library launches on the current "
+                         f"device cuda:{dev}")
+    if kv:
+        if cache._shape is None:
+            raise ValueError("cache: has no keys and values")
+        if cache._shape != (p.n_pages, p.Hkv, p.page_size, p.d) or cache._fmt != p.format:
+            raise ValueError(f"cache: shape {cache._shape}, format {cache._fmt}, but the "
+                             f"parameters say {(p.n_pages, p.Hkv, p.page_size, p.d)}, {p.format}")
+    q = ta_cache_params.from_buffer_copy(p)
+    q.stride_page, q.stride_head, q.stride_slot = cache._strides
+    if not isinstance(table, torch.Tensor):
+        raise TypeError(f"table: expected a torch.Tensor, got {type(table).__name__}")
+    if table.get_device() != dev or table.dtype is not torch.int32:
+        raise TypeError(f"table: expected torch.int32 on cuda:{dev}, got {table.dtype} on {table.device}")
+    if table.dim() != 2 or table.shape[0] != p.S or table.shape[1] < p.max_pages or \
+            table.stride(1) != 1:
+        raise ValueError(f"table: expected [{p.S}, >= {p.max_pages}] with contiguous rows, got "
+                         f"{tuple(table.shape)} with strides {table.stride()}")
+    q.stride_table = table.stride(0)
+    ln = _plain("lens", lens, torch.int32, (p.S,), dev)
+    c = None if cu is None else _plain("cu", cu, torch.int32, (p.S + 1,), dev)
+    return q, dev, table.data_ptr(), ln, c, _plain("ws", ws, torch.uint8, (ws.numel(),), dev)
+
+
+def _stream_of(stream, dev) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return _b._stream(stream)
+
+
+def cache_append(p: ta_cache_params, cache: PagedCache, K, V, table, lens, ws, cu=None, cos=None,
+                 sin=None, pos=None, Q=None, Q_out=None, stream=None) -> None:
+    """Append the new tokens K, V bf16 [T, Hkv, d] to the cache, keys rotated
+    by the table rows ``pos`` (their positions, where None) of ``cos`` and
+    ``sin`` (f32 [rows, rot_dim / 2]); rotate Q [T, H, d] into ``Q_out`` (may
+    be Q itself) with the same angles.  ``lens`` counts the new tokens."""
+    q, dev, tb, ln, c, w = _begin(p, cache, table, lens, ws, cu, True)
+    k = _rows("K", K, (p.T, p.Hkv, p.d), dev)
+    v = _rows("V", V, (p.T, p.Hkv, p.d), dev)
+    q.stride_k_t, q.stride_k_h, _ = K.stride()
+    q.stride_v_t, q.stride_v_h, _ = V.stride()
+    qi = qo = cp = sp = pp = None
+    if Q is not None:
+        qi = _rows("Q", Q, (p.T, p.H, p.d), dev)
+        qo = _rows("Q_out", Q_out, (p.T, p.H, p.d), dev)
+        if qi == qo and Q.stride() != Q_out.stride():
+            raise ValueError("Q_out: shares Q's memory with other strides")
+        q.stride_q_t, q.stride_q_h, _ = Q.stride()
+        q.stride_o_t, q.stride_o_h, _ = Q_out.stride()
+    if p.rot_dim:
+        if not isinstance(cos, torch.Tensor):
+            raise TypeError(f"cos: expected a torch.Tensor, got {type(cos).__name__}")
+        q.rot_rows = cos.shape[0]
+        cp = _plain("cos", cos, torch.float32, (q.rot_rows, p.rot_dim // 2), dev)
+        sp = _plain("sin", sin, torch.float32, (q.rot_rows, p.rot_dim // 2), dev)
+    if pos is not None:
+        pp = _plain("pos", pos, torch.int32, (p.T,), dev)
+    _check("tiered_attn_cache_append", _fn("tiered_attn_cache_append")(
+        q, cache._c, k, v, qi, qo, cp, sp, pp, c, ln, tb, w, ws.numel(), _stream_of(stream, dev)))
+
+
+def cache_decode(p: ta_cache_params, cache: PagedCache, Q, table, lens, ws, O,
+                 lse: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Attention of one new token for each sequence, Q bf16 [S, H, d], over
+    its whole cache into O (and ``lse`` f32 [S, H])."""
+    q, dev, tb, ln, _, w = _begin(p, cache, table, lens, ws, None, True)
+    qp = _rows("Q", Q, (p.T, p.H, p.d), dev)
+    op = _rows("O", O, (p.T, p.H, p.d), dev)
+    lp = None if lse is None else _plain("lse", lse, torch.float32, (p.T, p.H), dev)
+    q.stride_q_t, q.stride_q_h, _ = Q.stride()
+    q.stride_o_t, q.stride_o_h, _ = O.stride()
+    _check("tiered_attn_cache_decode", _fn("tiered_attn_cache_decode")(
+        q, cache._c, qp, ln, tb, op, lp, w, ws.numel(), _stream_of(stream, dev)))
+
+
+def cache_select(p: ta_cache_params, cache: PagedCache, Q, table, lens, ws, sel, cu=None,
+                 stream=None) -> None:
+    """The pages that each row reads: ``sel`` int32 [T, Hkv, n_select], page
+    indices of the row's sequence in ascending order, then -1."""
+    q, dev, tb, ln, c, w = _begin(p, cache, table, lens, ws, cu, False)
+    if cache.k_mean is None or cache.k_mean.shape != (p.n_pages, p.Hkv, p.d):
+        raise ValueError(f"cache: expected k_mean of shape {(p.n_pages, p.Hkv, p.d)}")
+    qp = _rows("Q", Q, (p.T, p.H, p.d), dev)
+    sl = _plain("sel", sel, torch.int32, (p.T, p.Hkv, p.n_select), dev)
+    q.stride_q_t, q.stride_q_h, _ = Q.stride()
+    _check("tiered_attn_cache_select", _fn("tiered_attn_cache_select")(
+        q, cache._c, qp, c, ln, tb, sl, w, ws.numel(), _stream_of(stream, dev)))
+
+
+def cache_sparse(p: ta_cache_params, cache: PagedCache, Q, sel, table, lens, ws, O, cu=None,
+                 lse: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Attention of each row, Q bf16 [T, H, d], over the pages of its list
+    ``sel`` into O (and ``lse`` f32 [T, H])."""
+    q, dev, tb, ln, c, w = _begin(p, cache, table, lens, ws, cu, True)
+    qp = _rows("Q", Q, (p.T, p.H, p.d), dev)
+    op = _rows("O", O, (p.T, p.H, p.d), dev)
+    sl = _plain("sel", sel, torch.int32, (p.T, p.Hkv, p.n_select), dev)
+    lp = None if lse is None else _plain("lse", lse, torch.float32, (p.T, p.H), dev)
+    q.stride_q_t, q.stride_q_h, _ = Q.stride()
+    q.stride_o_t, q.stride_o_h, _ = O.stride()
+    _check("tiered_attn_cache_sparse", _fn("tiered_attn_cache_sparse")(
+        q, cache._c, qp, sl, c, ln, tb, op, lp, w, ws.numel(), _stream_of(stream, dev)))

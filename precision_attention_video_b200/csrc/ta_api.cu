@@ -321,6 +321,7 @@ const char* tiered_attn_status_string(ta_status s) {
     case TA_ERR_WORKSPACE: return "workspace too small";
     case TA_ERR_CUDA: return "CUDA error";
     case TA_ERR_TIMEOUT: return "device wait timed out";
+    case TA_ERR_BAD_INDEX: return "length or page number out of range";
   }
   return "unknown status";
 }

@@ -1,0 +1,120 @@
+// ta_cache.cuh -- argument block, launchers and device helpers of the
+// cached-attention kernels (append, decode, page choice, sparse attention).
+#pragma once
+
+#include "ta_common.cuh"
+#include "tiered_attn_cache.h"
+
+namespace ta {
+
+// Fixed part of a cache workspace, the same whatever the parameters, so that
+// calls with different ones can take turns on a workspace: the status word,
+// one arrival counter and two partial results for each CTA of the attention
+// grid.
+constexpr int kMaxAttnCtas = 512;
+constexpr int kMaxTileHeads = 16;                 // query heads of one CTA's item
+constexpr size_t kWsCounters = 256;
+constexpr size_t kWsPartML = kWsCounters + kMaxAttnCtas * 4;
+constexpr size_t kWsPartO = kWsPartML + (size_t)kMaxAttnCtas * 2 * 2 * kMaxTileHeads * 4;
+constexpr size_t kWsScratch = kWsPartO + (size_t)kMaxAttnCtas * 2 * kMaxTileHeads * 128 * 4;
+
+struct CacheArgs {
+  int n_pages, page_size, ps_log2;
+  int H, Hkv, G, d, fp8;
+  int S, T, max_pages;
+  int n_select, n_first, n_recent;
+  int rot_dim, rot_interleaved, rot_rows;
+  float scale_log2;               // softmax scale * log2(e)
+  double scale;                   // softmax scale (fp64, page choice)
+  int64_t s_page, s_head, s_slot; // cache code strides (elements)
+  int64_t s_table;
+  int64_t sk_t, sk_h, sv_t, sv_h, sq_t, sq_h, so_t, so_h;
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  float* k_mean;
+  const __nv_bfloat16* k_new;
+  const __nv_bfloat16* v_new;
+  const __nv_bfloat16* q;
+  __nv_bfloat16* o;               // O, or the rotated queries of an append
+  float* lse;
+  const float* cos;
+  const float* sin;
+  const int* pos;
+  const int* cu;                  // null: one row for each sequence
+  const int* lens;
+  const int* table;
+  int* sel;
+  int* status;
+  int* counters;
+  float* part_ml;
+  float* part_o;
+  double* scratch;
+};
+
+cudaError_t launch_cache_append(const CacheArgs& a, cudaStream_t s);
+cudaError_t launch_cache_select(const CacheArgs& a, cudaStream_t s);
+// `sparse`: over the lists in a.sel, else over whole sequences.
+cudaError_t launch_cache_attn(const CacheArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
+                              bool sparse, cudaStream_t s);
+
+#ifdef __CUDACC__
+
+__device__ __forceinline__ void report_bad_index(int* status) {
+  if (atomicCAS(status + ST_CODE, 0, (int)TA_ERR_BAD_INDEX) == 0)
+    status[ST_BLOCK] = (int)(blockIdx.x + gridDim.x * blockIdx.y);
+}
+
+// Length of sequence s, clamped to what its table row can hold.
+__device__ __forceinline__ int seq_len(const CacheArgs& a, int s) {
+  const int n = a.lens[s];
+  const int64_t most = (int64_t)a.max_pages << a.ps_log2;
+  if (n < 0 || n > most) {
+    report_bad_index(a.status);
+    return n < 0 ? 0 : (int)most;
+  }
+  return n;
+}
+
+// Rows in use: everything from cu[S] on is padding.
+__device__ __forceinline__ int rows_used(const CacheArgs& a) {
+  if (!a.cu) return a.S;
+  const int n = a.cu[a.S];
+  return n < 0 ? 0 : (n > a.T ? a.T : n);
+}
+
+// Sequence of row t, and the row's position in it (-1 where the row has
+// none: before the sequence's first position, or a malformed cu).
+__device__ __forceinline__ int row_seq(const CacheArgs& a, int t) {
+  if (!a.cu) return t;
+  int lo = 0, hi = a.S - 1;       // largest s with cu[s] <= t
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.cu[mid] <= t) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+__device__ __forceinline__ int row_pos(const CacheArgs& a, int t, int s) {
+  const int n = seq_len(a, s);
+  const int64_t back = a.cu ? (int64_t)a.cu[s + 1] - t : 1;
+  const int64_t p = n - back;
+  if (p >= 0 && p < n) return (int)p;
+  if (a.cu) report_bad_index(a.status);   // (without cu, an empty sequence has no row)
+  return -1;
+}
+
+// Physical page of entry e of sequence s; -1 (and the status) when the table
+// holds a number outside the cache.
+__device__ __forceinline__ int page_of(const CacheArgs& a, int s, int e) {
+  const int pg = a.table[(int64_t)s * a.s_table + e];
+  if (pg < 0 || pg >= a.n_pages) {
+    report_bad_index(a.status);
+    return -1;
+  }
+  return pg;
+}
+
+#endif  // __CUDACC__
+
+}  // namespace ta
