@@ -135,7 +135,8 @@ ta_status tiered_attn_cache_append(const ta_cache_params* p, const ta_cache* cac
  * The keys are split evenly over the GPU and the parts joined in a fixed
  * order; the result depends on the lengths and not on timing.  O_dev: bf16
  * [S, H, d]; lse_dev: f32 [S, H] ln sum_i exp(scale * q . k_i), or NULL.  An
- * empty sequence gives O = 0 and lse = -inf.  One launch. */
+ * empty sequence gives O = 0 and lse = -inf.  At most 2048 sequences (else
+ * TA_ERR_UNSUPPORTED).  One launch. */
 ta_status tiered_attn_cache_decode(const ta_cache_params* p, const ta_cache* cache,
                                    const void* Q_dev, const int32_t* seq_lens_dev,
                                    const int32_t* table_dev, void* O_dev, float* lse_dev,

@@ -240,7 +240,7 @@ ta_status tiered_attn_cache_decode(const ta_cache_params* p, const ta_cache* cac
   if (st != TA_OK) return st;
   // the kernel keeps a prefix over the sequences in shared memory, in 31 bits
   const int64_t units = ((int64_t)p->max_pages * p->page_size + 127) / 128;
-  if (p->S > 4096 || p->S * units > 0x7fffffff) return TA_ERR_UNSUPPORTED;
+  if (p->S > 2048 || p->S * units > 0x7fffffff) return TA_ERR_UNSUPPORTED;
   return attend(p, cache, Q, nullptr, nullptr, lens, table, O, lse, ws, ws_bytes, stream, false);
 }
 

@@ -9,12 +9,15 @@
 // m = max m_a, l = sum 2^{m_a - m} l_a, n = sum 2^{m_a - m} n_a.
 //
 // Layout of the work.  An item is a (row, key head); its keys go in units of
-// 128.  The units of all items, in order, are cut into equal runs, one for
-// each CTA, whatever the lengths: a run may end inside an item, whose parts
-// then meet in the workspace, where the CTA that arrives last joins them in
-// the order of the parts.  Within a CTA one warp loads (TMA, one box a page
-// and 128-byte column) and four warps compute, each on 32 keys of a unit with
-// a softmax state of its own, joined at the item's end.
+// 128 (bf16, d = 128) or 256.  The units of all items, in order, are cut into
+// equal runs, one for each CTA, whatever the lengths: a run may end inside an
+// item, whose parts then meet in the workspace, where the CTA that arrives
+// last joins them in the order of the parts.  Within a CTA one warp loads
+// (TMA, one box a page and 128-byte column) and eight warps compute, each on
+// 16 or 32 keys of a unit with a softmax state of its own, joined at the
+// item's end.  (Four warps instead of eight: 238 us against 133 for 4
+// sequences of up to 131072 tokens in FP8, with the conversions below; one
+// warp on a scheduler does not hide its own latencies.)
 //
 // The products run transposed, S^T = K Q^T and O^T = V^T P^T, with mma.sync
 // m16n8k16: the keys (or the head dim) fill the 16 rows and the query heads
@@ -22,34 +25,42 @@
 // nothing of the M side.  The operator is bound by the cache's bytes: a key
 // head's 256 bytes of one key need 2 * 8 * 128 multiply-adds at most, a tenth
 // of what mma.sync does in that time, so tcgen05 (M = 128 rows) would only
-// idle.  P is rounded to bf16 for the second product (at most 2^-9 relative
-// for each weight, the size of O's own rounding); l sums the unrounded
-// weights in fp32.
+// idle.
+//
+// bf16 caches multiply in bf16, P rounded to it (at most 2^-8 relative for
+// each weight, as O's own rounding).  FP8 caches multiply in f16, which holds
+// every e4m3 value and which one conversion instruction reaches for two codes
+// (bf16 took five on the integer pipe, half of all issue slots); K's scale
+// multiplies a score, V's the weight.  l sums the unrounded weights in fp32.
+#include <type_traits>
+
 #include "ta_cache.cuh"
 
 namespace ta {
 namespace {
 
-constexpr int kUnit = 128;               // keys of a unit (one pipeline stage)
-constexpr int kWarps = 4;                // computing warps, 32 keys of a unit each
+constexpr int kWarps = 8;                // computing warps
 constexpr int kThreads = 32 * (kWarps + 1);
 
 template <int D, bool FP8, int NT>
 struct Cfg {
   static constexpr int kRow = D * (FP8 ? 1 : 2);          // bytes of a key
+  static constexpr int kKT = kRow > 128 ? 1 : 2;          // 16-key tiles of a warp
+  static constexpr int kUnit = kWarps * 16 * kKT;         // keys of a unit (one stage)
   static constexpr int kCols = kRow > 128 ? 2 : 1;        // 128-byte columns of a row
   static constexpr int kColB = kRow / kCols;              // 128 or 64
-  static constexpr int kTile = kUnit * kRow;
+  static constexpr int kTile = kUnit * kRow;               // 16 or 32 KB
   static constexpr int kScales = FP8 ? kUnit * 4 : 0;
   static constexpr int kStage = 2 * kTile + 2 * kScales;
-  static constexpr int kStages = kStage > 40000 ? 3 : (kStage > 20000 ? 5 : 8);
+  static constexpr int kStages = kStage > 40000 ? 3 : 6;
   static constexpr int kRegs = D / 16 * NT * 4;           // accumulators of a lane
   static constexpr int oJoin = kStages * ((kStage + 1023) / 1024 * 1024);
-  static constexpr int oML = oJoin + 2 * kRegs * 32 * 4;
+  static constexpr int kJoin = NT == 1 ? 4 : 2;           // warps that join at a time
+  static constexpr int oML = oJoin + kJoin * kRegs * 32 * 4;
   static constexpr int oCnt = oML + 2 * 2 * kWarps * kMaxTileHeads * 4;  // m, l; items take turns
-  static constexpr int oBar = oCnt + kStages * 8 * 4;
+  static constexpr int oBar = oCnt + kStages * (kUnit / 16) * 4;
   static constexpr int oMisc = oBar + 2 * kStages * 8;
-  static constexpr int oPre = oMisc + 64;
+  static constexpr int oPre = oMisc + 128;
   static constexpr int kBytes = oPre + 1024;              // 1024 to align; + a decode's prefix
   static constexpr int kStageStep = (kStage + 1023) / 1024 * 1024;
 };
@@ -71,28 +82,44 @@ __device__ __forceinline__ uint32_t movm(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
+template <bool F16>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  if constexpr (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
 }
-// Two e4m3 codes, in bytes 1 and 3 of w, to bf16x2 (exact): exponent and
-// mantissa moved to bf16's places give the value times 2^-120 (the biases
-// differ by 120; a subnormal code becomes a bf16 subnormal), which the
-// product with 2^120 undoes.  The NaN code comes out as 480: a token that
-// holds one has a NaN scale.
-__device__ __forceinline__ uint32_t e4m3_bf16x2(uint32_t w) {
-  const uint32_t t = ((w >> 4) & 0x07F007F0u) | (w & 0x80008000u);
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+// The e4m3 codes in the low or high half of w to f16x2 (exact).
+__device__ __forceinline__ uint32_t e4m3_f16x2_lo(uint32_t w) {
   uint32_t r;
-  asm("mul.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(t), "r"(0x7B807B80u));
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
   return r;
+}
+__device__ __forceinline__ uint32_t e4m3_f16x2_hi(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+// 2^floor(log2 x) of a normal x > 0.
+__device__ __forceinline__ float pow2_of(float x) {
+  return __uint_as_float(__float_as_uint(x) & 0x7F800000u);
 }
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -112,11 +139,11 @@ __device__ __forceinline__ void compute_sync() {
 }
 
 // Where a run of units stands: row, head group, and unit of that item.
-template <bool SPARSE>
+template <bool SPARSE, int UNIT>
 struct Cursor {
   int row, hx, k, units;
   __device__ __forceinline__ int units_of(const CacheArgs& a, const int* pre, int r) const {
-    return SPARSE ? (a.n_select * a.page_size + kUnit - 1) / kUnit : pre[r + 1] - pre[r];
+    return SPARSE ? (a.n_select * a.page_size + UNIT - 1) / UNIT : pre[r + 1] - pre[r];
   }
   __device__ __forceinline__ void start(const CacheArgs& a, const int* pre, int rows, int HX,
                                         int64_t u) {
@@ -158,6 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const CacheArgs a) {
   using C = Cfg<D, FP8, NT>;
   constexpr int NH = 8 * NT;                       // query heads of an item
+  constexpr int KT = C::kKT, kUnit = C::kUnit, kGroups = kUnit / 16;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -198,10 +226,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
-    if (lane == 31) misc[4 + warp] = inc;
+    if (lane == 31) misc[8 + warp] = inc;
     __syncthreads();
     int base = inc - sum;
-    for (int w = 0; w < warp; ++w) base += misc[4 + w];
+    for (int w = 0; w < warp; ++w) base += misc[8 + w];
     for (int r = r0; r < r1; ++r) {
       pre[r] = base;
       base += (seq_len(a, r) + kUnit - 1) / kUnit;
@@ -226,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if ((int64_t)blockIdx.x >= n) return;
   const int64_t u0 = W * blockIdx.x / n, u1 = W * (blockIdx.x + 1) / n;
   const int n_units = (int)(u1 - u0);
-  Cursor<SPARSE> cur;
+  Cursor<SPARSE, kUnit> cur;
   cur.start(a, pre, rows, HX, u0);
 
   if (warp == kWarps) {
@@ -255,9 +283,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t live = __ballot_sync(0xffffffffu, vc > 0);
       if (i >= C::kStages && !mbar_wait(&empty[st], ((i / C::kStages) - 1) & 1, abort, 1)) break;
       unsigned char* stage = smem + st * C::kStageStep;
-      const int v16 = __shfl_sync(0xffffffffu, vc, (lane & 7) >> (a.ps_log2 - 4));
-      if (lane < 8)
-        cnt[st * 8 + lane] = min(16, max(0, v16 - 16 * (lane & ((1 << (a.ps_log2 - 4)) - 1))));
+      const int v16 = __shfl_sync(0xffffffffu, vc, (lane & (kGroups - 1)) >> (a.ps_log2 - 4));
+      if (lane < kGroups)
+        cnt[st * kGroups + lane] = min(16, max(0, v16 - 16 * (lane & ((1 << (a.ps_log2 - 4)) - 1))));
       __syncwarp();
       if (lane == 0) {
         const uint32_t bytes = (uint32_t)a.page_size * (2 * C::kRow + (FP8 ? 8 : 0));
@@ -295,7 +323,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const float sc = a.scale_log2;
   uint32_t qf[D / 16][NT][2];
   float acc[D / 16][NT][4];
-  float m[NT][2], l[NT][2];
+  float m[NT][2], l[NT][2];      // running maximum (of s * sq, log2 units) and sum
+  float sq[NT][2];               // what a raw product counts for, in log2 units
+  float vmax = 1.0f;             // FP8: the numerators' unit, the largest V scale so far
   float* join = reinterpret_cast<float*>(smem + C::oJoin);
   const float kNegInf = -__int_as_float(0x7f800000);
   bool fresh = true;                               // no unit of the item taken yet
@@ -310,6 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (fresh) {
       fresh = false;
       k_first = cur.k;
+      vmax = 0.0f;
       const __nv_bfloat16* q = a.q + (int64_t)cur.row * a.sq_t + (int64_t)h0 * a.sq_h;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -323,6 +354,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           qf[c][nt][0] = on ? *reinterpret_cast<const uint32_t*>(qh + d0) : 0u;
           qf[c][nt][1] = on ? *reinterpret_cast<const uint32_t*>(qh + d1) : 0u;
         }
+        if constexpr (FP8) {
+          // FP8 keys are f16 operands, so the query is one too, its largest
+          // element scaled to [2^8, 2^9) by a power of two: what falls below
+          // f16's smallest step is under 2^-33 of that element
+          uint32_t am = 0;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              am = max(am, max((qf[c][nt][e] & 0x7FFFu) << 16, qf[c][nt][e] & 0x7FFF0000u));
+          am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+          am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+          // (a head of zeros or with values that are not finite is left as it is)
+          const float ax = __uint_as_float(am);
+          const bool plain = ax >= 1e-35f && ax <= 3.4e38f;
+          const float up = plain ? 256.0f / pow2_of(ax) : 1.0f;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t w = qf[c][nt][e];
+              qf[c][nt][e] = pack_f16(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xFFFF0000u) * up);
+            }
+          const float down = plain ? pow2_of(ax) * 0.00390625f : 1.0f;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)                // from the lanes that hold head 2 tg + j
+            sq[nt][j] = sc * __shfl_sync(0xffffffffu, down, (2 * tg + j) * 4);
+        } else {
+          sq[nt][0] = sq[nt][1] = sc;
+        }
         m[nt][0] = m[nt][1] = kNegInf;
         l[nt][0] = l[nt][1] = 0.0f;
 #pragma unroll
@@ -332,14 +393,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     const bool ok = mbar_wait(&full[st], (i / C::kStages) & 1, abort, 2);
-    const int c0 = ok ? cnt[st * 8 + 2 * warp] : 0, c1 = ok ? cnt[st * 8 + 2 * warp + 1] : 0;
-    if (c0 | c1) {
+    int cn[KT], any = 0;                           // keys of this warp's tiles
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) {
+      cn[kt] = ok ? cnt[st * kGroups + KT * warp + kt] : 0;
+      any |= cn[kt];
+    }
+    if (any) {
       const uint32_t kbase = smem_u32(smem + st * C::kStageStep);
       const uint32_t vbase = kbase + C::kTile;
-      const int key0 = warp * 32;
-      float s[2][NT][4];
+      const int key0 = warp * 16 * KT;
+      float s[KT][NT][4];
 #pragma unroll
-      for (int kt = 0; kt < 2; ++kt)
+      for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -355,55 +421,60 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < D / 16; ++c)
 #pragma unroll
-          for (int kt = 0; kt < 2; ++kt) {
+          for (int kt = 0; kt < KT; ++kt) {
             uint32_t r[4];
             ldsm4(r, chunk(kbase, key0 + kt * 16 + (lane & 15), 2 * c + (lane >> 4)));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma16816(s[kt][nt], r[0], r[1], r[2], r[3], qf[c][nt][0], qf[c][nt][1]);
+              mma16816<false>(s[kt][nt], r[0], r[1], r[2], r[3], qf[c][nt][0], qf[c][nt][1]);
           }
       } else {
 #pragma unroll
         for (int c = 0; c < D / 16; c += 2)
 #pragma unroll
-          for (int kt = 0; kt < 2; ++kt) {
+          for (int kt = 0; kt < KT; ++kt) {
             uint32_t r[4];   // rows 0-7 and 8-15 of chunk c, then of chunk c + 1
             ldsm4(r, chunk(kbase, key0 + kt * 16 + (lane & 15), c + (lane >> 4)));
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const uint32_t x = r[2 * e], y = r[2 * e + 1];
-              const uint32_t a0 = e4m3_bf16x2(__byte_perm(x, 0, 0x1404));
-              const uint32_t a2 = e4m3_bf16x2(__byte_perm(x, 0, 0x3424));
-              const uint32_t a1 = e4m3_bf16x2(__byte_perm(y, 0, 0x1404));
-              const uint32_t a3 = e4m3_bf16x2(__byte_perm(y, 0, 0x3424));
+              const uint32_t a0 = e4m3_f16x2_lo(x), a2 = e4m3_f16x2_hi(x);
+              const uint32_t a1 = e4m3_f16x2_lo(y), a3 = e4m3_f16x2_hi(y);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
-                mma16816(s[kt][nt], a0, a1, a2, a3, qf[c + e][nt][0], qf[c + e][nt][1]);
+                mma16816<true>(s[kt][nt], a0, a1, a2, a3, qf[c + e][nt][0], qf[c + e][nt][1]);
             }
           }
       }
-      // hidden keys, key scales, running maximum
-      const float* kss = reinterpret_cast<const float*>(smem + st * C::kStageStep + 2 * C::kTile);
-      const float* vss = kss + kUnit;
+      // scores in log2 units, hidden keys out, running maximum
+      float vs[KT][2], vm = vmax;
       float mx[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = kNegInf;
 #pragma unroll
-      for (int kt = 0; kt < 2; ++kt) {
-        const int c = kt ? c1 : c0;
-        float f0 = 1.0f, f1 = 1.0f;
-        if (FP8) {
-          f0 = kss[key0 + kt * 16 + g];
-          f1 = kss[key0 + kt * 16 + g + 8];
+      for (int kt = 0; kt < KT; ++kt) {
+        float ks[2] = {1.0f, 1.0f};
+        if constexpr (FP8) {
+          const float* kss = reinterpret_cast<const float*>(smem + st * C::kStageStep + 2 * C::kTile);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = key0 + kt * 16 + g + 8 * e;
+            ks[e] = kss[r];
+            vs[kt][e] = g + 8 * e < cn[kt] ? kss[kUnit + r] : 0.0f;
+            vm = fmaxf(vm, vs[kt][e]);
+          }
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            s[kt][nt][j] = g < c ? (FP8 ? s[kt][nt][j] * f0 : s[kt][nt][j]) : kNegInf;
-            s[kt][nt][j + 2] = g + 8 < c ? (FP8 ? s[kt][nt][j + 2] * f1 : s[kt][nt][j + 2]) : kNegInf;
-            mx[nt][j] = fmax3(mx[nt][j], s[kt][nt][j], s[kt][nt][j + 2]);
+          for (int j = 0; j < 4; ++j) {
+            const float x = FP8 ? s[kt][nt][j] * ks[j >> 1] : s[kt][nt][j];
+            s[kt][nt][j] = g + 8 * (j >> 1) < cn[kt] ? x * sq[nt][j & 1] : kNegInf;
           }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) mx[nt][j] = fmax3(mx[nt][j], s[kt][nt][j], s[kt][nt][j + 2]);
       }
       bool up = false;
 #pragma unroll
@@ -416,88 +487,104 @@ __global__ void __launch_bounds__(kThreads, 1)
           mx[nt][j] = fmaxf(mx[nt][j], m[nt][j]);
           up |= mx[nt][j] > m[nt][j];
         }
+      if constexpr (FP8) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+        up |= vm > vmax;
+      }
       if (__any_sync(0xffffffffu, up)) {
+        const float fv = FP8 && vmax > 0.0f ? vmax / vm : 1.0f;   // powers of two
+        vmax = vm;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float f = m[nt][j] == kNegInf ? 0.0f : ex2((m[nt][j] - mx[nt][j]) * sc);
+            const float f = m[nt][j] == kNegInf ? 0.0f : ex2(m[nt][j] - mx[nt][j]);
             m[nt][j] = mx[nt][j];
             l[nt][j] *= f;
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
-              acc[c][nt][j] *= f;
-              acc[c][nt][j + 2] *= f;
+              acc[c][nt][j] *= f * fv;
+              acc[c][nt][j + 2] *= f * fv;
             }
           }
       }
       // weights, their sums, and P^T as the second product's B operand
-      uint32_t pf[2][NT][2];
+      uint32_t pf[KT][NT][2];
+      float vf[KT][2];
+      if constexpr (FP8) {
+        // f16 weights, the largest V scale's at 2^15: a weight keeps its 11
+        // bits down to 2^-29 of that scale
+        const float iv = vmax > 0.0f ? 1.0f / vmax : 1.0f;
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) vf[kt][e] = vs[kt][e] * iv * 32768.0f;
+      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float mm[2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) mm[j] = m[nt][j] == kNegInf ? 0.0f : m[nt][j] * sc;
+        for (int j = 0; j < 2; ++j) mm[j] = m[nt][j] == kNegInf ? 0.0f : m[nt][j];
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
-          const int c = kt ? c1 : c0;
+        for (int kt = 0; kt < KT; ++kt) {
           float p[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            p[j] = ex2(fmaf(s[kt][nt][j], sc, -mm[j & 1]));
+            p[j] = ex2(s[kt][nt][j] - mm[j & 1]);
             l[nt][j & 1] += p[j];
+            if (FP8) p[j] *= vf[kt][j >> 1];
           }
-          if (FP8) {
-            const float f0 = g < c ? vss[key0 + kt * 16 + g] : 0.0f;
-            const float f1 = g + 8 < c ? vss[key0 + kt * 16 + g + 8] : 0.0f;
-            p[0] *= f0;
-            p[1] *= f0;
-            p[2] *= f1;
-            p[3] *= f1;
-          }
-          pf[kt][nt][0] = movm(pack_bf16(p[0], p[1]));
-          pf[kt][nt][1] = movm(pack_bf16(p[2], p[3]));
+          pf[kt][nt][0] = movm(FP8 ? pack_f16(p[0], p[1]) : pack_bf16(p[0], p[1]));
+          pf[kt][nt][1] = movm(FP8 ? pack_f16(p[2], p[3]) : pack_bf16(p[2], p[3]));
         }
       }
       // O^T += V^T P^T; slots behind the last key hold anything, NaN included
 #pragma unroll
-      for (int kt = 0; kt < 2; ++kt) {
-        const int c = kt ? c1 : c0;
+      for (int kt = 0; kt < KT; ++kt) {
+        const int c = cn[kt];
         if (c == 0) continue;
-        const uint32_t m0 = (2 * tg < c ? 0xFFFFu : 0u) | (2 * tg + 1 < c ? 0xFFFF0000u : 0u);
-        const uint32_t m1 = (2 * tg + 8 < c ? 0xFFFFu : 0u) | (2 * tg + 9 < c ? 0xFFFF0000u : 0u);
-        if constexpr (!FP8) {
-#pragma unroll
-          for (int cd = 0; cd < D / 16; ++cd) {
-            uint32_t r[4];   // keys 0-7 by d 0-7 and 8-15, then keys 8-15
-            ldsm4t(r, chunk(vbase, key0 + kt * 16 + (lane & 7) + ((lane >> 4) << 3),
-                            2 * cd + ((lane >> 3) & 1)));
-            r[0] &= m0;
-            r[1] &= m0;
-            r[2] &= m1;
-            r[3] &= m1;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma16816(acc[cd][nt], r[0], r[1], r[2], r[3], pf[kt][nt][0], pf[kt][nt][1]);
+        auto product = [&](auto whole) {
+          uint32_t m0 = 0xFFFFFFFFu, m1 = 0xFFFFFFFFu;
+          if constexpr (!decltype(whole)::value) {
+            m0 = (2 * tg < c ? 0xFFFFu : 0u) | (2 * tg + 1 < c ? 0xFFFF0000u : 0u);
+            m1 = (2 * tg + 8 < c ? 0xFFFFu : 0u) | (2 * tg + 9 < c ? 0xFFFF0000u : 0u);
           }
-        } else {
+          if constexpr (!FP8) {
 #pragma unroll
-          for (int cd = 0; cd < D / 16; cd += 2) {
-            uint32_t r[4];   // chunk cd by keys 0-7 and 8-15, then chunk cd + 1
-            ldsm4t(r, chunk(vbase, key0 + kt * 16 + (lane & 15), cd + (lane >> 4)));
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t x = r[2 * e], y = r[2 * e + 1];
-              const uint32_t a0 = e4m3_bf16x2(__byte_perm(x, 0, 0x2404)) & m0;
-              const uint32_t a1 = e4m3_bf16x2(__byte_perm(x, 0, 0x3414)) & m0;
-              const uint32_t a2 = e4m3_bf16x2(__byte_perm(y, 0, 0x2404)) & m1;
-              const uint32_t a3 = e4m3_bf16x2(__byte_perm(y, 0, 0x3414)) & m1;
+            for (int cd = 0; cd < D / 16; ++cd) {
+              uint32_t r[4];   // keys 0-7 by d 0-7 and 8-15, then keys 8-15
+              ldsm4t(r, chunk(vbase, key0 + kt * 16 + (lane & 7) + ((lane >> 4) << 3),
+                              2 * cd + ((lane >> 3) & 1)));
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
-                mma16816(acc[cd + e][nt], a0, a1, a2, a3, pf[kt][nt][0], pf[kt][nt][1]);
+                mma16816<false>(acc[cd][nt], r[0] & m0, r[1] & m0, r[2] & m1, r[3] & m1,
+                                pf[kt][nt][0], pf[kt][nt][1]);
+            }
+          } else {
+#pragma unroll
+            for (int cd = 0; cd < D / 16; cd += 2) {
+              uint32_t r[4];   // chunk cd by keys 0-7 and 8-15, then chunk cd + 1
+              ldsm4t(r, chunk(vbase, key0 + kt * 16 + (lane & 15), cd + (lane >> 4)));
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                // bytes (key, d), (key, d + 1), (key + 1, d), (key + 1, d + 1)
+                // to the pairs of keys at d and at d + 1
+                const uint32_t x = __byte_perm(r[2 * e], 0, 0x3120);
+                const uint32_t y = __byte_perm(r[2 * e + 1], 0, 0x3120);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                  mma16816<true>(acc[cd + e][nt], e4m3_f16x2_lo(x) & m0, e4m3_f16x2_hi(x) & m0,
+                                 e4m3_f16x2_lo(y) & m1, e4m3_f16x2_hi(y) & m1, pf[kt][nt][0],
+                                 pf[kt][nt][1]);
+              }
             }
           }
-        }
+        };
+        if (c == 16)
+          product(std::true_type{});
+        else
+          product(std::false_type{});
       }
     }
     __syncwarp();
@@ -526,38 +613,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           float mm = kNegInf;
           for (int w = 0; w < kWarps; ++w)
             mm = fmaxf(mm, sm_m[w * kMaxTileHeads + nt * 8 + 2 * tg + j]);
-          const float f = m[nt][j] == kNegInf ? 0.0f : ex2((m[nt][j] - mm) * sc);
+          float f = m[nt][j] == kNegInf ? 0.0f : ex2(m[nt][j] - mm);
+          if (FP8) f *= vmax * 3.0517578125e-5f;     // back to V's own units
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {
             acc[c][nt][j] *= f;
             acc[c][nt][j + 2] *= f;
           }
         }
-      float* mine = join + (warp & 1) * (C::kRegs * 32) + lane;
-      if (warp >= 2) {
+      float* mine = join + (warp & (C::kJoin - 1)) * (C::kRegs * 32) + lane;
+      for (int r = kWarps / C::kJoin - 1; r >= 0; --r) {
+        if (warp / C::kJoin == r) {
+          const bool put_first = r == kWarps / C::kJoin - 1;
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c)
+          for (int c = 0; c < D / 16; ++c)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) mine[((c * NT + nt) * 4 + j) * 32] = acc[c][nt][j];
+              for (int j = 0; j < 4; ++j) {
+                float* at = mine + ((c * NT + nt) * 4 + j) * 32;
+                *at = put_first ? acc[c][nt][j] : *at + acc[c][nt][j];
+              }
+        }
+        compute_sync();
       }
-      compute_sync();
-      if (warp < 2) {
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) mine[((c * NT + nt) * 4 + j) * 32] += acc[c][nt][j];
-      }
-      compute_sync();
       // element (head n, pair of d) of the joined numerators
       auto joined = [&](int nn, int d) -> float {
         const int dd = d & 15;
         const int gg = FP8 ? dd >> 1 : dd & 7, hi = FP8 ? dd & 1 : dd >> 3;
         const int at = (((d >> 4) * NT + (nn >> 3)) * 4 + hi * 2 + (nn & 1)) * 32 + gg * 4 + ((nn & 7) >> 1);
-        return join[at] + join[C::kRegs * 32 + at];
+        float x = join[at];
+#pragma unroll
+        for (int b = 1; b < C::kJoin; ++b) x += join[b * (C::kRegs * 32) + at];
+        return x;
       };
       auto state = [&](int nn, float& mm, float& ll) {
         mm = kNegInf;
@@ -567,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
           const float mw = sm_m[w * kMaxTileHeads + nn];
-          ll += mw == kNegInf ? 0.0f : ex2((mw - mm) * sc) * sm_l[w * kMaxTileHeads + nn];
+          ll += mw == kNegInf ? 0.0f : ex2(mw - mm) * sm_l[w * kMaxTileHeads + nn];
         }
       };
       __nv_bfloat16* out = a.o + (int64_t)cur.row * a.so_t + (int64_t)h0 * a.so_h;
@@ -576,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         *reinterpret_cast<uint32_t*>(out + (int64_t)nn * a.so_h + d) = pack_bf16(x * inv, y * inv);
         if (d == 0 && a.lse)
           a.lse[(int64_t)cur.row * a.H + h0 + nn] =
-              ll == 0.0f ? kNegInf : (mm * sc + log2f(ll)) * 0.6931471805599453f;
+              ll == 0.0f ? kNegInf : (mm + log2f(ll)) * 0.6931471805599453f;
       };
       const bool begins = k_first == 0, ends = cur.k + 1 == cur.units;
       if (begins && ends) {
@@ -621,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = cf; c <= cl; ++c) {
               const int sl = 2 * c + (c == cf);
               const float mw = __ldcg(a.part_ml + sl * (2 * kMaxTileHeads) + nn);
-              const float f = mw == kNegInf ? 0.0f : ex2((mw - mm) * sc);
+              const float f = mw == kNegInf ? 0.0f : ex2(mw - mm);
               const float2 v = __ldcg(reinterpret_cast<const float2*>(
                   a.part_o + (int64_t)sl * (kMaxTileHeads * 128) + nn * D + d));
               ll += f * __ldcg(a.part_ml + sl * (2 * kMaxTileHeads) + kMaxTileHeads + nn);
@@ -651,6 +739,7 @@ cudaError_t run(const CacheArgs& a, const CUtensorMap& mk, const CUtensorMap& mv
   auto k = cache_attn_kernel<D, FP8, NT, SPARSE>;
   e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
+  constexpr int kUnit = C::kUnit;
   // no more CTAs than units the call can have
   const int64_t HX = (int64_t)a.Hkv * ((a.G + 8 * NT - 1) / (8 * NT));
   const int64_t per = ((int64_t)(SPARSE ? a.n_select : a.max_pages) * a.page_size + kUnit - 1) / kUnit;
