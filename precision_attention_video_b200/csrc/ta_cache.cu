@@ -1,6 +1,8 @@
 // ta_cache.cu -- the paged key-value cache: appending new tokens with the
 // position rotation (and the mean key of every page that fills up), and the
 // choice of the pages that a row reads.
+#include <type_traits>
+
 #include "ta_cache.cuh"
 
 namespace ta {
@@ -9,78 +11,85 @@ namespace {
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
-  x[0] = bf_lo(w.x), x[1] = bf_hi(w.x), x[2] = bf_lo(w.y), x[3] = bf_hi(w.y);
-  x[4] = bf_lo(w.z), x[5] = bf_hi(w.z), x[6] = bf_lo(w.w), x[7] = bf_hi(w.w);
-}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
 }
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                    pack_bf16(x[6], x[7]));
-}
 
-// x * c - y * s (sign < 0) or x * c + y * s.  In fp32 each operation rounds
-// by itself, as an elementwise evaluation does.  In fp64 both products are
-// exact, so the result is rounded once; narrowed to fp32 by truncation with
-// the last bit set when anything was cut off, it still rounds to any format of
-// at most 22 bits as the exact value would: an FP8 code is one rounding away
-// from the rotated key.
-__device__ __forceinline__ float turn32(float x, float c, float y, float s, bool minus) {
-  const float a = __fmul_rn(x, c), b = __fmul_rn(y, s);
-  return minus ? __fsub_rn(a, b) : __fadd_rn(a, b);
-}
-__device__ __forceinline__ float turn64(float x, float c, float y, float s, bool minus) {
-  const double b = (double)y * (double)s;
-  const double r = __fma_rn((double)x, (double)c, minus ? -b : b);
+// One pair of a rotation: x c - y s and y c + x s.  In fp32 each operation
+// rounds by itself, as an elementwise evaluation does.  In fp64 the products
+// of a bf16 and an fp32 value are exact, so the result is rounded once;
+// narrowed to fp32 by truncation with the last bit set when anything was cut
+// off, it still rounds to any format of at most 22 bits as the exact value
+// would: an FP8 code is one rounding away from the rotated key.
+__device__ __forceinline__ float narrow_odd(double r) {
   const float f = __double2float_rz(r);
   return (double)f == r || !(fabsf(f) < __int_as_float(0x7f800000))
              ? f
              : __uint_as_float(__float_as_uint(f) | 1u);
 }
+__device__ __forceinline__ void turn_pair(float& x, float& y, float c, float s) {
+  const float u = __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
+  y = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
+  x = u;
+}
+__device__ __forceinline__ void turn_pair(float& x, float& y, double c, double s) {
+  const double a = x, b = y;
+  x = narrow_odd(__fma_rn(a, c, -(b * s)));
+  y = narrow_odd(__fma_rn(b, c, a * s));
+}
 
-// Elements e0 .. e0+7 of a head, rotated by the angles of one table row.
-// `row` is the head's first element (16-byte aligned).
-template <bool F64>
-__device__ __forceinline__ void rotated8(const __nv_bfloat16* row, int e0, const float* cos,
-                                         const float* sin, int rot, bool inter, float (&y)[8]) {
-  float x[8];
-  unpack8(*reinterpret_cast<const uint4*>(row + e0), x);
-  if (e0 >= rot) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = x[i];
-    return;
-  }
-  auto turn = [](float x, float c, float y, float s, bool minus) {
-    return F64 ? turn64(x, c, y, s, minus) : turn32(x, c, y, s, minus);
-  };
-  if (inter) {
-    const float4 c = *reinterpret_cast<const float4*>(cos + e0 / 2);
-    const float4 s = *reinterpret_cast<const float4*>(sin + e0 / 2);
-    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      y[2 * i] = turn(x[2 * i], cc[i], x[2 * i + 1], ss[i], true);
-      y[2 * i + 1] = turn(x[2 * i + 1], cc[i], x[2 * i], ss[i], false);
+// A lane's part of the heads of one token: two chunks of 8 elements that the
+// rotation pairs with each other (or within themselves), and the angles'
+// cosines and sines, which serve every head of the token.  D / 16 lanes hold a
+// head.
+template <int D>
+struct Turn {
+  int eA, eB;          // first elements of the chunks
+  bool on, inter;
+  float c[8], s[8];
+  __device__ __forceinline__ void place(int rot, bool interleaved, int pr) {
+    inter = interleaved;
+    on = 16 * pr < rot;
+    if (on && !inter) {
+      eA = 8 * pr;
+      eB = eA + rot / 2;
+    } else {
+      eA = 16 * pr;      // (behind the rotated part, chunks pair up in order)
+      eB = eA + 8;
     }
-  } else {
-    const int r2 = rot / 2;
-    const bool first = e0 < r2;
-    const int j0 = first ? e0 : e0 - r2;
-    float z[8];
-    unpack8(*reinterpret_cast<const uint4*>(row + (first ? e0 + r2 : e0 - r2)), z);
+  }
+  __device__ __forceinline__ void angles(const float* cos, const float* sin, int pr) {
+    if (!on) return;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const float4 c = *reinterpret_cast<const float4*>(cos + j0 + 4 * h);
-      const float4 s = *reinterpret_cast<const float4*>(sin + j0 + 4 * h);
-      const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        y[4 * h + i] = turn(x[4 * h + i], cc[i], z[4 * h + i], ss[i], first);
+      const float4 u = *reinterpret_cast<const float4*>(cos + 8 * pr + 4 * h);
+      const float4 v = *reinterpret_cast<const float4*>(sin + 8 * pr + 4 * h);
+      c[4 * h] = u.x, c[4 * h + 1] = u.y, c[4 * h + 2] = u.z, c[4 * h + 3] = u.w;
+      s[4 * h] = v.x, s[4 * h + 1] = v.y, s[4 * h + 2] = v.z, s[4 * h + 3] = v.w;
     }
   }
+  template <typename F>    // float or double arithmetic
+  __device__ __forceinline__ void apply(float (&x)[16]) const {
+    if (!on) return;
+    if (inter) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) turn_pair(x[2 * i], x[2 * i + 1], (F)c[i], (F)s[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) turn_pair(x[i], x[8 + i], (F)c[i], (F)s[i]);
+    }
+  }
+};
+
+__device__ __forceinline__ void unpack16(const uint4& a, const uint4& b, float (&x)[16]) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[2 * i] = bf_lo(w[i]), x[2 * i + 1] = bf_hi(w[i]);
+}
+__device__ __forceinline__ uint4 pack8(const float* x) {
+  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                    pack_bf16(x[6], x[7]));
 }
 
 // Smallest power of two s >= 2^-126 with amax <= 448 s; 1 for 0, NaN when
@@ -97,12 +106,14 @@ __device__ __forceinline__ float token_scale(float amax) {
 // Append
 // ---------------------------------------------------------------------------
 // Bound by memory: a token's keys and values are read once and written once.
-// A block takes the new tokens of one page (of one sequence) and a few key
-// heads; d / 8 lanes hold one head of one token, 16 bytes each.  The tables'
-// rows are shared by the block's heads in L1.  When the block's tokens fill
-// the page, it reads the page's keys back (its own from L2) and sums them in
-// slot order, so the mean is a function of the page alone.
-constexpr int kAppendThreads = 128;
+// A block takes the new tokens of one page (of one sequence) and some key
+// heads; a warp takes one token and 4 (d = 64: 8) heads at a time, a lane 16
+// elements, with the token's cosines and sines in registers.  When the block's
+// tokens fill the page, it reads the page's keys back (its own from L2) and
+// sums them in slot order, so the mean is a function of the page alone.
+constexpr int kAppendThreads = 256;
+constexpr int kAppendWarps = kAppendThreads / 32;
+constexpr int kQueryHeads = 16;        // query heads of a warp
 
 // Page item w -> sequence: the pages that sequence s touches get the items
 // from cu[s] / page_size + 2 s on, and touch at most n / page_size + 2 pages,
@@ -112,41 +123,53 @@ __device__ __forceinline__ int item_start(const CacheArgs& a, int s) {
 }
 
 template <int D, bool FP8>
-__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const CacheArgs a, int items,
+__global__ void __launch_bounds__(kAppendThreads, 4) cache_append_kernel(const CacheArgs a, int items,
                                                                       int chunks, int hc_log2) {
-  constexpr int LPR = D / 8, GROUPS = kAppendThreads / LPR;
-  const int grp = threadIdx.x / LPR, e0 = (threadIdx.x % LPR) * 8;
-  const int HC = 1 << hc_log2;
+  constexpr int LPH = D / 16, HPI = 32 / LPH;      // lanes of a head, heads of a warp
+  constexpr int HPI_LOG2 = D == 128 ? 2 : 3;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hl = lane / LPH, pr = lane % LPH;
   const int r2 = a.rot_dim / 2;
 
   if ((int)blockIdx.x >= items * chunks) {
-    // ---- queries: (row, head) pairs ----
-    const int64_t pairs = (int64_t)rows_used(a) * a.H;
-    const int64_t base = (int64_t)(blockIdx.x - items * chunks) * (GROUPS * 4);
-#pragma unroll 1
-    for (int it = 0; it < 4; ++it) {
-      const int64_t i = base + it * GROUPS + grp;
-      float y[8];
-      bool on = i < pairs;
-      int t = 0, h = 0;
-      if (on) {
-        t = (int)(i / a.H);
-        h = (int)(i - (int64_t)t * a.H);
-        const int s = row_seq(a, t);
-        int p = row_pos(a, t, s);
-        on = p >= 0;
-        if (on && a.pos) p = a.pos[t];
-        if (on && a.rot_dim && (p < 0 || p >= a.rot_rows)) {
-          report_bad_index(a.status);
-          on = false;
-        }
-        if (on)
-          rotated8<false>(a.q + (int64_t)t * a.sq_t + (int64_t)h * a.sq_h, e0, a.cos + (int64_t)p * r2,
-                          a.sin + (int64_t)p * r2, a.rot_dim, a.rot_interleaved, y);
+    // ---- queries: a warp takes one row and 16 heads ----
+    const int hg = (a.H + kQueryHeads - 1) / kQueryHeads;
+    const int w = ((int)blockIdx.x - items * chunks) * kAppendWarps + warp;
+    const int t = w / hg, h0 = (w - t * hg) * kQueryHeads;
+    if (t >= rows_used(a)) return;
+    int p = row_pos(a, t, row_seq(a, t));
+    if (p < 0) return;
+    if (a.pos) p = a.pos[t];
+    if (a.rot_dim && (p < 0 || p >= a.rot_rows)) {
+      report_bad_index(a.status);
+      return;
+    }
+    Turn<D> turn;
+    turn.place(a.rot_dim, a.rot_interleaved, pr);
+    turn.angles(a.cos + (int64_t)p * r2, a.sin + (int64_t)p * r2, pr);
+    const __nv_bfloat16* q = a.q + (int64_t)t * a.sq_t;
+    __nv_bfloat16* o = a.o + (int64_t)t * a.so_t;
+    // each head is read and written by its own lanes: in place is fine
+    constexpr int IT = kQueryHeads / HPI;
+    uint4 x[IT][2];
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const int h = h0 + i * HPI + hl;
+      if (h < a.H) {
+        x[i][0] = __ldcs(reinterpret_cast<const uint4*>(q + (int64_t)h * a.sq_h + turn.eA));
+        x[i][1] = __ldcs(reinterpret_cast<const uint4*>(q + (int64_t)h * a.sq_h + turn.eB));
       }
-      __syncwarp();   // rotation in place: every lane has read its pairs
-      if (on)
-        *reinterpret_cast<uint4*>(a.o + (int64_t)t * a.so_t + (int64_t)h * a.so_h + e0) = pack8(y);
+    }
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const int h = h0 + i * HPI + hl;
+      if (h < a.H) {
+        float y[16];
+        unpack16(x[i][0], x[i][1], y);
+        turn.template apply<float>(y);
+        __stcs(reinterpret_cast<uint4*>(o + (int64_t)h * a.so_h + turn.eA), pack8(y));
+        __stcs(reinterpret_cast<uint4*>(o + (int64_t)h * a.so_h + turn.eB), pack8(y + 8));
+      }
     }
     return;
   }
@@ -178,59 +201,81 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Cach
   const int page = page_of(a, s, pj);
   if (page < 0) return;
   const int used = rows_used(a);
-  const int total = (p1 - p0) << hc_log2;
+  const int upt = hc_log2 - HPI_LOG2;              // log2 of a token's head groups
+  const int units = (p1 - p0) << upt;
+  Turn<D> turn;
+  turn.place(a.rot_dim, a.rot_interleaved, pr);
 
-  for (int base = 0; base < total; base += GROUPS) {
-    const int i = base + grp;
-    const int p = p0 + (i >> hc_log2), h = h0 + (i & (HC - 1));
+  for (int u = warp; u < units; u += kAppendWarps) {
+    const int p = p0 + (u >> upt), h = h0 + ((u & ((1 << upt) - 1)) << HPI_LOG2) + hl;
     const int t = t1 - (len - p);
-    bool on = i < total && h < a.Hkv && t >= 0 && t < used;
-    int ang = p;
-    if (on && a.pos) ang = a.pos[t];
-    if (on && a.rot_dim && (ang < 0 || ang >= a.rot_rows)) {
+    if (t < 0 || t >= used) continue;
+    const int ang = a.pos ? a.pos[t] : p;
+    if (a.rot_dim && (ang < 0 || ang >= a.rot_rows)) {
       report_bad_index(a.status);
-      on = false;
+      continue;
     }
-    float k[8], v[8];
+    const bool on = h < a.Hkv;
+    const __nv_bfloat16* kr = a.k_new + (int64_t)t * a.sk_t + (int64_t)h * a.sk_h;
+    const __nv_bfloat16* vr = a.v_new + (int64_t)t * a.sv_t + (int64_t)h * a.sv_h;
+    uint4 xk[2], xv[2];
     if (on) {
-      rotated8<FP8>(a.k_new + (int64_t)t * a.sk_t + (int64_t)h * a.sk_h, e0, a.cos + (int64_t)ang * r2,
-                    a.sin + (int64_t)ang * r2, a.rot_dim, a.rot_interleaved, k);
-      unpack8(*reinterpret_cast<const uint4*>(a.v_new + (int64_t)t * a.sv_t + (int64_t)h * a.sv_h + e0), v);
+      xk[0] = __ldcs(reinterpret_cast<const uint4*>(kr + turn.eA));
+      xk[1] = __ldcs(reinterpret_cast<const uint4*>(kr + turn.eB));
+      xv[0] = __ldcs(reinterpret_cast<const uint4*>(vr + turn.eA));
+      xv[1] = __ldcs(reinterpret_cast<const uint4*>(vr + turn.eB));
     }
+    turn.angles(a.cos + (int64_t)ang * r2, a.sin + (int64_t)ang * r2, pr);
     const int slot = p & (a.page_size - 1);
-    const int64_t at = (int64_t)page * a.s_page + (int64_t)h * a.s_head + (int64_t)slot * a.s_slot + e0;
+    const int64_t at = (int64_t)page * a.s_page + (int64_t)h * a.s_head + (int64_t)slot * a.s_slot;
+    float k[16];
+    if (on) {
+      unpack16(xk[0], xk[1], k);
+      turn.template apply<typename std::conditional<FP8, double, float>::type>(k);
+    }
     if constexpr (!FP8) {
       if (on) {
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.k) + at) = pack8(k);
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.v) + at) = pack8(v);
+        __nv_bfloat16* kd = static_cast<__nv_bfloat16*>(a.k) + at;
+        __nv_bfloat16* vd = static_cast<__nv_bfloat16*>(a.v) + at;
+        *reinterpret_cast<uint4*>(kd + turn.eA) = pack8(k);
+        *reinterpret_cast<uint4*>(kd + turn.eB) = pack8(k + 8);
+        *reinterpret_cast<uint4*>(vd + turn.eA) = xv[0];
+        *reinterpret_cast<uint4*>(vd + turn.eB) = xv[1];
       }
     } else {
-      // |x| as integers order like the floats, and any NaN lies above inf
+      // |x| as integers order like the floats, and any NaN lies above inf;
+      // V's maximum comes from the packed bf16 words
       uint32_t mk = 0, mv = 0;
       if (on) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          mk = max(mk, __float_as_uint(k[j]) & 0x7fffffffu);
-          mv = max(mv, __float_as_uint(v[j]) & 0x7fffffffu);
-        }
+        for (int j = 0; j < 16; ++j) mk = max(mk, __float_as_uint(k[j]) & 0x7fffffffu);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          mv = __vmaxu2(mv, __vmaxu2(__vmaxu2(xv[j].x & 0x7fff7fffu, xv[j].y & 0x7fff7fffu),
+                                     __vmaxu2(xv[j].z & 0x7fff7fffu, xv[j].w & 0x7fff7fffu)));
+        mv = max(mv << 16, mv & 0xffff0000u);
       }
 #pragma unroll
-      for (int o = 1; o < LPR; o <<= 1) {
+      for (int o = 1; o < LPH; o <<= 1) {
         mk = max(mk, __shfl_xor_sync(0xffffffffu, mk, o));
         mv = max(mv, __shfl_xor_sync(0xffffffffu, mv, o));
       }
       if (on) {
         const float sk = token_scale(__uint_as_float(mk)), sv = token_scale(__uint_as_float(mv));
         const float ik = 1.0f / sk, iv = 1.0f / sv;   // powers of two: exact
-        uint32_t ck[2] = {0, 0}, cv[2] = {0, 0};
+        uint32_t ck[4] = {0, 0, 0, 0}, cv[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          ck[j >> 1] |= cvt_e4m3x2(k[2 * j] * ik, k[2 * j + 1] * ik) << (16 * (j & 1));
-          cv[j >> 1] |= cvt_e4m3x2(v[2 * j] * iv, v[2 * j + 1] * iv) << (16 * (j & 1));
-        }
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.k) + at) = make_uint2(ck[0], ck[1]);
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v) + at) = make_uint2(cv[0], cv[1]);
-        if (e0 == 0) {
+        for (int j = 0; j < 8; ++j) ck[j >> 1] |= cvt_e4m3x2(k[2 * j] * ik, k[2 * j + 1] * ik) << (16 * (j & 1));
+        const uint32_t w[8] = {xv[0].x, xv[0].y, xv[0].z, xv[0].w, xv[1].x, xv[1].y, xv[1].z, xv[1].w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) cv[j >> 1] |= cvt_e4m3x2(bf_lo(w[j]) * iv, bf_hi(w[j]) * iv) << (16 * (j & 1));
+        uint8_t* kd = static_cast<uint8_t*>(a.k) + at;
+        uint8_t* vd = static_cast<uint8_t*>(a.v) + at;
+        *reinterpret_cast<uint2*>(kd + turn.eA) = make_uint2(ck[0], ck[1]);
+        *reinterpret_cast<uint2*>(kd + turn.eB) = make_uint2(ck[2], ck[3]);
+        *reinterpret_cast<uint2*>(vd + turn.eA) = make_uint2(cv[0], cv[1]);
+        *reinterpret_cast<uint2*>(vd + turn.eB) = make_uint2(cv[2], cv[3]);
+        if (pr == 0) {
           const int64_t so = (((int64_t)page * a.Hkv + h) << a.ps_log2) + slot;
           a.k_scale[so] = sk;
           a.v_scale[so] = sv;
@@ -240,36 +285,53 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Cach
   }
 
   if (!a.k_mean || p1 != (pj + 1) << a.ps_log2) return;
-  // ---- the page is full: its mean key ----
+  // ---- the page is full: its mean key, 32 lanes a head ----
   __syncthreads();
+  constexpr int E = D / 32;                        // elements of a lane
   const float inv = 1.0f / (float)a.page_size;
-  for (int h = h0 + grp; h < min(h0 + HC, a.Hkv); h += GROUPS) {
-    const int64_t at = (int64_t)page * a.s_page + (int64_t)h * a.s_head + e0;
+  for (int h = h0 + warp; h < min(h0 + (1 << hc_log2), a.Hkv); h += kAppendWarps) {
+    const int64_t at = (int64_t)page * a.s_page + (int64_t)h * a.s_head + E * lane;
     const float* sc = FP8 ? a.k_scale + (((int64_t)page * a.Hkv + h) << a.ps_log2) : nullptr;
-    float sum[8];
+    float sum[E];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+    for (int j = 0; j < E; ++j) sum[j] = 0.0f;
 #pragma unroll 16
     for (int r = 0; r < a.page_size; ++r) {
-      float x[8];
+      float x[E];
       if constexpr (!FP8) {
-        unpack8(__ldcg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.k) + at + r * a.s_slot)), x);
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.k) + at + r * a.s_slot);
+        uint32_t w[E / 2];
+        if constexpr (E == 4) {
+          const uint2 y = __ldcg(reinterpret_cast<const uint2*>(src));
+          w[0] = y.x, w[1] = y.y;
+        } else {
+          w[0] = __ldcg(src);
+        }
+#pragma unroll
+        for (int j = 0; j < E / 2; ++j) x[2 * j] = bf_lo(w[j]), x[2 * j + 1] = bf_hi(w[j]);
       } else {
-        const uint2 w = __ldcg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.k) + at + r * a.s_slot));
+        const uint8_t* src = static_cast<const uint8_t*>(a.k) + at + r * a.s_slot;
+        uint32_t w;
+        if constexpr (E == 4)
+          w = __ldcg(reinterpret_cast<const uint32_t*>(src));
+        else
+          w = __ldcg(reinterpret_cast<const uint16_t*>(src));
         const float f = __ldcg(sc + r);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 y = e4m3x2_to_float2((j < 2 ? w.x : w.y) >> (16 * (j & 1)));
+        for (int j = 0; j < E / 2; ++j) {
+          const float2 y = e4m3x2_to_float2(w >> (16 * j));
           x[2 * j] = y.x * f;
           x[2 * j + 1] = y.y * f;
         }
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum[j] += x[j];
+      for (int j = 0; j < E; ++j) sum[j] += x[j];
     }
-    float4* out = reinterpret_cast<float4*>(a.k_mean + ((int64_t)page * a.Hkv + h) * D + e0);
-    out[0] = make_float4(sum[0] * inv, sum[1] * inv, sum[2] * inv, sum[3] * inv);
-    out[1] = make_float4(sum[4] * inv, sum[5] * inv, sum[6] * inv, sum[7] * inv);
+    float* out = a.k_mean + ((int64_t)page * a.Hkv + h) * D + E * lane;
+    if constexpr (E == 4)
+      *reinterpret_cast<float4*>(out) = make_float4(sum[0] * inv, sum[1] * inv, sum[2] * inv, sum[3] * inv);
+    else
+      *reinterpret_cast<float2*>(out) = make_float2(sum[0] * inv, sum[1] * inv);
   }
 }
 
@@ -541,14 +603,17 @@ __global__ void __launch_bounds__(kSelThreads) cache_choose_kernel(const CacheAr
 
 cudaError_t launch_cache_append(const CacheArgs& a, cudaStream_t s) {
   const int64_t items = a.cu ? (int64_t)(a.T >> a.ps_log2) + 2 * (int64_t)a.S : a.S;
-  // heads of a block: 8 share the tables' rows; fewer where that leaves the
-  // GPU without blocks
-  int hc_log2 = 3;
-  while (hc_log2 > 0 && ((a.Hkv >> (hc_log2 - 1)) == 0 || items * ((a.Hkv + (1 << hc_log2) - 1) >> hc_log2) < 592))
+  // heads of a block: eight warps' worth where each block has one token;
+  // with more tokens fewer, down to one warp's, until every SM has blocks
+  const int hpi_log2 = a.d == 128 ? 2 : 3;
+  int hc_log2 = hpi_log2 + 3;
+  auto chunks_of = [&](int hc) { return (int64_t)((a.Hkv + (1 << hc) - 1) >> hc); };
+  while (hc_log2 > hpi_log2 &&
+         (chunks_of(hc_log2 - 1) == 1 || (a.cu && items * chunks_of(hc_log2) < 592)))
     --hc_log2;
-  const int64_t chunks = (a.Hkv + (1 << hc_log2) - 1) >> hc_log2;
-  const int groups = kAppendThreads / (a.d / 8);
-  const int64_t qblocks = a.q ? ((int64_t)a.T * a.H + groups * 4 - 1) / (groups * 4) : 0;
+  const int64_t chunks = chunks_of(hc_log2);
+  const int64_t hg = (a.H + kQueryHeads - 1) / kQueryHeads;
+  const int64_t qblocks = a.q ? ((int64_t)a.T * hg + kAppendWarps - 1) / kAppendWarps : 0;
   const int64_t grid = items * chunks + qblocks;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
   auto go = [&](auto kernel) {
