@@ -151,7 +151,9 @@ ta_status tiered_attn_cache_decode(const ta_cache_params* p, const ta_cache* cac
  * mass router of tiered_attn_plan with a query block of one row.  A product
  * that is not finite adds no mass.
  * sel_dev: int32 [T, Hkv, n_select], a row's page indices (in its sequence)
- * in ascending order, then -1.  Only k_mean of the cache is read. */
+ * in ascending order, then -1.  Only k_mean of the cache is read.  At most
+ * 16384 pages of a sequence and 128 query heads of a key head (else
+ * TA_ERR_UNSUPPORTED). */
 ta_status tiered_attn_cache_select(const ta_cache_params* p, const ta_cache* cache,
                                    const void* Q_dev, const int32_t* cu_dev,
                                    const int32_t* seq_lens_dev, const int32_t* table_dev,

@@ -168,61 +168,76 @@ def init_cache_workspace(ws: torch.Tensor, stream=None) -> None:
 
 def _plain(name, t, dtype, shape, dev) -> int:
     """Pointer of a contiguous tensor of this type and shape on device `dev`."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse_type(name, t, dtype, dev)
+    raise ValueError(f"{name}: expected a contiguous tensor of shape {tuple(shape)}, got "
+                     f"{tuple(t.shape)} with strides {t.stride()}")
+
+
+def _rows(name, t, shape, dev):
+    """(pointer, row stride, head stride) of a bf16 [rows, heads, d] tensor, d
+    contiguous."""
+    try:
+        if t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == dev:
+            st, sh, sd = t.stride()
+            if sd == 1:
+                return t.data_ptr(), st, sh
+    except AttributeError:
+        pass
+    _refuse_type(name, t, torch.bfloat16, dev)
+    raise ValueError(f"{name}: expected shape {tuple(shape)} with the last dimension "
+                     f"contiguous, got {tuple(t.shape)} with strides {t.stride()}")
+
+
+def _refuse_type(name, t, dtype, dev) -> None:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if t.get_device() != dev:
         raise ValueError(f"{name}: expected a tensor on device {dev}, got one on {t.device}")
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor of shape {tuple(shape)}, got "
-                         f"{tuple(t.shape)} with strides {t.stride()}")
-    return t.data_ptr()
-
-
-def _rows(name, t, shape, dev) -> int:
-    """Pointer of a bf16 [rows, heads, d] tensor, d contiguous."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name}: expected a tensor on device {dev}, got one on {t.device}")
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
-    if t.shape != shape or t.stride(2) != 1:
-        raise ValueError(f"{name}: expected shape {tuple(shape)} with the last dimension "
-                         f"contiguous, got {tuple(t.shape)} with strides {t.stride()}")
-    return t.data_ptr()
 
 
 def _begin(p, cache, table, lens, ws, cu, kv: bool):
     """Checks shared by every call; (a copy of p with the cache's strides,
-    device, pointers of table, lens, cu, ws)."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
-    if cache._dev < 0:
+    device, pointers of table, lens and cu, pointer and size of ws)."""
+    dev = cache._dev
+    if dev < 0:
         raise ValueError("cache: expected CUDA tensors")
-    if cache._dev != dev:
-        raise ValueError(f"cache: on cuda:{cache._dev}, but the library launches on the current "
-                         f"device cuda:{dev}")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"cache: on cuda:{dev}, but the library launches on the current device "
+                         f"cuda:{torch._C._cuda_getDevice()}")
+    S, W = p.S, p.max_pages
+    q = ta_cache_params.from_buffer_copy(p)
     if kv:
         if cache._shape is None:
             raise ValueError("cache: has no keys and values")
         if cache._shape != (p.n_pages, p.Hkv, p.page_size, p.d) or cache._fmt != p.format:
             raise ValueError(f"cache: shape {cache._shape}, format {cache._fmt}, but the "
                              f"parameters say {(p.n_pages, p.Hkv, p.page_size, p.d)}, {p.format}")
-    q = ta_cache_params.from_buffer_copy(p)
-    q.stride_page, q.stride_head, q.stride_slot = cache._strides
-    if not isinstance(table, torch.Tensor):
-        raise TypeError(f"table: expected a torch.Tensor, got {type(table).__name__}")
-    if table.get_device() != dev or table.dtype is not torch.int32:
-        raise TypeError(f"table: expected torch.int32 on cuda:{dev}, got {table.dtype} on {table.device}")
-    if table.dim() != 2 or table.shape[0] != p.S or table.shape[1] < p.max_pages or \
-            table.stride(1) != 1:
-        raise ValueError(f"table: expected [{p.S}, >= {p.max_pages}] with contiguous rows, got "
+        q.stride_page, q.stride_head, q.stride_slot = cache._strides
+    try:
+        rows, cols = table.shape
+        q.stride_table, one = table.stride()
+        ok = (table.dtype is torch.int32 and table.get_device() == dev and rows == S and
+              cols >= W and one == 1)
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok:
+        _refuse_type("table", table, torch.int32, dev)
+        raise ValueError(f"table: expected [{S}, >= {W}] with contiguous rows, got "
                          f"{tuple(table.shape)} with strides {table.stride()}")
-    q.stride_table = table.stride(0)
-    ln = _plain("lens", lens, torch.int32, (p.S,), dev)
-    c = None if cu is None else _plain("cu", cu, torch.int32, (p.S + 1,), dev)
-    return q, dev, table.data_ptr(), ln, c, _plain("ws", ws, torch.uint8, (ws.numel(),), dev)
+    ln = _plain("lens", lens, torch.int32, (S,), dev)
+    c = None if cu is None else _plain("cu", cu, torch.int32, (S + 1,), dev)
+    try:
+        n = ws.numel()
+    except AttributeError:
+        n = 0
+    return q, dev, table.data_ptr(), ln, c, _plain("ws", ws, torch.uint8, (n,), dev), n
 
 
 def _stream_of(stream, dev) -> int:
@@ -237,69 +252,67 @@ def cache_append(p: ta_cache_params, cache: PagedCache, K, V, table, lens, ws, c
     by the table rows ``pos`` (their positions, where None) of ``cos`` and
     ``sin`` (f32 [rows, rot_dim / 2]); rotate Q [T, H, d] into ``Q_out`` (may
     be Q itself) with the same angles.  ``lens`` counts the new tokens."""
-    q, dev, tb, ln, c, w = _begin(p, cache, table, lens, ws, cu, True)
-    k = _rows("K", K, (p.T, p.Hkv, p.d), dev)
-    v = _rows("V", V, (p.T, p.Hkv, p.d), dev)
-    q.stride_k_t, q.stride_k_h, _ = K.stride()
-    q.stride_v_t, q.stride_v_h, _ = V.stride()
+    q, dev, tb, ln, c, w, n = _begin(p, cache, table, lens, ws, cu, True)
+    T, d, rot = p.T, p.d, p.rot_dim
+    shape = (T, p.Hkv, d)
+    k, q.stride_k_t, q.stride_k_h = _rows("K", K, shape, dev)
+    v, q.stride_v_t, q.stride_v_h = _rows("V", V, shape, dev)
     qi = qo = cp = sp = pp = None
     if Q is not None:
-        qi = _rows("Q", Q, (p.T, p.H, p.d), dev)
-        qo = _rows("Q_out", Q_out, (p.T, p.H, p.d), dev)
-        if qi == qo and Q.stride() != Q_out.stride():
+        shape = (T, p.H, d)
+        qi, qt, qh = _rows("Q", Q, shape, dev)
+        qo, ot, oh = _rows("Q_out", Q_out, shape, dev)
+        if qi == qo and (qt, qh) != (ot, oh):
             raise ValueError("Q_out: shares Q's memory with other strides")
-        q.stride_q_t, q.stride_q_h, _ = Q.stride()
-        q.stride_o_t, q.stride_o_h, _ = Q_out.stride()
-    if p.rot_dim:
+        q.stride_q_t, q.stride_q_h, q.stride_o_t, q.stride_o_h = qt, qh, ot, oh
+    if rot:
         if not isinstance(cos, torch.Tensor):
             raise TypeError(f"cos: expected a torch.Tensor, got {type(cos).__name__}")
-        q.rot_rows = cos.shape[0]
-        cp = _plain("cos", cos, torch.float32, (q.rot_rows, p.rot_dim // 2), dev)
-        sp = _plain("sin", sin, torch.float32, (q.rot_rows, p.rot_dim // 2), dev)
+        shape = (len(cos), rot // 2)
+        cp = _plain("cos", cos, torch.float32, shape, dev)
+        sp = _plain("sin", sin, torch.float32, shape, dev)
+        q.rot_rows = shape[0]
     if pos is not None:
-        pp = _plain("pos", pos, torch.int32, (p.T,), dev)
+        pp = _plain("pos", pos, torch.int32, (T,), dev)
     _check("tiered_attn_cache_append", _fn("tiered_attn_cache_append")(
-        q, cache._c, k, v, qi, qo, cp, sp, pp, c, ln, tb, w, ws.numel(), _stream_of(stream, dev)))
+        q, cache._c, k, v, qi, qo, cp, sp, pp, c, ln, tb, w, n, _stream_of(stream, dev)))
 
 
 def cache_decode(p: ta_cache_params, cache: PagedCache, Q, table, lens, ws, O,
                  lse: Optional[torch.Tensor] = None, stream=None) -> None:
     """Attention of one new token for each sequence, Q bf16 [S, H, d], over
     its whole cache into O (and ``lse`` f32 [S, H])."""
-    q, dev, tb, ln, _, w = _begin(p, cache, table, lens, ws, None, True)
-    qp = _rows("Q", Q, (p.T, p.H, p.d), dev)
-    op = _rows("O", O, (p.T, p.H, p.d), dev)
-    lp = None if lse is None else _plain("lse", lse, torch.float32, (p.T, p.H), dev)
-    q.stride_q_t, q.stride_q_h, _ = Q.stride()
-    q.stride_o_t, q.stride_o_h, _ = O.stride()
+    q, dev, tb, ln, _, w, n = _begin(p, cache, table, lens, ws, None, True)
+    shape = (p.T, p.H, p.d)
+    qp, q.stride_q_t, q.stride_q_h = _rows("Q", Q, shape, dev)
+    op, q.stride_o_t, q.stride_o_h = _rows("O", O, shape, dev)
+    lp = None if lse is None else _plain("lse", lse, torch.float32, shape[:2], dev)
     _check("tiered_attn_cache_decode", _fn("tiered_attn_cache_decode")(
-        q, cache._c, qp, ln, tb, op, lp, w, ws.numel(), _stream_of(stream, dev)))
+        q, cache._c, qp, ln, tb, op, lp, w, n, _stream_of(stream, dev)))
 
 
 def cache_select(p: ta_cache_params, cache: PagedCache, Q, table, lens, ws, sel, cu=None,
                  stream=None) -> None:
     """The pages that each row reads: ``sel`` int32 [T, Hkv, n_select], page
     indices of the row's sequence in ascending order, then -1."""
-    q, dev, tb, ln, c, w = _begin(p, cache, table, lens, ws, cu, False)
+    q, dev, tb, ln, c, w, n = _begin(p, cache, table, lens, ws, cu, False)
     if cache.k_mean is None or cache.k_mean.shape != (p.n_pages, p.Hkv, p.d):
         raise ValueError(f"cache: expected k_mean of shape {(p.n_pages, p.Hkv, p.d)}")
-    qp = _rows("Q", Q, (p.T, p.H, p.d), dev)
+    qp, q.stride_q_t, q.stride_q_h = _rows("Q", Q, (p.T, p.H, p.d), dev)
     sl = _plain("sel", sel, torch.int32, (p.T, p.Hkv, p.n_select), dev)
-    q.stride_q_t, q.stride_q_h, _ = Q.stride()
     _check("tiered_attn_cache_select", _fn("tiered_attn_cache_select")(
-        q, cache._c, qp, c, ln, tb, sl, w, ws.numel(), _stream_of(stream, dev)))
+        q, cache._c, qp, c, ln, tb, sl, w, n, _stream_of(stream, dev)))
 
 
 def cache_sparse(p: ta_cache_params, cache: PagedCache, Q, sel, table, lens, ws, O, cu=None,
                  lse: Optional[torch.Tensor] = None, stream=None) -> None:
     """Attention of each row, Q bf16 [T, H, d], over the pages of its list
     ``sel`` into O (and ``lse`` f32 [T, H])."""
-    q, dev, tb, ln, c, w = _begin(p, cache, table, lens, ws, cu, True)
-    qp = _rows("Q", Q, (p.T, p.H, p.d), dev)
-    op = _rows("O", O, (p.T, p.H, p.d), dev)
+    q, dev, tb, ln, c, w, n = _begin(p, cache, table, lens, ws, cu, True)
+    shape = (p.T, p.H, p.d)
+    qp, q.stride_q_t, q.stride_q_h = _rows("Q", Q, shape, dev)
+    op, q.stride_o_t, q.stride_o_h = _rows("O", O, shape, dev)
     sl = _plain("sel", sel, torch.int32, (p.T, p.Hkv, p.n_select), dev)
-    lp = None if lse is None else _plain("lse", lse, torch.float32, (p.T, p.H), dev)
-    q.stride_q_t, q.stride_q_h, _ = Q.stride()
-    q.stride_o_t, q.stride_o_h, _ = O.stride()
+    lp = None if lse is None else _plain("lse", lse, torch.float32, shape[:2], dev)
     _check("tiered_attn_cache_sparse", _fn("tiered_attn_cache_sparse")(
-        q, cache._c, qp, sl, c, ln, tb, op, lp, w, ws.numel(), _stream_of(stream, dev)))
+        q, cache._c, qp, sl, c, ln, tb, op, lp, w, n, _stream_of(stream, dev)))

@@ -340,21 +340,29 @@ __global__ void __launch_bounds__(kAppendThreads, 4) cache_append_kernel(const C
 // ---------------------------------------------------------------------------
 // Per row, key head and query head g of it: logits l_gj = scale * q_g . kbar_j
 // over the pages j that compete, masses M_gj = exp(l_gj - max) / sum, and the
-// n_select - n_first - n_recent pages of greatest sum_g M_gj, in fp64 so that
-// the choice depends on the inputs and not on an order of summation.
+// n_select - n_first - n_recent pages of greatest sum_g M_gj, as fp64 decides.
 //
-// The logits are fp64 matrix products (mma.sync m8n8k4): a warp holds the
-// means of 8 pages as A fragments and runs over the (row, query head) columns
-// of its tile.
+// Single rows are bound by reading the means: their logits are fp64 products
+// (mma.sync m8n8k4), and a block chooses for each (row, key head).
+//
+// Where many rows of a sequence share its means, fp64 would bound, and it
+// decides only where it has to.  There the logits come from f16 tensor-core
+// products with an fp32 sum and a bound of their error; where the last page
+// that is in and the first that is out lie further apart than the bound, the
+// set is the one that fp64 would find, whatever the rounding.  The other rows
+// (about one in a hundred on random means, and ties) are done again in fp64
+// by the block that found them.
+//
+// The error: a page's mean is scaled by a power of two to f16's range and
+// split into two f16 parts (22 bits of each element), the query scaled the same
+// way (its 8 bits are exact down to 2^-14 of its largest element); what is cut
+// off is at most 2^-21 of |q| |kbar|.  Each 16 products go into a sum of their
+// own, where an addend may lose 2^-24 of the largest: 2^-20 in all; their eight
+// sums add up in fp32, 2^-21.  2^-18.9 scale |q| |kbar| covers these.
 constexpr int kSelThreads = 256;
-constexpr int kSelPages = 128;         // pages of a logits block
 constexpr int kSelCols = 64;           // (row, head) columns of a logits block
-
-__device__ __forceinline__ void dmma(double (&c)[2], double a, double b) {
-  asm volatile("mma.sync.aligned.m8n8k4.row.col.f64.f64.f64.f64 {%0, %1}, {%2}, {%3}, {%0, %1};"
-               : "+d"(c[0]), "+d"(c[1])
-               : "d"(a), "d"(b));
-}
+constexpr float kLogitErr = 2.05e-6f;  // 2^-18.9
+constexpr float kInf = 3.0e38f;        // a logit above is taken as not finite
 
 // Pages that row t sees, and the pages [c0, c1) that compete for it.
 struct RowPages {
@@ -369,34 +377,101 @@ __device__ __forceinline__ RowPages row_pages(const CacheArgs& a, int t, int s) 
   return r;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kSelThreads) cache_logits_kernel(const CacheArgs a, int tile_rows) {
-  extern __shared__ double qs[];
-  constexpr int QP = D + 4;            // padded: a column's chunks fall on banks of their own
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tg = lane & 3;
-  const int hk = blockIdx.y;
-  int s, t0, t1;
+// Scratch: for each (row, query head) `pitch` doubles, of which the fp32
+// logits (in log2 units) take the first half until the row is done in fp64;
+// then, for each (sequence, key head), the pages' norms.
+__device__ __forceinline__ double* logit_row(const CacheArgs& a, int t, int h) {
+  return a.scratch + ((int64_t)t * a.H + h) * select_pitch(a.max_pages);
+}
+__device__ __forceinline__ float* norm_row(const CacheArgs& a, int s, int hk) {
+  return reinterpret_cast<float*>(a.scratch + (int64_t)a.T * a.H * select_pitch(a.max_pages)) +
+         ((int64_t)s * a.Hkv + hk) * select_pitch(a.max_pages);
+}
+
+__device__ __forceinline__ void dmma(double (&c)[2], double a, double b) {
+  asm volatile("mma.sync.aligned.m8n8k4.row.col.f64.f64.f64.f64 {%0, %1}, {%2}, {%3}, {%0, %1};"
+               : "+d"(c[0]), "+d"(c[1])
+               : "d"(a), "d"(b));
+}
+__device__ __forceinline__ void hmma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two floats as f16 parts: x = hi + lo + (at most 2^-22 |x|, or 2^-25).
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x, y);
+  const float2 f = __half22float2(h);
+  const __half2 l = __floats2half2_rn(x - f.x, y - f.y);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+// Power of two that brings a largest magnitude x to [1, 2); 1 where x is zero,
+// or not finite, or tiny: such a column's logits are made NaN, which sends
+// the row to fp64.
+__device__ __forceinline__ float unit_scale(float x) {
+  return x >= 1e-35f && x < kInf ? 1.0f / __uint_as_float(__float_as_uint(x) & 0x7F800000u) : 1.0f;
+}
+
+__device__ __forceinline__ double kInf64() { return __longlong_as_double(0x7ff0000000000000ll); }
+__device__ __forceinline__ bool tiny(float x) { return x > 0.0f && x < 1e-35f; }
+
+// Rows of a logits block: up to tile_rows of one sequence.
+struct RowTile {
+  int s, t0, t1, t_end;
+};
+__device__ __forceinline__ RowTile row_tile(const CacheArgs& a, int tile, int tile_rows) {
+  RowTile r;
   if (a.cu) {
     // tiles of sequence s start at cu[s] / tile_rows + s
     int lo = 0, hi = a.S - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (max(a.cu[mid], 0) / tile_rows + mid <= (int)blockIdx.x) lo = mid; else hi = mid - 1;
+      if (max(a.cu[mid], 0) / tile_rows + mid <= tile) lo = mid; else hi = mid - 1;
     }
-    s = lo;
-    const int c0 = max(a.cu[s], 0);
-    t0 = c0 + ((int)blockIdx.x - (c0 / tile_rows + s)) * tile_rows;
-    t1 = min(min(a.cu[s + 1], rows_used(a)), t0 + tile_rows);
+    r.s = lo;
+    const int c0 = max(a.cu[lo], 0);
+    r.t0 = c0 + (tile - (c0 / tile_rows + lo)) * tile_rows;
+    r.t_end = min(a.cu[lo + 1], rows_used(a));
+    r.t1 = min(r.t_end, r.t0 + tile_rows);
   } else {
-    s = t0 = blockIdx.x;
-    t1 = t0 + 1;
+    r.s = r.t0 = tile;
+    r.t1 = r.t_end = tile + 1;
   }
+  return r;
+}
+
+// fp64 logits of a tile of few rows: a warp takes 8 pages (A fragments) at a
+// time, the next 8 on their way, and all columns of the tile.
+template <int D>
+__global__ void __launch_bounds__(kSelThreads, 2) cache_logits64_kernel(const CacheArgs a, int tile_rows,
+                                                                        int pages) {
+  extern __shared__ __align__(16) unsigned char sel_smem[];
+  double* qs = reinterpret_cast<double*>(sel_smem);
+  constexpr int QP = D + 4;            // padded: a column's chunks fall on banks of their own
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tg = lane & 3;
+  const int hk = blockIdx.y;
+  const RowTile tile = row_tile(a, blockIdx.x, tile_rows);
+  const int s = tile.s, t0 = tile.t0, t1 = tile.t1;
   if (t0 >= t1) return;
   const RowPages last = row_pages(a, t1 - 1, s);   // the tile's longest row
-  const int j_end = min(last.c1, (int)(blockIdx.z + 1) * kSelPages);
-  const int j0 = blockIdx.z * kSelPages;
-  if (j0 >= j_end) return;
+  const int j0 = max(blockIdx.z * pages, min(a.n_first, last.n));
+  const int j_end = min(last.c1, (int)(blockIdx.z + 1) * pages);
+  if (j0 >= j_end || last.n <= a.n_select) return;
   const int cols = (t1 - t0) * a.G, tiles = (cols + 7) / 8;
+
+  float4 v[D / 16];
+  int page = -1;
+  auto fetch = [&](int j) {            // the lane's 32 elements of page j + g
+    page = j + g < j_end ? page_of(a, s, j + g) : -1;
+    const float4* src = reinterpret_cast<const float4*>(a.k_mean + ((int64_t)max(page, 0) * a.Hkv + hk) * D);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) v[i] = page >= 0 ? __ldg(src + 4 * i + tg) : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  const int j_first = j0 + warp * 8;
+  if (j_first < j_end) fetch(j_first);
   for (int i = threadIdx.x; i < tiles * 8 * (D / 2); i += kSelThreads) {
     const int c = i / (D / 2), d = 2 * (i - c * (D / 2));
     double2 x = make_double2(0.0, 0.0);
@@ -408,18 +483,12 @@ __global__ void __launch_bounds__(kSelThreads) cache_logits_kernel(const CacheAr
     *reinterpret_cast<double2*>(qs + c * QP + d) = x;
   }
   __syncthreads();
-  for (int j = j0 + warp * 8; j < j_end; j += (kSelThreads / 32) * 8) {
-    const int page_j = j + g;
-    int page = -1;
-    if (page_j < j_end) page = page_of(a, s, page_j);
+  for (int j = j_first; j < j_end; j += kSelThreads / 32 * 8) {
     double am[D / 16][4];
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (page >= 0)
-        v = __ldg(reinterpret_cast<const float4*>(a.k_mean + ((int64_t)page * a.Hkv + hk) * D + 16 * i + 4 * tg));
-      am[i][0] = v.x, am[i][1] = v.y, am[i][2] = v.z, am[i][3] = v.w;
-    }
+    for (int i = 0; i < D / 16; ++i) am[i][0] = v[i].x, am[i][1] = v[i].y, am[i][2] = v[i].z, am[i][3] = v[i].w;
+    const bool live = page >= 0;
+    if (j + kSelThreads / 32 * 8 < j_end) fetch(j + kSelThreads / 32 * 8);
     for (int ct = 0; ct < tiles; ++ct) {
       double c0[2] = {0.0, 0.0}, c1[2] = {0.0, 0.0};
       const double* q = qs + (ct * 8 + g) * QP + 4 * tg;
@@ -432,169 +501,579 @@ __global__ void __launch_bounds__(kSelThreads) cache_logits_kernel(const CacheAr
         dmma(c0, am[i][2], y.x);
         dmma(c1, am[i][3], y.y);
       }
-      if (page_j < j_end) {
+      if (j + g < j_end) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int c = ct * 8 + 2 * tg + e;
           if (c >= cols) continue;
           const int r = c / a.G, h = hk * a.G + (c - r * a.G);
-          a.scratch[((int64_t)(t0 + r) * a.H + h) * a.max_pages + page_j] =
-              page < 0 ? -__longlong_as_double(0x7ff0000000000000ll) : (c0[e] + c1[e]) * a.scale;
+          logit_row(a, t0 + r, h)[j + g] = live ? (c0[e] + c1[e]) * a.scale : -kInf64();
         }
       }
     }
   }
 }
 
-__device__ __forceinline__ double block_max(double x, double* red) {
+// fp32 logits (in log2 units) of a tile of many rows: a warp takes 16 pages
+// at a time and all columns of the tile.
+template <int D>
+__global__ void __launch_bounds__(kSelThreads, 2) cache_logits_kernel(const CacheArgs a, int tile_rows,
+                                                                      int pages) {
+  extern __shared__ __align__(16) unsigned char sel_smem[];
+  constexpr int QB = D * 2 + 16;       // bytes of a column, padded against bank conflicts
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tg = lane & 3;
+  const int hk = blockIdx.y;
+  const RowTile tile = row_tile(a, blockIdx.x, tile_rows);
+  const int s = tile.s, t0 = tile.t0, t1 = tile.t1;
+  if (t0 >= t1) return;
+  const RowPages last = row_pages(a, t1 - 1, s);   // the tile's longest row
+  const int j0 = blockIdx.z * pages;
+  const int j_end = min(last.c1, j0 + pages);
+  if (j0 >= j_end || j_end <= a.n_first || last.n <= a.n_select) return;
+  const int cols = (t1 - t0) * a.G, tiles = (cols + 7) / 8;
+  unsigned char* qs = sel_smem;                    // f16 queries, [column][D]
+  float* qsc = reinterpret_cast<float*>(sel_smem + ((tile_rows * a.G + 7) / 8 * 8) * QB);
+
+  // A fragments: a lane's four k indices of a step are four consecutive
+  // elements of its rows g and g + 8
+  float4 v[2][D / 16];
+  auto fetch = [&](int j) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) x = fmax(x, __shfl_xor_sync(0xffffffffu, x, o));
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-  __syncthreads();
-  x = red[0];
+    for (int e = 0; e < 2; ++e) {
+      const int jj = j + g + 8 * e;
+      int page = -1;
+      if (jj < j_end && jj >= a.n_first) page = page_of(a, s, jj);
+      const float4* src = reinterpret_cast<const float4*>(a.k_mean + ((int64_t)max(page, 0) * a.Hkv + hk) * D);
 #pragma unroll
-  for (int w = 1; w < kSelThreads / 32; ++w) x = fmax(x, red[w]);
-  return x;
-}
-__device__ __forceinline__ double block_sum(double x, double* red) {
+      for (int c = 0; c < D / 16; ++c)
+        v[e][c] = page >= 0 ? __ldg(src + 4 * c + tg) : make_float4(__int_as_float(0x7fffffff), 0.f, 0.f, 0.f);
+    }
+  };
+
+  // queries: a warp takes a column at a time
+  for (int c = warp; c < tiles * 8; c += kSelThreads / 32) {
+    constexpr int E = D / 32;                      // elements of a lane
+    float x[E];
+    float am = 0.0f;
+    if (c < cols) {
+      const int r = c / a.G, h = hk * a.G + (c - r * a.G);
+      const __nv_bfloat16* q = a.q + (int64_t)(t0 + r) * a.sq_t + (int64_t)h * a.sq_h + E * lane;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-  __syncthreads();
-  x = red[0];
+      for (int i = 0; i < E; i += 2) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(q + i);
+        x[i] = bf_lo(w), x[i + 1] = bf_hi(w);
+        am = fmaxf(am, fmaxf(fabsf(x[i]), fabsf(x[i + 1])));
+      }
+    } else {
 #pragma unroll
-  for (int w = 1; w < kSelThreads / 32; ++w) x += red[w];
-  return x;
+      for (int i = 0; i < E; ++i) x[i] = 0.0f;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+    const float up = unit_scale(am);
+#pragma unroll
+    for (int i = 0; i < E; i += 2)
+      *reinterpret_cast<__half2*>(qs + c * QB + (E * lane + i) * 2) = __floats2half2_rn(x[i] * up, x[i + 1] * up);
+    if (lane == 0)
+      qsc[c] = tiny(am) ? __int_as_float(0x7fffffff) : (float)(a.scale * 1.4426950408889634) / up;
+  }
+  __syncthreads();
+
+  const int64_t pitch2 = select_pitch(a.max_pages) * 2;
+  for (int j = j0 + warp * 16; j < j_end; j += kSelThreads / 32 * 16) {
+    fetch(j);
+    uint32_t hi[D / 16][4], lo[D / 16][4];
+    float down[2];
+    float am[2] = {0.0f, 0.0f}, n2[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        const float4 x = v[e][c];
+        am[e] = fmaxf(fmax3(am[e], fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
+      }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) am[e] = fmaxf(am[e], __shfl_xor_sync(0xffffffffu, am[e], o));
+      const float up = unit_scale(am[e]);
+      down[e] = tiny(am[e]) ? __int_as_float(0x7fffffff) : 1.0f / up;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        const float4 x = v[e][c];
+        const float y0 = x.x * up, y1 = x.y * up, y2 = x.z * up, y3 = x.w * up;
+        n2[e] += y0 * y0 + y1 * y1 + y2 * y2 + y3 * y3;
+        split2(y0, y1, hi[c][e], lo[c][e]);
+        split2(y2, y3, hi[c][e + 2], lo[c][e + 2]);
+      }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) n2[e] += __shfl_xor_sync(0xffffffffu, n2[e], o);
+    }
+    if (t1 == tile.t_end && tg == 0) {   // the sequence's last tile sees all of its pages
+      float* nr = norm_row(a, s, hk);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (j + g + 8 * e < j_end) nr[j + g + 8 * e] = sqrtf(n2[e]) * down[e];
+    }
+    float* out = reinterpret_cast<float*>(logit_row(a, t0, hk * a.G)) + j + g;
+    for (int ct = 0; ct < tiles; ++ct) {
+      float sum[4] = {0.f, 0.f, 0.f, 0.f}, cl[4] = {0.f, 0.f, 0.f, 0.f};
+      const unsigned char* q = qs + (ct * 8 + g) * QB + 8 * tg;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        const uint2 b = *reinterpret_cast<const uint2*>(q + 32 * c);
+        float ch[4] = {0.f, 0.f, 0.f, 0.f};
+        hmma(ch, hi[c], b.x, b.y);
+        hmma(cl, lo[c], b.x, b.y);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) sum[u] += ch[u];
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int c = ct * 8 + 2 * tg + u;
+        if (c >= cols) continue;
+        const int r = c / a.G;
+        const float f = qsc[c];
+        float* o = out + ((int64_t)r * a.H + (c - r * a.G)) * pitch2;
+        if (j + g < j_end) o[0] = (sum[u] + cl[u]) * (down[0] * f);
+        if (j + g + 8 < j_end) o[8] = (sum[u + 2] + cl[u + 2]) * (down[1] * f);
+      }
+    }
+  }
 }
 
-__global__ void __launch_bounds__(kSelThreads) cache_choose_kernel(const CacheArgs a) {
-  extern __shared__ double mass[];     // one for each competing page
-  __shared__ double red[kSelThreads / 32];
-  __shared__ int hist[256];
-  __shared__ int found[2];
-  __shared__ int wsum[2][kSelThreads / 32];
-  const int t = blockIdx.x, hk = blockIdx.y, tid = threadIdx.x;
-  if (t >= rows_used(a)) return;
-  const int s = row_seq(a, t);
-  const RowPages r = row_pages(a, t, s);
+// Reductions over the threads of an item: one warp, or the block.
+template <int WPI>
+struct Group {
+  float* red;                          // shared memory, 8 floats (WPI > 1)
+  __device__ __forceinline__ float max(float x) const {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    if constexpr (WPI > 1) {
+      __syncthreads();
+      if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < WPI; ++w) x = fmaxf(x, red[w]);
+    }
+    return x;
+  }
+  __device__ __forceinline__ float sum(float x) const {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if constexpr (WPI > 1) {
+      __syncthreads();
+      if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+      __syncthreads();
+      x = red[0];
+#pragma unroll
+      for (int w = 1; w < WPI; ++w) x += red[w];
+    }
+    return x;
+  }
+  __device__ __forceinline__ int count(int x) const {
+    x = __reduce_add_sync(0xffffffffu, x);
+    if constexpr (WPI > 1) {
+      __syncthreads();
+      if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = __int_as_float(x);
+      __syncthreads();
+      x = 0;
+#pragma unroll
+      for (int w = 0; w < WPI; ++w) x += __float_as_int(red[w]);
+    }
+    return x;
+  }
+};
+
+// Shared memory of a block's fp64 choice; reductions take turns on its halves,
+// so one barrier each is enough.
+struct ExactSmem {
+  double red[2][kSelThreads / 32];
+  int cnt[2][kSelThreads / 32];
+  uint32_t keep[kMaxSelectPages / 32];
+};
+struct Block64 {
+  ExactSmem& sm;
+  int turn = 0;
+  template <typename Op>
+  __device__ __forceinline__ double reduce(double x, Op op) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x = op(x, __shfl_xor_sync(0xffffffffu, x, o));
+    double* r = sm.red[turn ^= 1];
+    if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = r[0];
+#pragma unroll
+    for (int w = 1; w < kSelThreads / 32; ++w) x = op(x, r[w]);
+    return x;
+  }
+  __device__ __forceinline__ int count(int x) {
+    x = __reduce_add_sync(0xffffffffu, x);
+    int* r = sm.cnt[turn ^= 1];
+    if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = 0;
+#pragma unroll
+    for (int w = 0; w < kSelThreads / 32; ++w) x += r[w];
+    return x;
+  }
+};
+
+// The choice of one item from its fp64 logits, by the whole block; E pages a
+// thread (page r.c0 + tid + 256 i).
+template <int E>
+__device__ __forceinline__ void choose64(const CacheArgs& a, int t, int hk, ExactSmem& sm) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const RowPages r = row_pages(a, t, row_seq(a, t));
   int* sel = a.sel + ((int64_t)t * a.Hkv + hk) * a.n_select;
   const int nc = r.c1 - r.c0;
-  if (r.n <= a.n_select) {
-    for (int i = tid; i < a.n_select; i += kSelThreads) sel[i] = i < r.n ? i : -1;
-    return;
-  }
-  int want = a.n_select - a.n_first - a.n_recent;   // < nc here
+  const int want = a.n_select - a.n_first - a.n_recent;
+  Block64 blk{sm};
+  auto larger = [](double x, double y) { return fmax(x, y); };
+  auto plus = [](double x, double y) { return x + y; };
 
   // ---- masses ----
-  for (int j = tid; j < nc; j += kSelThreads) mass[j] = 0.0;
+  double mass[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) mass[i] = 0.0;
   for (int gq = 0; gq < a.G; ++gq) {
-    const double* l = a.scratch + ((int64_t)t * a.H + hk * a.G + gq) * a.max_pages + r.c0;
-    double mx = -__longlong_as_double(0x7ff0000000000000ll);
-    for (int j = tid; j < nc; j += kSelThreads)
-      if (isfinite(l[j])) mx = fmax(mx, l[j]);
-    mx = block_max(mx, red);
-    if (mx == -__longlong_as_double(0x7ff0000000000000ll)) continue;
+    const double* l = logit_row(a, t, hk * a.G + gq) + r.c0;
+    constexpr int R = E <= 8 ? E : 1;              // logits kept in registers
+    double x[R], mx = -kInf64();
+#pragma unroll(E <= 8 ? E : 4)
+    for (int i = 0; i < E; ++i) {
+      const int j = tid + kSelThreads * i;
+      const double y = j < nc ? l[j] : -kInf64();
+      if (E <= 8) x[i % R] = y;
+      if (isfinite(y)) mx = fmax(mx, y);
+    }
+    mx = blk.reduce(mx, larger);
+    if (mx == -kInf64()) continue;                 // (a head without a finite logit)
     double sum = 0.0;
-    for (int j = tid; j < nc; j += kSelThreads)
-      if (isfinite(l[j])) sum += exp(l[j] - mx);
-    const double inv = 1.0 / block_sum(sum, red);
-    for (int j = tid; j < nc; j += kSelThreads)
-      if (isfinite(l[j])) mass[j] += exp(l[j] - mx) * inv;
+#pragma unroll(E <= 8 ? E : 4)
+    for (int i = 0; i < E; ++i) {
+      const int j = tid + kSelThreads * i;
+      double y = E <= 8 ? x[i % R] : (j < nc ? l[j] : -kInf64());
+      y = isfinite(y) ? exp(y - mx) : 0.0;
+      if (E <= 8) x[i % R] = y;
+      sum += y;
+    }
+    const double inv = 1.0 / blk.reduce(sum, plus);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int j = tid + kSelThreads * i;
+      if (E <= 8) {
+        mass[i] += x[i % R] * inv;
+      } else {
+        const double y = j < nc ? l[j] : -kInf64();
+        if (isfinite(y)) mass[i] += exp(y - mx) * inv;
+      }
+    }
+  }
+
+  // ---- the want-th greatest mass, by bisection on the bits (masses are not
+  // negative, so their bits order as they do) ----
+  double top = 0.0;
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    top = fmax(top, mass[i]);
+    if (tid + kSelThreads * i >= nc) mass[i] = -1.0;
+  }
+  top = blk.reduce(top, larger);
+  long long lo = 0, hi = __double_as_longlong(top) + 1;   // count(>= lo) > want > count(>= hi)
+  int above = 0;                                          // count(>= hi)
+  while (hi - lo > 1) {
+    const long long mid = lo + ((hi - lo) >> 1);
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < E; ++i) n += __double_as_longlong(mass[i]) >= mid;
+    n = blk.count(n);
+    if (n == want) {
+      lo = hi = mid;
+      above = want;
+      break;
+    }
+    if (n > want) {
+      lo = mid;
+    } else {
+      hi = mid;
+      above = n;
+    }
+  }
+  // kept: every mass >= hi, and of those equal to lo (ties) the first ones
+  int ties = want - above;
+#pragma unroll 1
+  for (int i = 0; i < E; ++i) {
+    const int first = kSelThreads * i;
+    if (first >= nc) break;
+    long long b = -1;
+#pragma unroll
+    for (int k = 0; k < E; ++k)
+      if (k == i) b = __double_as_longlong(mass[k]);
+    bool keep = b >= hi;
+    if (ties > 0) {                                       // uniform
+      const bool eq = b == lo && b < hi;
+      const uint32_t be = __ballot_sync(0xffffffffu, eq);
+      int* r2 = sm.cnt[blk.turn ^= 1];
+      if (lane == 0) r2[warp] = __popc(be);
+      __syncthreads();
+      int before = 0, all = 0;
+#pragma unroll
+      for (int w = 0; w < kSelThreads / 32; ++w) {
+        if (w < warp) before += r2[w];
+        all += r2[w];
+      }
+      keep |= eq && before + __popc(be & ((1u << lane) - 1)) < ties;
+      ties -= min(ties, all);
+    }
+    const uint32_t bk = __ballot_sync(0xffffffffu, keep);
+    if (lane == 0) sm.keep[i * (kSelThreads / 32) + warp] = bk;
   }
   __syncthreads();
-
-  // ---- the want-th greatest mass: radix select on the bits (masses are not
-  // negative, so their bits order as they do), most significant byte first ----
-  unsigned long long pivot = 0;        // every kept mass is >= pivot
-  int equal = 0;                       // of those equal to it, this many are kept (0: all)
-  if (want > 0) {
-    unsigned long long mask = 0;
-    int need = want;
-    for (int shift = 56; shift >= 0; shift -= 8) {
-      hist[tid] = 0;
-      __syncthreads();
-      for (int j = tid; j < nc; j += kSelThreads) {
-        const unsigned long long b = (unsigned long long)__double_as_longlong(mass[j]);
-        if ((b & mask) == pivot) atomicAdd(&hist[(b >> shift) & 255], 1);
+  // ---- the list, in page order ----
+  if (warp == 0) {
+    const int words = (nc + 31) / 32, per = (words + 31) / 32;
+    int n = 0;
+    for (int k = 0; k < per; ++k)
+      if (lane * per + k < words) n += __popc(sm.keep[lane * per + k]);
+    int inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    int at = a.n_first + inc - n;
+    for (int k = 0; k < per; ++k) {
+      if (lane * per + k >= words) break;
+      uint32_t w = sm.keep[lane * per + k];
+      while (w) {
+        const int b = __ffs(w) - 1;
+        w &= w - 1;
+        if (at < a.n_select - a.n_recent) sel[at++] = r.c0 + (lane * per + k) * 32 + b;
       }
-      __syncthreads();
-      if (tid < 32) {
-        // lane i holds bins 255 - 8 i .. 248 - 8 i
-        int c = 0;
+    }
+  }
+}
+
+// The fixed pages of a row's list, or the whole list where every page fits;
+// true where pages compete for places.
+__device__ __forceinline__ bool fixed_pages(const CacheArgs& a, const RowPages& r, int64_t item, int id,
+                                            int step) {
+  int* sel = a.sel + item * a.n_select;
+  if (r.n <= a.n_select) {
+    for (int i = id; i < a.n_select; i += step) sel[i] = i < r.n ? i : -1;
+    return false;
+  }
+  for (int i = id; i < a.n_first; i += step) sel[i] = i;
+  for (int i = id; i < a.n_recent; i += step) sel[a.n_select - a.n_recent + i] = r.c1 + i;
+  return a.n_select > a.n_first + a.n_recent;
+}
+
+template <int E>
+__global__ void __launch_bounds__(kSelThreads) cache_choose64_kernel(const CacheArgs a) {
+  __shared__ ExactSmem sm;
+  const int t = blockIdx.x, hk = blockIdx.y;
+  if (t >= rows_used(a)) return;
+  const RowPages r = row_pages(a, t, row_seq(a, t));
+  if (fixed_pages(a, r, (int64_t)t * a.Hkv + hk, threadIdx.x, kSelThreads)) choose64<E>(a, t, hk, sm);
+}
+
+// fp64 logits of one item by the whole block, into the item's scratch rows.
+template <int D>
+__device__ __noinline__ void logits64_item(const CacheArgs& a, int t, int hk, double* qs) {
+  constexpr int QP = D + 4;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tg = lane & 3;
+  const int s = row_seq(a, t);
+  const RowPages r = row_pages(a, t, s);
+  for (int g0 = 0; g0 < a.G; g0 += 8) {
+    __syncthreads();
+    for (int i = tid; i < 8 * D; i += kSelThreads) {
+      const int c = i / D, d = i - c * D;
+      qs[c * QP + d] = g0 + c < a.G ? (double)__bfloat162float(a.q[(int64_t)t * a.sq_t + (int64_t)(hk * a.G + g0 + c) * a.sq_h + d]) : 0.0;
+    }
+    __syncthreads();
+    for (int j = r.c0 + warp * 8; j < r.c1; j += kSelThreads / 32 * 8) {
+      const int page = j + g < r.c1 ? page_of(a, s, j + g) : -1;
+      const float4* src = reinterpret_cast<const float4*>(a.k_mean + ((int64_t)max(page, 0) * a.Hkv + hk) * D);
+      float4 v[D / 16];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) c += hist[255 - 8 * tid - u];
-        int inc = c;
+      for (int i = 0; i < D / 16; ++i) v[i] = page >= 0 ? __ldg(src + 4 * i + tg) : make_float4(0.f, 0.f, 0.f, 0.f);
+      double c0[2] = {0.0, 0.0}, c1[2] = {0.0, 0.0};
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, inc, o);
-          if (tid >= o) inc += y;
+      for (int i = 0; i < D / 16; ++i) {
+        const double* q = qs + g * QP + 4 * tg + 16 * i;
+        const double2 x = *reinterpret_cast<const double2*>(q);
+        const double2 y = *reinterpret_cast<const double2*>(q + 2);
+        dmma(c0, v[i].x, x.x);
+        dmma(c1, v[i].y, x.y);
+        dmma(c0, v[i].z, y.x);
+        dmma(c1, v[i].w, y.y);
+      }
+      if (j + g < r.c1) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (g0 + 2 * tg + e < a.G)
+            logit_row(a, t, hk * a.G + g0 + 2 * tg + e)[j + g] = page < 0 ? -kInf64() : (c0[e] + c1[e]) * a.scale;
+      }
+    }
+  }
+  __syncthreads();
+}
+
+// WPI warps choose for one (row, key head), each thread holding E of its
+// pages; a block has 8 / WPI items.
+template <int D, int WPI, int E>
+__global__ void __launch_bounds__(kSelThreads) cache_choose_kernel(const CacheArgs a) {
+  __shared__ double qs[8 * (D + 4)];
+  __shared__ ExactSmem sm;
+  __shared__ float red[kSelThreads / 32];
+  __shared__ uint32_t bits[WPI > 1 ? WPI * E : 1];
+  __shared__ int todo[8 / WPI];
+  constexpr int IPB = 8 / WPI, GS = 32 * WPI;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lid = WPI == 1 ? lane : threadIdx.x;           // thread of the item
+  const int64_t item = (int64_t)blockIdx.x * IPB + (WPI == 1 ? warp : 0);
+  const int t = (int)(item / a.Hkv), hk = (int)(item - (int64_t)t * a.Hkv);
+  const Group<WPI> grp{red};
+  bool again = false;                                      // the item needs fp64
+
+  if (t < rows_used(a)) {
+    const int s = row_seq(a, t);
+    const RowPages r = row_pages(a, t, s);
+    int* sel = a.sel + item * a.n_select;
+    const int nc = r.c1 - r.c0, want = a.n_select - a.n_first - a.n_recent;
+    if (fixed_pages(a, r, item, lid, GS)) {                // 0 < want < nc
+      float mass[E];
+#pragma unroll
+      for (int i = 0; i < E; ++i) mass[i] = 0.0f;
+      float kn = 0.0f, qn = 0.0f;
+      const float* nr = norm_row(a, s, hk) + r.c0;
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (lid + GS * i < nc) kn = fmaxf(kn, nr[lid + GS * i]);
+      bool bad = false;
+      for (int gq = 0; gq < a.G; ++gq) {
+        const __nv_bfloat16* q = a.q + (int64_t)t * a.sq_t + (int64_t)(hk * a.G + gq) * a.sq_h + (D / 32) * lane;
+        float q2 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 32; i += 2) {
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(q + i);
+          q2 += bf_lo(w) * bf_lo(w) + bf_hi(w) * bf_hi(w);
         }
-        int before = inc - c;
-        if (before < need && inc >= need) {
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const int bin = 255 - 8 * tid - u;
-            if (before < need && before + hist[bin] >= need) {
-              found[0] = bin;
-              found[1] = before;
+        for (int o = 16; o; o >>= 1) q2 += __shfl_xor_sync(0xffffffffu, q2, o);
+        qn = fmaxf(qn, q2);
+        const float* l = reinterpret_cast<const float*>(logit_row(a, t, hk * a.G + gq)) + r.c0;
+        float x[E], mx = -kInf;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          const bool in = lid + GS * i < nc;
+          x[i] = in ? l[lid + GS * i] : -kInf;
+          bad |= in && !(fabsf(x[i]) < kInf);
+          mx = fmaxf(mx, x[i]);
+        }
+        mx = grp.max(mx);
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x[i]) : "f"(x[i] - mx));
+          sum += x[i];
+        }
+        const float inv = 1.0f / grp.sum(sum);
+#pragma unroll
+        for (int i = 0; i < E; ++i) mass[i] = fmaf(x[i], inv, mass[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (lid + GS * i >= nc) mass[i] = -1.0f;
+      kn = grp.max(kn);
+      bad |= !(kn * qn < kInf);
+      // a float that `want` masses reach and the others do not, by bisection
+      // on the bits
+      float top = mass[0];
+#pragma unroll
+      for (int i = 1; i < E; ++i) top = fmaxf(top, mass[i]);
+      top = grp.max(top);
+      int lo = 0, hi = __float_as_int(top) + 1;            // count(>= lo) > want > count(>= hi)
+      int cut = -1;
+      if (grp.count(bad) == 0) {
+        while (hi - lo > 1) {
+          const int mid = lo + ((hi - lo) >> 1);
+          int n = 0;
+#pragma unroll
+          for (int i = 0; i < E; ++i) n += mass[i] >= __int_as_float(mid);
+          n = grp.count(n);
+          if (n == want) {
+            cut = mid;
+            break;
+          }
+          if (n > want) lo = mid; else hi = mid;
+        }
+      }
+      if (cut < 0) {
+        again = true;                                      // equal floats, or values not finite
+      } else {
+        const float c = __int_as_float(cut);
+        float in = kInf, out = 0.0f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          if (mass[i] >= c) in = fminf(in, mass[i]); else out = fmaxf(out, mass[i]);
+        }
+        in = -grp.max(-in);
+        out = grp.max(out);
+        // relative error of a mass: the logits' error in the exponent of the
+        // term and of the sum, ex2 and its argument (near the border up to
+        // ln(1 / mass) below the maximum), and the sums' roundings
+        const float delta = kLogitErr * (float)a.scale * sqrtf(qn) * kn;
+        const float err = 2.0f * delta + 1.2e-7f * (float)(E + 26 + a.G) + 4.8e-7f * (8.0f - logf(fmaxf(out, 1e-37f)));
+        again = !(delta < 0.05f) || !(in * (1.0f - 1.1f * err) > out * (1.0f + 1.1f * err));
+        if (!again) {
+          uint32_t mine = 0;                               // WPI = 1: word `lane`
+#pragma unroll
+          for (int i = 0; i < E; ++i) {
+            const uint32_t b = __ballot_sync(0xffffffffu, mass[i] >= c);
+            if constexpr (WPI == 1) {
+              if (lane == i) mine = b;
+            } else {
+              if (lane == 0) bits[i * WPI + warp] = b;
             }
-            before += hist[bin];
+          }
+          constexpr int WPL = WPI == 1 ? 1 : (WPI * E + 31) / 32;   // words of a lane
+          if constexpr (WPI > 1) __syncthreads();
+          if (WPI == 1 || warp == 0) {
+            uint32_t w[WPL];
+            int n = 0;
+#pragma unroll
+            for (int k = 0; k < WPL; ++k) {
+              w[k] = WPI == 1 ? mine : (lane * WPL + k < WPI * E ? bits[lane * WPL + k] : 0u);
+              n += __popc(w[k]);
+            }
+            int inc = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const int y = __shfl_up_sync(0xffffffffu, inc, o);
+              if (lane >= o) inc += y;
+            }
+            int at = a.n_first + inc - n;
+#pragma unroll
+            for (int k = 0; k < WPL; ++k)
+              while (w[k]) {
+                const int b = __ffs(w[k]) - 1;
+                w[k] &= w[k] - 1;
+                sel[at++] = r.c0 + (lane * WPL + k) * 32 + b;
+              }
           }
         }
       }
-      __syncthreads();
-      const int bin = found[0], in_bin = hist[bin];
-      need -= found[1];
-      pivot |= (unsigned long long)bin << shift;
-      mask |= 255ull << shift;
-      __syncthreads();
-      if (in_bin == need) {            // the whole bin is kept
-        need = 0;
-        break;
-      }
     }
-    equal = need;
   }
-
-  // ---- the list, in page order ----
-  int at = 0, eq_seen = 0;
-  for (int base = 0; base < r.n; base += kSelThreads) {
-    const int j = base + tid;
-    bool keep = j < r.c0 || (j >= r.c1 && j < r.n), eq = false;
-    if (j >= r.c0 && j < r.c1 && want > 0) {
-      const unsigned long long b = (unsigned long long)__double_as_longlong(mass[j - r.c0]);
-      if (equal == 0) {
-        keep = b >= pivot;
-      } else {
-        keep = b > pivot;
-        eq = b == pivot;
-      }
-    }
-    const uint32_t be = __ballot_sync(0xffffffffu, eq), below = (1u << (tid & 31)) - 1;
-    if ((tid & 31) == 0) wsum[0][tid >> 5] = __popc(be);
-    __syncthreads();
-    int e0 = eq_seen, e_all = 0;
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-      if (w < (tid >> 5)) e0 += wsum[0][w];
-      e_all += wsum[0][w];
-    }
-    if (eq) keep = e0 + __popc(be & below) < equal;
-    eq_seen += e_all;
-    const uint32_t bk = __ballot_sync(0xffffffffu, keep);
-    if ((tid & 31) == 0) wsum[1][tid >> 5] = __popc(bk);
-    __syncthreads();
-    int k0 = at, k_all = 0;
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-      if (w < (tid >> 5)) k0 += wsum[1][w];
-      k_all += wsum[1][w];
-    }
-    if (keep) {
-      const int i = k0 + __popc(bk & below);
-      if (i < a.n_select) sel[i] = j;
-    }
-    at += k_all;
+  // ---- items that fp64 decides, one after the other ----
+  if (lid == 0) todo[WPI == 1 ? warp : 0] = again;
+  __syncthreads();
+#pragma unroll 1
+  for (int i = 0; i < IPB; ++i) {
+    if (!todo[i]) continue;
+    const int64_t it = (int64_t)blockIdx.x * IPB + i;
+    logits64_item<D>(a, (int)(it / a.Hkv), (int)(it % a.Hkv), qs);
+    choose64<E * WPI / 8 < 1 ? 1 : E * WPI / 8>(a, (int)(it / a.Hkv), (int)(it % a.Hkv), sm);
     __syncthreads();
   }
 }
@@ -624,25 +1103,56 @@ cudaError_t launch_cache_append(const CacheArgs& a, cudaStream_t s) {
   return a.fp8 ? go(cache_append_kernel<64, true>) : go(cache_append_kernel<64, false>);
 }
 
-cudaError_t launch_cache_select(const CacheArgs& a, cudaStream_t s) {
-  const int tile_rows = a.cu ? (a.G >= kSelCols ? 1 : kSelCols / a.G) : 1;
+template <int D>
+static cudaError_t select_d(const CacheArgs& a, cudaStream_t s) {
+  int dev = 0, sms = 0;
+  cudaError_t e = device_sms(dev, sms);
+  if (e != cudaSuccess) return e;
+  // two rows of a sequence or more on average: the fast logits
+  const bool fast = a.cu && a.T >= 2 * (int64_t)a.S;
+  const int most = fast ? kSelCols : 8;
+  const int tile_rows = !a.cu || a.G >= most ? 1 : most / a.G;
   const int64_t tiles = a.cu ? (int64_t)(a.T / tile_rows) + a.S : a.S;
   const int cols = (tile_rows * a.G + 7) / 8 * 8;
-  const int bytes = cols * (a.d + 4) * 8;
-  const dim3 grid((unsigned)tiles, a.Hkv, (a.max_pages + kSelPages - 1) / kSelPages);
-  auto go = [&](auto kernel) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-    kernel<<<grid, kSelThreads, bytes, s>>>(a, tile_rows);
+  // pages of a logits block: all of them, or so few that every SM has blocks,
+  // a multiple of what a block's warps take at a time
+  const int step = fast ? 128 : 64;
+  int pages = (a.max_pages + step - 1) / step * step;
+  while (pages > 2 * step && tiles * a.Hkv * ((a.max_pages + pages - 1) / pages) < 4ll * sms)
+    pages = (pages / 2 + step - 1) / step * step;
+  const dim3 grid((unsigned)tiles, a.Hkv, (a.max_pages + pages - 1) / pages);
+  const int lb = fast ? cols * (D * 2 + 16 + 4) : cols * (D + 4) * 8;
+  static OncePerDevice once_f, once_d;
+  auto go = [&](auto kernel, OncePerDevice& once) {
+    if (lb > 48 * 1024) {
+      const cudaError_t r = once.allow(reinterpret_cast<const void*>(kernel), dev, 232448);
+      if (r != cudaSuccess) return r;
+    }
+    kernel<<<grid, kSelThreads, lb, s>>>(a, tile_rows, pages);
     return cudaGetLastError();
   };
-  cudaError_t e = a.d == 128 ? go(cache_logits_kernel<128>) : go(cache_logits_kernel<64>);
+  e = fast ? go(cache_logits_kernel<D>, once_f) : go(cache_logits64_kernel<D>, once_d);
   if (e != cudaSuccess) return e;
-  const int mb = a.max_pages * 8;
-  e = cudaFuncSetAttribute(cache_choose_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, mb);
-  if (e != cudaSuccess) return e;
-  cache_choose_kernel<<<dim3(a.T, a.Hkv), kSelThreads, mb, s>>>(a);
+  const int64_t items = (int64_t)a.T * a.Hkv;
+  if (!fast) {
+    const dim3 all(a.T, a.Hkv);
+    if (a.max_pages <= 512) cache_choose64_kernel<2><<<all, kSelThreads, 0, s>>>(a);
+    else if (a.max_pages <= 2048) cache_choose64_kernel<8><<<all, kSelThreads, 0, s>>>(a);
+    else cache_choose64_kernel<64><<<all, kSelThreads, 0, s>>>(a);
+  } else if (a.max_pages <= 512) {
+    cache_choose_kernel<D, 1, 16><<<(unsigned)((items + 7) / 8), kSelThreads, 0, s>>>(a);
+  } else if (a.max_pages <= 1024) {
+    cache_choose_kernel<D, 1, 32><<<(unsigned)((items + 7) / 8), kSelThreads, 0, s>>>(a);
+  } else if (a.max_pages <= 8192) {
+    cache_choose_kernel<D, 8, 32><<<(unsigned)items, kSelThreads, 0, s>>>(a);
+  } else {
+    cache_choose_kernel<D, 8, 64><<<(unsigned)items, kSelThreads, 0, s>>>(a);
+  }
   return cudaGetLastError();
+}
+
+cudaError_t launch_cache_select(const CacheArgs& a, cudaStream_t s) {
+  return a.d == 128 ? select_d<128>(a, s) : select_d<64>(a, s);
 }
 
 }  // namespace ta

@@ -2,6 +2,8 @@
 // cached-attention kernels (append, decode, page choice, sparse attention).
 #pragma once
 
+#include <atomic>
+
 #include "ta_common.cuh"
 #include "tiered_attn_cache.h"
 
@@ -12,6 +14,8 @@ namespace ta {
 // one arrival counter and two partial results for each CTA of the attention
 // grid.
 constexpr int kMaxAttnCtas = 512;
+constexpr int kMaxDecodeSeqs = 2048;              // rows of a decode (a prefix in shared memory)
+constexpr int kMaxSelectPages = 16384;            // pages of a row that chooses (masses there)
 constexpr int kMaxTileHeads = 16;                 // query heads of one CTA's item
 constexpr size_t kWsCounters = 256;
 constexpr size_t kWsPartML = kWsCounters + kMaxAttnCtas * 4;
@@ -53,11 +57,32 @@ struct CacheArgs {
   double* scratch;
 };
 
+// Doubles of a row of the choice's scratch: whole 128-byte lines of floats.
+__host__ __device__ inline int64_t select_pitch(int max_pages) { return (max_pages + 31) / 32 * 32; }
+
 cudaError_t launch_cache_append(const CacheArgs& a, cudaStream_t s);
 cudaError_t launch_cache_select(const CacheArgs& a, cudaStream_t s);
 // `sparse`: over the lists in a.sel, else over whole sequences.
 cudaError_t launch_cache_attn(const CacheArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
                               bool sparse, cudaStream_t s);
+
+// The current device and its number of SMs, and a kernel's shared-memory limit
+// raised once for each device: neither changes while the process lives.
+struct OncePerDevice {
+  std::atomic<unsigned long long> done{0};
+  cudaError_t allow(const void* kernel, int dev, int bytes) {
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
+};
+inline cudaError_t device_sms(int& dev, int& sms) {
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return e;
+}
 
 #ifdef __CUDACC__
 

@@ -34,7 +34,8 @@ ta_status validate(const ta_cache_params* p) {
 }
 
 size_t scratch_bytes(const ta_cache_params* p) {
-  return p->n_select > 0 ? (size_t)p->T * p->H * p->max_pages * 8 : 0;
+  if (p->n_select <= 0) return 0;
+  return (size_t)ta::select_pitch(p->max_pages) * ((size_t)p->T * p->H * 8 + (size_t)p->S * p->Hkv * 4);
 }
 
 ta_status check_ws(const void* ws, size_t have, size_t need) {
@@ -240,7 +241,7 @@ ta_status tiered_attn_cache_decode(const ta_cache_params* p, const ta_cache* cac
   if (st != TA_OK) return st;
   // the kernel keeps a prefix over the sequences in shared memory, in 31 bits
   const int64_t units = ((int64_t)p->max_pages * p->page_size + 127) / 128;
-  if (p->S > 2048 || p->S * units > 0x7fffffff) return TA_ERR_UNSUPPORTED;
+  if (p->S > ta::kMaxDecodeSeqs || p->S * units > 0x7fffffff) return TA_ERR_UNSUPPORTED;
   return attend(p, cache, Q, nullptr, nullptr, lens, table, O, lse, ws, ws_bytes, stream, false);
 }
 
@@ -250,7 +251,8 @@ ta_status tiered_attn_cache_select(const ta_cache_params* p, const ta_cache* cac
   ta_status st = validate(p);
   if (st != TA_OK) return st;
   if (p->n_select < 1) return TA_ERR_INVALID_ARG;
-  if (p->max_pages > 16384) return TA_ERR_UNSUPPORTED;   // a row's masses stand in shared memory
+  // a row's masses, and the queries of a key head, stand in shared memory
+  if (p->max_pages > ta::kMaxSelectPages || p->H / p->Hkv > 128) return TA_ERR_UNSUPPORTED;
   if ((st = check_cache(p, cache, false, true)) != TA_OK) return st;
   if ((st = check_index(p, cu, lens, table)) != TA_OK) return st;
   if (!rows_ok(Q, p->stride_q_t, p->stride_q_h) || !aligned(sel, 4)) return TA_ERR_INVALID_ARG;

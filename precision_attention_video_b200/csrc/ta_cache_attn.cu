@@ -732,12 +732,13 @@ template <int D, bool FP8, int NT, bool SPARSE>
 cudaError_t run(const CacheArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
   using C = Cfg<D, FP8, NT>;
   int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaError_t e = device_sms(dev, sms);
   if (e != cudaSuccess) return e;
   const int bytes = C::kBytes + (SPARSE ? 0 : (a.S + 1) * 4);
+  static_assert(C::kBytes + (SPARSE ? 0 : (kMaxDecodeSeqs + 1) * 4) <= 232448, "shared memory");
   auto k = cache_attn_kernel<D, FP8, NT, SPARSE>;
-  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  static OncePerDevice once;
+  e = once.allow(reinterpret_cast<const void*>(k), dev, C::kBytes + (SPARSE ? 0 : (kMaxDecodeSeqs + 1) * 4));
   if (e != cudaSuccess) return e;
   constexpr int kUnit = C::kUnit;
   // no more CTAs than units the call can have

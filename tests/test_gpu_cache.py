@@ -394,6 +394,51 @@ def test_select(cuda_ok, case, tie):
     np.testing.assert_array_equal(sel.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("near", [1e-2, 1e-4, 1e-6, 3e-8])
+@pytest.mark.parametrize("span", [0.0, 12.0])
+def test_select_near_ties(cuda_ok, near, span):
+    # pages that differ by little, means of very different sizes and queries
+    # of very different elements: fp64's choice, whatever the fast sums say
+    for old, new, kw in (([3000, 500], [60, 3], dict(ps=16, n_select=12, H=12, Hkv=3)),
+                         ([40000], [1], dict(ps=16, n_select=64, H=4, Hkv=1, d=64)),
+                         ([12000, 9000], [700, 1], dict(ps=16, n_select=7, H=8, Hkv=4))):
+        st = Step(old, new, seed=17, **kw)
+        base = torch.randn(3, 1, st.Hkv, st.d, generator=st.g)
+        mean = base[torch.randint(0, 3, (st.P,), generator=st.g), 0]
+        mean = mean + near * torch.randn(st.P, st.Hkv, st.d, generator=st.g)
+        mean *= torch.exp2(span * (torch.rand(st.Hkv, st.d, generator=st.g) - 0.5))
+        st.cache.k_mean.copy_(mean)
+        st.Q *= torch.exp2(span * (torch.rand(st.H, st.d, generator=st.g) - 0.7)).to(BF).to(DEV)
+        sel = st.select()
+        want = OC.select(np64(st.Q), np64(st.cache.k_mean), st.lens, st.cu, st.table, st.G, st.ps,
+                         st.p.n_select, 1, 1, st.scale)
+        np.testing.assert_array_equal(sel.cpu().numpy(), want)
+    assert st.status() == 0
+
+
+def test_select_many_pages(cuda_ok):
+    for W, new in ((16384, [1]), (5000, [2]), (700, [300])):
+        st = Step([W * 16 - new[0]], new, H=2, Hkv=1, d=64, ps=16, n_select=20, seed=W)
+        means_of(st)
+        want = OC.select(np64(st.Q), np64(st.cache.k_mean), st.lens, st.cu, st.table, st.G, st.ps, 20, 1,
+                         1, st.scale)
+        np.testing.assert_array_equal(st.select().cpu().numpy(), want)
+
+
+def test_select_extreme_magnitudes(cuda_ok):
+    # means and queries outside f16's range, denormal and huge
+    for ek, eq in ((30, -20), (-40, 30), (-140, 0), (100, -90), (0, -135), (60, 60)):
+        st = Step([900], [4], H=4, Hkv=2, n_select=5, ps=32, seed=3)
+        means_of(st)
+        st.cache.k_mean *= 2.0 ** ek if ek > -126 else 2.0 ** (ek + 40) * 2.0 ** -40
+        st.Q *= 2.0 ** eq if eq > -126 else 2.0 ** (eq + 40)
+        if eq <= -126:
+            st.Q *= 2.0 ** -40
+        want = OC.select(np64(st.Q), np64(st.cache.k_mean), st.lens, st.cu, st.table, st.G, st.ps, 5, 1, 1,
+                         st.scale)
+        np.testing.assert_array_equal(st.select().cpu().numpy(), want, err_msg=str((ek, eq)))
+
+
 def test_select_values_that_are_not_finite(cuda_ok):
     st = Step([700], [1], H=4, Hkv=2, n_select=5, seed=1)
     means_of(st)
