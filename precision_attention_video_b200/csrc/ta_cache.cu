@@ -342,8 +342,8 @@ __global__ void __launch_bounds__(kAppendThreads, 4) cache_append_kernel(const C
 // over the pages j that compete, masses M_gj = exp(l_gj - max) / sum, and the
 // n_select - n_first - n_recent pages of greatest sum_g M_gj, as fp64 decides.
 //
-// Single rows are bound by reading the means: their logits are fp64 products
-// (mma.sync m8n8k4), and a block chooses for each (row, key head).
+// Single rows are bound by reading the means: their logits are fp64 sums, and
+// a block chooses for each (row, key head).
 //
 // Where many rows of a sequence share its means, fp64 would bound, and it
 // decides only where it has to.  There the logits come from f16 tensor-core
@@ -356,12 +356,12 @@ __global__ void __launch_bounds__(kAppendThreads, 4) cache_append_kernel(const C
 // The error: a page's mean is scaled by a power of two to f16's range and
 // split into two f16 parts (22 bits of each element), the query scaled the same
 // way (its 8 bits are exact down to 2^-14 of its largest element); what is cut
-// off is at most 2^-21 of |q| |kbar|.  Each 16 products go into a sum of their
-// own, where an addend may lose 2^-24 of the largest: 2^-20 in all; their eight
-// sums add up in fp32, 2^-21.  2^-18.9 scale |q| |kbar| covers these.
+// off is at most 2^-21 of |q| |kbar|.  Each 32 products go into a sum of their
+// own, where an addend may lose 2^-24 of the largest: 2^-19 in all; these sums
+// add up in fp32, 2^-22.  2^-18.5 scale |q| |kbar| covers them.
 constexpr int kSelThreads = 256;
 constexpr int kSelCols = 64;           // (row, head) columns of a logits block
-constexpr float kLogitErr = 2.05e-6f;  // 2^-18.9
+constexpr float kLogitErr = 2.7e-6f;   // 2^-18.5
 constexpr float kInf = 3.0e38f;        // a logit above is taken as not finite
 
 // Pages that row t sees, and the pages [c0, c1) that compete for it.
@@ -379,13 +379,18 @@ __device__ __forceinline__ RowPages row_pages(const CacheArgs& a, int t, int s) 
 
 // Scratch: for each (row, query head) `pitch` doubles, of which the fp32
 // logits (in log2 units) take the first half until the row is done in fp64;
-// then, for each (sequence, key head), the pages' norms.
+// then, for each (sequence, key head), the pages' norms,
 __device__ __forceinline__ double* logit_row(const CacheArgs& a, int t, int h) {
   return a.scratch + ((int64_t)t * a.H + h) * select_pitch(a.max_pages);
 }
 __device__ __forceinline__ float* norm_row(const CacheArgs& a, int s, int hk) {
   return reinterpret_cast<float*>(a.scratch + (int64_t)a.T * a.H * select_pitch(a.max_pages)) +
          ((int64_t)s * a.Hkv + hk) * select_pitch(a.max_pages);
+}
+
+// and, for each (row, query head), the query's norm.
+__device__ __forceinline__ float* qnorm_row(const CacheArgs& a) {
+  return norm_row(a, a.S, 0);
 }
 
 __device__ __forceinline__ void dmma(double (&c)[2], double a, double b) {
@@ -418,6 +423,12 @@ __device__ __forceinline__ float unit_scale(float x) {
 __device__ __forceinline__ double kInf64() { return __longlong_as_double(0x7ff0000000000000ll); }
 __device__ __forceinline__ bool tiny(float x) { return x > 0.0f && x < 1e-35f; }
 
+// Place of element d in a column of fp64 queries: the two elements that a lane
+// reads at a time, of its four consecutive ones, next to its neighbours'.
+__device__ __forceinline__ int q_slot(int d) {
+  return (d & ~15) + ((d >> 1) & 1) * 8 + ((d >> 2) & 3) * 2 + (d & 1);
+}
+
 // Rows of a logits block: up to tile_rows of one sequence.
 struct RowTile {
   int s, t0, t1, t_end;
@@ -443,36 +454,53 @@ __device__ __forceinline__ RowTile row_tile(const CacheArgs& a, int tile, int ti
   return r;
 }
 
-// fp64 logits of a tile of few rows: a warp takes 8 pages (A fragments) at a
-// time, the next 8 on their way, and all columns of the tile.
+// fp64 logits of a tile of few rows.  A warp takes 8 pages at a time, the next
+// 8 on their way to shared memory: 8 lanes hold a page and multiply it with 4 columns, two
+// pages for each column element read from shared memory, and 7 exchanges with
+// halving leave one of the 8 sums (2 pages by 4 columns) with each lane.
 template <int D>
-__global__ void __launch_bounds__(kSelThreads, 2) cache_logits64_kernel(const CacheArgs a, int tile_rows,
+__global__ void __launch_bounds__(kSelThreads, 3) cache_logits64_kernel(const CacheArgs a, int tile_rows,
                                                                         int pages) {
   extern __shared__ __align__(16) unsigned char sel_smem[];
-  double* qs = reinterpret_cast<double*>(sel_smem);
-  constexpr int QP = D + 4;            // padded: a column's chunks fall on banks of their own
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tg = lane & 3;
+  double2* qs = reinterpret_cast<double2*>(sel_smem);
+  constexpr int K = D / 32, STEP = kSelThreads / 32 * 8;   // 16-byte chunks of a lane; pages of a step
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane >> 3, li = lane & 7;
   const int hk = blockIdx.y;
   const RowTile tile = row_tile(a, blockIdx.x, tile_rows);
   const int s = tile.s, t0 = tile.t0, t1 = tile.t1;
   if (t0 >= t1) return;
   const RowPages last = row_pages(a, t1 - 1, s);   // the tile's longest row
-  const int j0 = max(blockIdx.z * pages, min(a.n_first, last.n));
+  const int j0 = max((int)blockIdx.z * pages, min(a.n_first, last.n));
   const int j_end = min(last.c1, (int)(blockIdx.z + 1) * pages);
   if (j0 >= j_end || last.n <= a.n_select) return;
-  const int cols = (t1 - t0) * a.G, tiles = (cols + 7) / 8;
+  const int cols = (t1 - t0) * a.G, groups = (cols + 3) / 4;
 
-  float4 v[D / 16];
-  int page = -1;
-  auto fetch = [&](int j) {            // the lane's 32 elements of page j + g
-    page = j + g < j_end ? page_of(a, s, j + g) : -1;
-    const float4* src = reinterpret_cast<const float4*>(a.k_mean + ((int64_t)max(page, 0) * a.Hkv + hk) * D);
+  int ids = -1;                        // lane l < 8: page l of the batch after the next
+  auto ask = [&](int j) {
+    ids = -1;
+    if (lane < 8 && j + lane < j_end) ids = page_of(a, s, j + lane);
+  };
+  // two batches of 8 pages for each warp, behind the queries
+  float4* stage = reinterpret_cast<float4*>(qs + groups * 4 * (D / 2)) + warp * (16 * (D / 4));
+  uint32_t live = 0, nlive = 0;        // pages of a batch with a mean
+  auto fetch = [&](int buf, uint32_t& on) {
+    on = __ballot_sync(0xffffffffu, ids >= 0);
+    constexpr int PPI = 128 / D;       // pages that the warp copies at a time
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) v[i] = page >= 0 ? __ldg(src + 4 * i + tg) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < 8; i += PPI) {
+      const int p = i + lane / (D / 4), x = lane % (D / 4);
+      const int page = __shfl_sync(0xffffffffu, ids, p);
+      if (page >= 0)
+        cp_async16(stage + (buf * 8 + p) * (D / 4) + x, a.k_mean + ((int64_t)page * a.Hkv + hk) * D + 4 * x, 16);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
   const int j_first = j0 + warp * 8;
-  if (j_first < j_end) fetch(j_first);
-  for (int i = threadIdx.x; i < tiles * 8 * (D / 2); i += kSelThreads) {
+  ask(j_first);
+  fetch(0, live);
+  ask(j_first + STEP);
+  // element 4 (8 k + l) + 2 h + (0, 1) of column c at ((c K + k) 2 + h) 8 + l
+  for (int i = threadIdx.x; i < groups * 4 * (D / 2); i += kSelThreads) {
     const int c = i / (D / 2), d = 2 * (i - c * (D / 2));
     double2 x = make_double2(0.0, 0.0);
     if (c < cols) {
@@ -480,38 +508,62 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_logits64_kernel(const Ca
       const uint32_t w = *reinterpret_cast<const uint32_t*>(a.q + (int64_t)(t0 + r) * a.sq_t + (int64_t)h * a.sq_h + d);
       x = make_double2((double)bf_lo(w), (double)bf_hi(w));
     }
-    *reinterpret_cast<double2*>(qs + c * QP + d) = x;
+    qs[((c * K + d / 32) * 2 + (d >> 1 & 1)) * 8 + (d >> 2 & 7)] = x;
   }
   __syncthreads();
-  for (int j = j_first; j < j_end; j += kSelThreads / 32 * 8) {
-    double am[D / 16][4];
+  int buf = 0;
+  for (int j = j_first; j < j_end; j += STEP) {
+    fetch(buf ^ 1, nlive);
+    ask(j + 2 * STEP);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncwarp();
+    const float4* v = stage + (buf * 8 + sub) * (D / 4) + li;
+    for (int c0 = 0; c0 < groups * 4; c0 += 4) {
+      double w[8];                     // 4 (page) + column
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) am[i][0] = v[i].x, am[i][1] = v[i].y, am[i][2] = v[i].z, am[i][3] = v[i].w;
-    const bool live = page >= 0;
-    if (j + kSelThreads / 32 * 8 < j_end) fetch(j + kSelThreads / 32 * 8);
-    for (int ct = 0; ct < tiles; ++ct) {
-      double c0[2] = {0.0, 0.0}, c1[2] = {0.0, 0.0};
-      const double* q = qs + (ct * 8 + g) * QP + 4 * tg;
+      for (int k = 0; k < 8; ++k) w[k] = 0.0;
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        const double2 x = *reinterpret_cast<const double2*>(q + 16 * i);
-        const double2 y = *reinterpret_cast<const double2*>(q + 16 * i + 2);
-        dmma(c0, am[i][0], x.x);
-        dmma(c1, am[i][1], x.y);
-        dmma(c0, am[i][2], y.x);
-        dmma(c1, am[i][3], y.y);
-      }
-      if (j + g < j_end) {
+      for (int k = 0; k < K; ++k) {
+        double x[2][4];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int c = ct * 8 + 2 * tg + e;
-          if (c >= cols) continue;
-          const int r = c / a.G, h = hk * a.G + (c - r * a.G);
-          logit_row(a, t0 + r, h)[j + g] = live ? (c0[e] + c1[e]) * a.scale : -kInf64();
+          const float4 y = v[e * D + 8 * k];
+          x[e][0] = y.x, x[e][1] = y.y, x[e][2] = y.z, x[e][3] = y.w;
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const double2 q0 = qs[((c0 + c) * K + k) * 16 + li], q1 = qs[((c0 + c) * K + k) * 16 + 8 + li];
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            w[4 * e + c] = fma(x[e][3], q1.y, fma(x[e][2], q1.x, fma(x[e][1], q0.y, fma(x[e][0], q0.x, w[4 * e + c]))));
         }
       }
+#pragma unroll
+      for (int n = 4; n; n >>= 1) {    // exchange with lane ^ n, halving the sums
+        const bool up = lane & n;
+#pragma unroll
+        for (int k = 0; k < n; ++k) {
+          const double send = up ? w[k] : w[k + n], keep = up ? w[k + n] : w[k];
+          w[k] = keep + __shfl_xor_sync(0xffffffffu, send, n);
+        }
+      }
+      const int c = c0 + (li & 3), jj = j + sub + (li & 4);
+      if (c < cols && jj < j_end) {
+        const int r = c / a.G, h = hk * a.G + (c - r * a.G);
+        logit_row(a, t0 + r, h)[jj] = live >> (sub + (li & 4)) & 1 ? w[0] * a.scale : -kInf64();
+      }
     }
+    live = nlive;
+    buf ^= 1;
+    __syncwarp();                      // all lanes have read: the buffer may be refilled
   }
+}
+
+// Shared memory of the fast logits: queries (f16, padded columns), their
+// scales and rows, and 16 pages for each warp.
+template <int D>
+__host__ __device__ constexpr int logits_stage_off(int cols) {
+  return ((cols + 7) / 8 * 8 * (D * 2 + 32 + 8) + 15) / 16 * 16;
 }
 
 // fp32 logits (in log2 units) of a tile of many rows: a warp takes 16 pages
@@ -520,7 +572,7 @@ template <int D>
 __global__ void __launch_bounds__(kSelThreads, 2) cache_logits_kernel(const CacheArgs a, int tile_rows,
                                                                       int pages) {
   extern __shared__ __align__(16) unsigned char sel_smem[];
-  constexpr int QB = D * 2 + 16;       // bytes of a column, padded against bank conflicts
+  constexpr int QB = D * 2 + 32;       // bytes of a column, padded against bank conflicts
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tg = lane & 3;
   const int hk = blockIdx.y;
   const RowTile tile = row_tile(a, blockIdx.x, tile_rows);
@@ -533,63 +585,101 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_logits_kernel(const Cach
   const int cols = (t1 - t0) * a.G, tiles = (cols + 7) / 8;
   unsigned char* qs = sel_smem;                    // f16 queries, [column][D]
   float* qsc = reinterpret_cast<float*>(sel_smem + ((tile_rows * a.G + 7) / 8 * 8) * QB);
+  int* qat = reinterpret_cast<int*>(qsc) + (tile_rows * a.G + 7) / 8 * 8;   // a column's logit row
 
-  // A fragments: a lane's four k indices of a step are four consecutive
-  // elements of its rows g and g + 8
-  float4 v[2][D / 16];
+  // each warp has its next 16 pages on their way to shared memory while it
+  // multiplies the last ones
+  constexpr int PR = D * 4 + 64;                   // bytes of a page there (half a line off)
+  unsigned char* stage = sel_smem + logits_stage_off<D>(tile_rows * a.G) + warp * (16 * PR);
+  constexpr int CH = D / 4;                        // 16-byte chunks of a page
+  int pg_next = -1;                                // lane l < 16: page l of the next batch
+  auto page_ids = [&](int j) {
+    pg_next = -1;
+    if (lane < 16 && j + lane < j_end && j + lane >= a.n_first) pg_next = page_of(a, s, j + lane);
+  };
   auto fetch = [&](int j) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int jj = j + g + 8 * e;
-      int page = -1;
-      if (jj < j_end && jj >= a.n_first) page = page_of(a, s, jj);
-      const float4* src = reinterpret_cast<const float4*>(a.k_mean + ((int64_t)max(page, 0) * a.Hkv + hk) * D);
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c)
-        v[e][c] = page >= 0 ? __ldg(src + 4 * c + tg) : make_float4(__int_as_float(0x7fffffff), 0.f, 0.f, 0.f);
+    if (j < j_end) {
+#pragma unroll 4
+      for (int i = 0; i < CH / 2; ++i) {           // 16 pages of CH chunks
+        const int c = i * 32 + lane, p = c / CH, x = c - p * CH;
+        const int page = __shfl_sync(0xffffffffu, pg_next, p);
+        unsigned char* dst = stage + p * PR + x * 16;
+        if (page >= 0)
+          cp_async16(dst, a.k_mean + ((int64_t)page * a.Hkv + hk) * D + x * 4, 16);
+        else
+          *reinterpret_cast<uint4*>(dst) = make_uint4(0x7fffffffu, 0u, 0u, 0u);   // NaN: no such page
+      }
     }
   };
+  page_ids(j0 + warp * 16);
+  fetch(j0 + warp * 16);
+  page_ids(j0 + warp * 16 + 128);
 
-  // queries: a warp takes a column at a time
-  for (int c = warp; c < tiles * 8; c += kSelThreads / 32) {
-    constexpr int E = D / 32;                      // elements of a lane
-    float x[E];
-    float am = 0.0f;
-    if (c < cols) {
-      const int r = c / a.G, h = hk * a.G + (c - r * a.G);
-      const __nv_bfloat16* q = a.q + (int64_t)(t0 + r) * a.sq_t + (int64_t)h * a.sq_h + E * lane;
+  // queries: D / 8 lanes hold a column, 8 elements each
+  constexpr int LPC = D / 8, CPB = kSelThreads / LPC;
+#pragma unroll 1
+  for (int cb = 0; cb < tiles * 8; cb += 4 * CPB) {
+    uint4 w[4];
 #pragma unroll
-      for (int i = 0; i < E; i += 2) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(q + i);
-        x[i] = bf_lo(w), x[i + 1] = bf_hi(w);
-        am = fmaxf(am, fmaxf(fabsf(x[i]), fabsf(x[i + 1])));
+    for (int i = 0; i < 4; ++i) {
+      const int c = cb + i * CPB + threadIdx.x / LPC;
+      w[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (c < cols) {
+        const int r = c / a.G, h = hk * a.G + (c - r * a.G);
+        w[i] = *reinterpret_cast<const uint4*>(a.q + (int64_t)(t0 + r) * a.sq_t + (int64_t)h * a.sq_h + 8 * (threadIdx.x % LPC));
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) x[i] = 0.0f;
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-    const float up = unit_scale(am);
+    for (int i = 0; i < 4; ++i) {
+      const int c = cb + i * CPB + threadIdx.x / LPC;
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+      float am = 0.0f, n2 = 0.0f;
 #pragma unroll
-    for (int i = 0; i < E; i += 2)
-      *reinterpret_cast<__half2*>(qs + c * QB + (E * lane + i) * 2) = __floats2half2_rn(x[i] * up, x[i + 1] * up);
-    if (lane == 0)
-      qsc[c] = tiny(am) ? __int_as_float(0x7fffffff) : (float)(a.scale * 1.4426950408889634) / up;
+      for (int k = 0; k < 4; ++k) {
+        const float x = bf_lo(u[k]), y = bf_hi(u[k]);
+        am = fmax3(am, fabsf(x), fabsf(y));
+        n2 += x * x + y * y;
+      }
+#pragma unroll
+      for (int o = 1; o < LPC; o <<= 1) {
+        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+        n2 += __shfl_xor_sync(0xffffffffu, n2, o);
+      }
+      const float up = unit_scale(am);
+      uint32_t y[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const __half2 z = __floats2half2_rn(bf_lo(u[k]) * up, bf_hi(u[k]) * up);
+        y[k] = *reinterpret_cast<const uint32_t*>(&z);
+      }
+      if (c < tiles * 8) {
+        *reinterpret_cast<uint4*>(qs + c * QB + 16 * (threadIdx.x % LPC)) = make_uint4(y[0], y[1], y[2], y[3]);
+        if (threadIdx.x % LPC == 0) {
+          const int r = c / a.G, row = c < cols ? r * a.H + c - r * a.G : -1;
+          qsc[c] = tiny(am) ? __int_as_float(0x7fffffff) : (float)(a.scale * 1.4426950408889634) / up;
+          qat[c] = row;
+          if (row >= 0 && blockIdx.z == 0) qnorm_row(a)[(int64_t)t0 * a.H + hk * a.G + row] = sqrtf(n2);
+        }
+      }
+    }
   }
   __syncthreads();
 
   const int64_t pitch2 = select_pitch(a.max_pages) * 2;
   for (int j = j0 + warp * 16; j < j_end; j += kSelThreads / 32 * 16) {
-    fetch(j);
+    cp_async_wait_all();
+    __syncwarp();
+    // A fragments: a lane's four k indices of a step are four consecutive
+    // elements of its rows g and g + 8
     uint32_t hi[D / 16][4], lo[D / 16][4];
     float down[2];
     float am[2] = {0.0f, 0.0f}, n2[2] = {0.0f, 0.0f};
+    const unsigned char* pages_s = stage + g * PR + tg * 16;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
-        const float4 x = v[e][c];
+        const float4 x = *reinterpret_cast<const float4*>(pages_s + 8 * e * PR + 64 * c);
         am[e] = fmaxf(fmax3(am[e], fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
       }
 #pragma unroll
@@ -598,7 +688,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_logits_kernel(const Cach
       down[e] = tiny(am[e]) ? __int_as_float(0x7fffffff) : 1.0f / up;
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
-        const float4 x = v[e][c];
+        const float4 x = *reinterpret_cast<const float4*>(pages_s + 8 * e * PR + 64 * c);
         const float y0 = x.x * up, y1 = x.y * up, y2 = x.z * up, y3 = x.w * up;
         n2[e] += y0 * y0 + y1 * y1 + y2 * y2 + y3 * y3;
         split2(y0, y1, hi[c][e], lo[c][e]);
@@ -613,28 +703,32 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_logits_kernel(const Cach
       for (int e = 0; e < 2; ++e)
         if (j + g + 8 * e < j_end) nr[j + g + 8 * e] = sqrtf(n2[e]) * down[e];
     }
+    __syncwarp();                        // all lanes have read: the next batch may come
+    fetch(j + kSelThreads / 32 * 16);
+    page_ids(j + 2 * (kSelThreads / 32 * 16));
     float* out = reinterpret_cast<float*>(logit_row(a, t0, hk * a.G)) + j + g;
     for (int ct = 0; ct < tiles; ++ct) {
       float sum[4] = {0.f, 0.f, 0.f, 0.f}, cl[4] = {0.f, 0.f, 0.f, 0.f};
       const unsigned char* q = qs + (ct * 8 + g) * QB + 8 * tg;
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        const uint2 b = *reinterpret_cast<const uint2*>(q + 32 * c);
+      for (int c = 0; c < D / 16; c += 2) {
+        const uint2 b0 = *reinterpret_cast<const uint2*>(q + 32 * c);
+        const uint2 b1 = *reinterpret_cast<const uint2*>(q + 32 * c + 32);
         float ch[4] = {0.f, 0.f, 0.f, 0.f};
-        hmma(ch, hi[c], b.x, b.y);
-        hmma(cl, lo[c], b.x, b.y);
+        hmma(ch, hi[c], b0.x, b0.y);
+        hmma(cl, lo[c], b0.x, b0.y);
+        hmma(ch, hi[c + 1], b1.x, b1.y);
+        hmma(cl, lo[c + 1], b1.x, b1.y);
 #pragma unroll
         for (int u = 0; u < 4; ++u) sum[u] += ch[u];
       }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int c = ct * 8 + 2 * tg + u;
-        if (c >= cols) continue;
-        const int r = c / a.G;
+        const int c = ct * 8 + 2 * tg + u, row = qat[c];
         const float f = qsc[c];
-        float* o = out + ((int64_t)r * a.H + (c - r * a.G)) * pitch2;
-        if (j + g < j_end) o[0] = (sum[u] + cl[u]) * (down[0] * f);
-        if (j + g + 8 < j_end) o[8] = (sum[u + 2] + cl[u + 2]) * (down[1] * f);
+        float* o = out + (int64_t)row * pitch2;
+        if (row >= 0 && j + g < j_end) o[0] = (sum[u] + cl[u]) * (down[0] * f);
+        if (row >= 0 && j + g + 8 < j_end) o[8] = (sum[u + 2] + cl[u + 2]) * (down[1] * f);
       }
     }
   }
@@ -687,8 +781,12 @@ struct Group {
 // so one barrier each is enough.
 struct ExactSmem {
   double red[2][kSelThreads / 32];
-  int cnt[2][kSelThreads / 32];
+  int cnt[2][kSelThreads / 32][4];
   uint32_t keep[kMaxSelectPages / 32];
+  int key[kSelThreads];                // upper words of the threads' greatest masses
+  double cand[kSelThreads];            // candidates and their pages
+  int cand_j[kSelThreads];
+  int cut, n_cand;
 };
 struct Block64 {
   ExactSmem& sm;
@@ -705,22 +803,26 @@ struct Block64 {
     for (int w = 1; w < kSelThreads / 32; ++w) x = op(x, r[w]);
     return x;
   }
-  __device__ __forceinline__ int count(int x) {
-    x = __reduce_add_sync(0xffffffffu, x);
-    int* r = sm.cnt[turn ^= 1];
-    if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = x;
-    __syncthreads();
-    x = 0;
+  __device__ __forceinline__ void count(int (&x)[3]) {
+    int (*r)[4] = sm.cnt[turn ^= 1];
 #pragma unroll
-    for (int w = 0; w < kSelThreads / 32; ++w) x += r[w];
-    return x;
+    for (int k = 0; k < 3; ++k) {
+      x[k] = __reduce_add_sync(0xffffffffu, x[k]);
+      if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5][k] = x[k];
+    }
+    __syncthreads();
+    x[0] = x[1] = x[2] = 0;
+#pragma unroll
+    for (int w = 0; w < kSelThreads / 32; ++w)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) x[k] += r[w][k];
   }
 };
 
 // The choice of one item from its fp64 logits, by the whole block; E pages a
 // thread (page r.c0 + tid + 256 i).
 template <int E>
-__device__ __forceinline__ void choose64(const CacheArgs& a, int t, int hk, ExactSmem& sm) {
+__device__ __noinline__ void choose64(const CacheArgs& a, int t, int hk, ExactSmem& sm) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const RowPages r = row_pages(a, t, row_seq(a, t));
   int* sel = a.sel + ((int64_t)t * a.Hkv + hk) * a.n_select;
@@ -734,15 +836,28 @@ __device__ __forceinline__ void choose64(const CacheArgs& a, int t, int hk, Exac
   double mass[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) mass[i] = 0.0;
+  constexpr int R = E <= 8 ? E : 1;                // logits kept in registers, the next head's too
+  double nx[R];
+  if (E <= 8) {
+    const double* l = logit_row(a, t, hk * a.G) + r.c0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) nx[i] = tid + kSelThreads * i < nc ? l[tid + kSelThreads * i] : -kInf64();
+  }
   for (int gq = 0; gq < a.G; ++gq) {
     const double* l = logit_row(a, t, hk * a.G + gq) + r.c0;
-    constexpr int R = E <= 8 ? E : 1;              // logits kept in registers
     double x[R], mx = -kInf64();
+    if (E <= 8) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        x[i] = nx[i];
+        if (gq + 1 < a.G && tid + kSelThreads * i < nc)
+          nx[i] = l[select_pitch(a.max_pages) + tid + kSelThreads * i];
+      }
+    }
 #pragma unroll(E <= 8 ? E : 4)
     for (int i = 0; i < E; ++i) {
       const int j = tid + kSelThreads * i;
-      const double y = j < nc ? l[j] : -kInf64();
-      if (E <= 8) x[i % R] = y;
+      const double y = E <= 8 ? x[i % R] : (j < nc ? l[j] : -kInf64());
       if (isfinite(y)) mx = fmax(mx, y);
     }
     mx = blk.reduce(mx, larger);
@@ -769,68 +884,139 @@ __device__ __forceinline__ void choose64(const CacheArgs& a, int t, int hk, Exac
     }
   }
 
-  // ---- the want-th greatest mass, by bisection on the bits (masses are not
-  // negative, so their bits order as they do) ----
-  double top = 0.0;
+  double top = -1.0;
 #pragma unroll
   for (int i = 0; i < E; ++i) {
-    top = fmax(top, mass[i]);
     if (tid + kSelThreads * i >= nc) mass[i] = -1.0;
+    top = fmax(top, mass[i]);
   }
-  top = blk.reduce(top, larger);
-  long long lo = 0, hi = __double_as_longlong(top) + 1;   // count(>= lo) > want > count(>= hi)
-  int above = 0;                                          // count(>= hi)
-  while (hi - lo > 1) {
-    const long long mid = lo + ((hi - lo) >> 1);
-    int n = 0;
+  const int words = (nc + 31) / 32;
+  for (int w = tid; w < words; w += kSelThreads) sm.keep[w] = 0;
+  // ---- candidates: a value that `want` of the threads' greatest masses reach
+  // (in their upper words, which order as they do: masses are not negative),
+  // and hardly more, is one that everything kept reaches ----
+  sm.key[tid] = __double2hiint(top);
+  if (tid == 0) sm.n_cand = 0;
+  __syncthreads();
+  if (warp == 0) {
+    int k[8];
 #pragma unroll
-    for (int i = 0; i < E; ++i) n += __double_as_longlong(mass[i]) >= mid;
-    n = blk.count(n);
-    if (n == want) {
-      lo = hi = mid;
-      above = want;
-      break;
+    for (int i = 0; i < 8; ++i) k[i] = sm.key[lane + 32 * i];
+    int hi = k[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) hi = max(hi, k[i]);
+    hi = __reduce_max_sync(0xffffffffu, hi) + 1;
+    int lo = 0;
+    while (hi - lo > 1) {
+      const int mid = lo + ((hi - lo) >> 1);
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) n += k[i] >= mid;
+      n = __reduce_add_sync(0xffffffffu, n);
+      if (n >= want) lo = mid; else hi = mid;
+      if (n >= want && n <= want + 16) break;
     }
-    if (n > want) {
-      lo = mid;
-    } else {
-      hi = mid;
-      above = n;
-    }
+    if (lane == 0) sm.cut = lo;
   }
-  // kept: every mass >= hi, and of those equal to lo (ties) the first ones
-  int ties = want - above;
-#pragma unroll 1
+  __syncthreads();
+  const int cut = sm.cut;
+#pragma unroll 8
   for (int i = 0; i < E; ++i) {
-    const int first = kSelThreads * i;
-    if (first >= nc) break;
-    long long b = -1;
-#pragma unroll
-    for (int k = 0; k < E; ++k)
-      if (k == i) b = __double_as_longlong(mass[k]);
-    bool keep = b >= hi;
-    if (ties > 0) {                                       // uniform
-      const bool eq = b == lo && b < hi;
-      const uint32_t be = __ballot_sync(0xffffffffu, eq);
-      int* r2 = sm.cnt[blk.turn ^= 1];
-      if (lane == 0) r2[warp] = __popc(be);
-      __syncthreads();
-      int before = 0, all = 0;
-#pragma unroll
-      for (int w = 0; w < kSelThreads / 32; ++w) {
-        if (w < warp) before += r2[w];
-        all += r2[w];
+    const bool in = __double2hiint(mass[i]) >= cut;
+    const uint32_t b = __ballot_sync(0xffffffffu, in);
+    if (b) {
+      int at = 0;
+      if (lane == 0) at = atomicAdd(&sm.n_cand, __popc(b));
+      at = __shfl_sync(0xffffffffu, at, 0) + __popc(b & ((1u << lane) - 1));
+      if (in && at < kSelThreads) {
+        sm.cand[at] = mass[i];
+        sm.cand_j[at] = tid + kSelThreads * i;
       }
-      keep |= eq && before + __popc(be & ((1u << lane) - 1)) < ties;
-      ties -= min(ties, all);
     }
-    const uint32_t bk = __ballot_sync(0xffffffffu, keep);
-    if (lane == 0) sm.keep[i * (kSelThreads / 32) + warp] = bk;
+  }
+  __syncthreads();
+  const int n_cand = sm.n_cand;
+  if (n_cand >= want && n_cand <= kSelThreads) {
+    // a candidate's rank by (-mass, page) settles it (whatever the order in
+    // which the candidates came)
+    if (tid < n_cand) {
+      const double m = sm.cand[tid];
+      const int j = sm.cand_j[tid];
+      int rank = 0;
+      for (int k = 0; k < n_cand; ++k) rank += sm.cand[k] > m || (sm.cand[k] == m && sm.cand_j[k] < j);
+      if (rank < want) atomicOr(&sm.keep[j >> 5], 1u << (j & 31));
+    }
+  } else {
+    // too many to rank (more than 256 places, or many equal masses): the
+    // want-th greatest mass, by bisection on the bits
+    top = blk.reduce(top, larger);
+    long long lo = 0, hi = __double_as_longlong(top) + 1;   // count(>= lo) > want > count(>= hi)
+    int above = 0;                                          // count(>= hi)
+    while (hi - lo > 1) {
+      // three cuts a pass: a barrier costs more than the comparisons
+      const long long step = max((hi - lo) >> 2, 1ll);
+      int n[3] = {0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const long long b = __double_as_longlong(mass[i]);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) n[k] += b >= lo + (k + 1) * step;
+      }
+      blk.count(n);
+      bool done = false;
+      long long nlo = lo, nhi = hi;
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const long long cut = lo + (k + 1) * step;
+        if (cut >= hi || done) continue;
+        if (n[k] == want) {
+          nlo = nhi = cut;
+          above = want;
+          done = true;
+        } else if (n[k] > want) {
+          nlo = cut;
+        } else if (cut < nhi) {
+          nhi = cut;
+          above = n[k];
+        }
+      }
+      lo = nlo;
+      hi = nhi;
+    }
+    // kept: every mass >= hi, and of those equal to lo (ties) the first ones
+    int ties = want - above;
+#pragma unroll 1
+    for (int i = 0; i < E; ++i) {
+      const int first = kSelThreads * i;
+      if (first >= nc) break;
+      long long b = -1;
+#pragma unroll
+      for (int k = 0; k < E; ++k)
+        if (k == i) b = __double_as_longlong(mass[k]);
+      bool keep = b >= hi;
+      if (ties > 0) {                                       // uniform
+        const bool eq = b == lo && b < hi;
+        const uint32_t be = __ballot_sync(0xffffffffu, eq);
+        int (*r2)[4] = sm.cnt[blk.turn ^= 1];
+        if (lane == 0) r2[warp][0] = __popc(be);
+        __syncthreads();
+        int before = 0, all = 0;
+#pragma unroll
+        for (int w = 0; w < kSelThreads / 32; ++w) {
+          if (w < warp) before += r2[w][0];
+          all += r2[w][0];
+        }
+        keep |= eq && before + __popc(be & ((1u << lane) - 1)) < ties;
+        ties -= min(ties, all);
+      }
+      const uint32_t bk = __ballot_sync(0xffffffffu, keep);
+      if (lane == 0) sm.keep[i * (kSelThreads / 32) + warp] = bk;
+    }
   }
   __syncthreads();
   // ---- the list, in page order ----
   if (warp == 0) {
-    const int words = (nc + 31) / 32, per = (words + 31) / 32;
+    const int per = (words + 31) / 32;
     int n = 0;
     for (int k = 0; k < per; ++k)
       if (lane * per + k < words) n += __popc(sm.keep[lane * per + k]);
@@ -879,7 +1065,7 @@ __global__ void __launch_bounds__(kSelThreads) cache_choose64_kernel(const Cache
 // fp64 logits of one item by the whole block, into the item's scratch rows.
 template <int D>
 __device__ __noinline__ void logits64_item(const CacheArgs& a, int t, int hk, double* qs) {
-  constexpr int QP = D + 4;
+  constexpr int QP = D + 8;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tg = lane & 3;
   const int s = row_seq(a, t);
   const RowPages r = row_pages(a, t, s);
@@ -887,7 +1073,7 @@ __device__ __noinline__ void logits64_item(const CacheArgs& a, int t, int hk, do
     __syncthreads();
     for (int i = tid; i < 8 * D; i += kSelThreads) {
       const int c = i / D, d = i - c * D;
-      qs[c * QP + d] = g0 + c < a.G ? (double)__bfloat162float(a.q[(int64_t)t * a.sq_t + (int64_t)(hk * a.G + g0 + c) * a.sq_h + d]) : 0.0;
+      qs[c * QP + q_slot(d)] = g0 + c < a.G ? (double)__bfloat162float(a.q[(int64_t)t * a.sq_t + (int64_t)(hk * a.G + g0 + c) * a.sq_h + d]) : 0.0;
     }
     __syncthreads();
     for (int j = r.c0 + warp * 8; j < r.c1; j += kSelThreads / 32 * 8) {
@@ -896,22 +1082,22 @@ __device__ __noinline__ void logits64_item(const CacheArgs& a, int t, int hk, do
       float4 v[D / 16];
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) v[i] = page >= 0 ? __ldg(src + 4 * i + tg) : make_float4(0.f, 0.f, 0.f, 0.f);
-      double c0[2] = {0.0, 0.0}, c1[2] = {0.0, 0.0};
+      double c0[2] = {0.0, 0.0}, c1[2] = {0.0, 0.0}, c2[2] = {0.0, 0.0}, c3[2] = {0.0, 0.0};
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
-        const double* q = qs + g * QP + 4 * tg + 16 * i;
+        const double* q = qs + g * QP + 2 * tg + 16 * i;
         const double2 x = *reinterpret_cast<const double2*>(q);
-        const double2 y = *reinterpret_cast<const double2*>(q + 2);
+        const double2 y = *reinterpret_cast<const double2*>(q + 8);
         dmma(c0, v[i].x, x.x);
         dmma(c1, v[i].y, x.y);
-        dmma(c0, v[i].z, y.x);
-        dmma(c1, v[i].w, y.y);
+        dmma(c2, v[i].z, y.x);
+        dmma(c3, v[i].w, y.y);
       }
       if (j + g < r.c1) {
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           if (g0 + 2 * tg + e < a.G)
-            logit_row(a, t, hk * a.G + g0 + 2 * tg + e)[j + g] = page < 0 ? -kInf64() : (c0[e] + c1[e]) * a.scale;
+            logit_row(a, t, hk * a.G + g0 + 2 * tg + e)[j + g] = page < 0 ? -kInf64() : ((c0[e] + c1[e]) + (c2[e] + c3[e])) * a.scale;
       }
     }
   }
@@ -922,11 +1108,12 @@ __device__ __noinline__ void logits64_item(const CacheArgs& a, int t, int hk, do
 // pages; a block has 8 / WPI items.
 template <int D, int WPI, int E>
 __global__ void __launch_bounds__(kSelThreads) cache_choose_kernel(const CacheArgs a) {
-  __shared__ double qs[8 * (D + 4)];
+  __shared__ __align__(16) double qs[8 * (D + 8)];
   __shared__ ExactSmem sm;
   __shared__ float red[kSelThreads / 32];
   __shared__ uint32_t bits[WPI > 1 ? WPI * E : 1];
   __shared__ int todo[8 / WPI];
+  __shared__ float few_mass[WPI == 1 ? 8 : 1][64];
   constexpr int IPB = 8 / WPI, GS = 32 * WPI;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int lid = WPI == 1 ? lane : threadIdx.x;           // thread of the item
@@ -944,32 +1131,32 @@ __global__ void __launch_bounds__(kSelThreads) cache_choose_kernel(const CacheAr
       float mass[E];
 #pragma unroll
       for (int i = 0; i < E; ++i) mass[i] = 0.0f;
+      // thread's pages lid + GS i, i < mine
+      const int mine_n = lid < nc ? (nc - lid + GS - 1) / GS : 0;
       float kn = 0.0f, qn = 0.0f;
-      const float* nr = norm_row(a, s, hk) + r.c0;
+      const float* nr = norm_row(a, s, hk) + r.c0 + lid;
 #pragma unroll
       for (int i = 0; i < E; ++i)
-        if (lid + GS * i < nc) kn = fmaxf(kn, nr[lid + GS * i]);
+        if (i < mine_n) kn = fmaxf(kn, nr[GS * i]);
+      kn = grp.max(kn);
       bool bad = false;
+      const int64_t lstep = select_pitch(a.max_pages) * 2;
+      const float* l = reinterpret_cast<const float*>(logit_row(a, t, hk * a.G)) + r.c0 + lid;
+      float nx[E];                                         // the next head's logits
+#pragma unroll
+      for (int i = 0; i < E; ++i) nx[i] = i < mine_n ? l[GS * i] : -kInf;
       for (int gq = 0; gq < a.G; ++gq) {
-        const __nv_bfloat16* q = a.q + (int64_t)t * a.sq_t + (int64_t)(hk * a.G + gq) * a.sq_h + (D / 32) * lane;
-        float q2 = 0.0f;
-#pragma unroll
-        for (int i = 0; i < D / 32; i += 2) {
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(q + i);
-          q2 += bf_lo(w) * bf_lo(w) + bf_hi(w) * bf_hi(w);
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) q2 += __shfl_xor_sync(0xffffffffu, q2, o);
-        qn = fmaxf(qn, q2);
-        const float* l = reinterpret_cast<const float*>(logit_row(a, t, hk * a.G + gq)) + r.c0;
+        qn = fmaxf(qn, qnorm_row(a)[(int64_t)t * a.H + hk * a.G + gq]);
         float x[E], mx = -kInf;
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-          const bool in = lid + GS * i < nc;
-          x[i] = in ? l[lid + GS * i] : -kInf;
-          bad |= in && !(fabsf(x[i]) < kInf);
-          mx = fmaxf(mx, x[i]);
+        for (int i = 0; i < E; ++i) x[i] = nx[i];
+        if (gq + 1 < a.G) {
+          l += lstep;
+#pragma unroll
+          for (int i = 0; i < E; ++i) nx[i] = i < mine_n ? l[GS * i] : -kInf;
         }
+#pragma unroll
+        for (int i = 0; i < E; ++i) mx = fmaxf(mx, x[i]);
         mx = grp.max(mx);
         float sum = 0.0f;
 #pragma unroll
@@ -977,29 +1164,66 @@ __global__ void __launch_bounds__(kSelThreads) cache_choose_kernel(const CacheAr
           asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x[i]) : "f"(x[i] - mx));
           sum += x[i];
         }
-        const float inv = 1.0f / grp.sum(sum);
+        sum = grp.sum(sum);
+        bad |= !(sum >= 0.5f && mx < kInf);                // a logit that is not finite
+        const float inv = 1.0f / sum;
 #pragma unroll
         for (int i = 0; i < E; ++i) mass[i] = fmaf(x[i], inv, mass[i]);
       }
+      bad |= !(kn * qn < kInf);                            // (all of these uniform)
+      float top = -1.0f;
 #pragma unroll
-      for (int i = 0; i < E; ++i)
-        if (lid + GS * i >= nc) mass[i] = -1.0f;
-      kn = grp.max(kn);
-      bad |= !(kn * qn < kInf);
-      // a float that `want` masses reach and the others do not, by bisection
-      // on the bits
-      float top = mass[0];
-#pragma unroll
-      for (int i = 1; i < E; ++i) top = fmaxf(top, mass[i]);
-      top = grp.max(top);
-      int lo = 0, hi = __float_as_int(top) + 1;            // count(>= lo) > want > count(>= hi)
+      for (int i = 0; i < E; ++i) {
+        if (i >= mine_n) mass[i] = -1.0f;
+        top = fmaxf(top, mass[i]);
+      }
+      // a float that `want` masses reach and the others do not: by bisection
+      // on the bits; count(>= lo) >= want >= count(>= hi)
       int cut = -1;
-      if (grp.count(bad) == 0) {
-        while (hi - lo > 1) {
+      if (!bad) {
+        int lo = 0, hi;
+        bool few = false;                                  // only few masses lie above lo
+        if (WPI == 1 && want <= 32) {
+          // the want-th greatest of the lanes' greatest: it and everything
+          // above it are `want` masses or more, and hardly more
+          int up = __float_as_int(__uint_as_float(__reduce_max_sync(0xffffffffu, max(__float_as_int(top), 0)))) + 1;
+          hi = up;
+          while (up - lo > 1) {
+            const int mid = lo + ((up - lo) >> 1);
+            const int n = __popc(__ballot_sync(0xffffffffu, __float_as_int(top) >= mid));
+            if (n >= want) lo = mid; else up = mid;
+            if (n == want) break;
+          }
+          // its survivors, up to two a lane
+          int n = 0;
+#pragma unroll
+          for (int i = 0; i < E; ++i) {
+            const uint32_t b = __ballot_sync(0xffffffffu, __float_as_int(mass[i]) >= lo);
+            const int at = n + __popc(b & ((1u << lane) - 1));
+            if (__float_as_int(mass[i]) >= lo && at < 64) few_mass[warp][at] = mass[i];
+            n += __popc(b);
+          }
+          few = n <= 64;
+          if (few) {
+            __syncwarp();
+            const int m0 = lane < n ? __float_as_int(few_mass[warp][lane]) : -1;
+            const int m1 = lane + 32 < n ? __float_as_int(few_mass[warp][lane + 32]) : -1;
+            if (n == want) cut = lo;
+            while (cut < 0 && hi - lo > 1) {
+              const int mid = lo + ((hi - lo) >> 1);
+              const int k = __popc(__ballot_sync(0xffffffffu, m0 >= mid)) + __popc(__ballot_sync(0xffffffffu, m1 >= mid));
+              if (k == want) cut = mid;
+              if (k > want) lo = mid; else hi = mid;
+            }
+          }
+        } else {
+          hi = __float_as_int(grp.max(top)) + 1;
+        }
+        while (!few && hi - lo > 1) {
           const int mid = lo + ((hi - lo) >> 1);
           int n = 0;
 #pragma unroll
-          for (int i = 0; i < E; ++i) n += mass[i] >= __int_as_float(mid);
+          for (int i = 0; i < E; ++i) n += __float_as_int(mass[i]) >= mid;
           n = grp.count(n);
           if (n == want) {
             cut = mid;
@@ -1022,7 +1246,7 @@ __global__ void __launch_bounds__(kSelThreads) cache_choose_kernel(const CacheAr
         // relative error of a mass: the logits' error in the exponent of the
         // term and of the sum, ex2 and its argument (near the border up to
         // ln(1 / mass) below the maximum), and the sums' roundings
-        const float delta = kLogitErr * (float)a.scale * sqrtf(qn) * kn;
+        const float delta = kLogitErr * (float)a.scale * qn * kn;
         const float err = 2.0f * delta + 1.2e-7f * (float)(E + 26 + a.G) + 4.8e-7f * (8.0f - logf(fmaxf(out, 1e-37f)));
         again = !(delta < 0.05f) || !(in * (1.0f - 1.1f * err) > out * (1.0f + 1.1f * err));
         if (!again) {
@@ -1121,7 +1345,7 @@ static cudaError_t select_d(const CacheArgs& a, cudaStream_t s) {
   while (pages > 2 * step && tiles * a.Hkv * ((a.max_pages + pages - 1) / pages) < 4ll * sms)
     pages = (pages / 2 + step - 1) / step * step;
   const dim3 grid((unsigned)tiles, a.Hkv, (a.max_pages + pages - 1) / pages);
-  const int lb = fast ? cols * (D * 2 + 16 + 4) : cols * (D + 4) * 8;
+  const int lb = fast ? logits_stage_off<D>(cols) + kSelThreads / 32 * 16 * (D * 4 + 64) : (cols + 3) / 4 * 4 * D * 8 + kSelThreads / 32 * 16 * D * 4;
   static OncePerDevice once_f, once_d;
   auto go = [&](auto kernel, OncePerDevice& once) {
     if (lb > 48 * 1024) {

@@ -35,7 +35,8 @@ ta_status validate(const ta_cache_params* p) {
 
 size_t scratch_bytes(const ta_cache_params* p) {
   if (p->n_select <= 0) return 0;
-  return (size_t)ta::select_pitch(p->max_pages) * ((size_t)p->T * p->H * 8 + (size_t)p->S * p->Hkv * 4);
+  return (size_t)ta::select_pitch(p->max_pages) * ((size_t)p->T * p->H * 8 + (size_t)p->S * p->Hkv * 4) +
+         (size_t)p->T * p->H * 4;
 }
 
 ta_status check_ws(const void* ws, size_t have, size_t need) {
