@@ -350,18 +350,19 @@ __global__ void __launch_bounds__(kAppendThreads, 4) cache_append_kernel(const C
 // products with an fp32 sum and a bound of their error; where the last page
 // that is in and the first that is out lie further apart than the bound, the
 // set is the one that fp64 would find, whatever the rounding.  The other rows
-// (about one in a hundred on random means, and ties) are done again in fp64
-// by the block that found them.
+// (about one in a hundred on random means, and ties) are listed and done again
+// in fp64.
 //
 // The error: a page's mean is scaled by a power of two to f16's range and
 // split into two f16 parts (22 bits of each element), the query scaled the same
 // way (its 8 bits are exact down to 2^-14 of its largest element); what is cut
-// off is at most 2^-21 of |q| |kbar|.  Each 32 products go into a sum of their
-// own, where an addend may lose 2^-24 of the largest: 2^-19 in all; these sums
-// add up in fp32, 2^-22.  2^-18.5 scale |q| |kbar| covers them.
+// off is at most 2^-21 of |q| |kbar|.  64 products each go into a sum of their
+// own, 16 at a time with what the sum was, and an addend may lose 2^-24 of the
+// largest: 4 * 17 * 2^-24 < 2^-17.9 in all.  2^-17.7 scale |q| |kbar| covers
+// both with fp32's few roundings.
 constexpr int kSelThreads = 256;
-constexpr int kSelCols = 64;           // (row, head) columns of a logits block
-constexpr float kLogitErr = 2.7e-6f;   // 2^-18.5
+constexpr int kSelCols = 128;          // (row, head) columns of a fast logits block
+constexpr float kLogitErr = 4.7e-6f;   // 2^-17.7
 constexpr float kInf = 3.0e38f;        // a logit above is taken as not finite
 
 // Pages that row t sees, and the pages [c0, c1) that compete for it.
@@ -377,33 +378,38 @@ __device__ __forceinline__ RowPages row_pages(const CacheArgs& a, int t, int s) 
   return r;
 }
 
-// Scratch: for each (row, query head) `pitch` doubles, of which the fp32
-// logits (in log2 units) take the first half until the row is done in fp64;
-// then, for each (sequence, key head), the pages' norms,
+// Scratch.  For each (row, query head) `pitch` doubles, of which the fp32
+// logits (in log2 units) take the first half until the row is done in fp64.
+// For the fast logits also: for each (sequence, key head) the split tiles, the
+// pages' norms and the powers of two that undo their scaling; the queries'
+// norms; for each row its sequence and number of pages; the list of items that
+// fp64 has to decide.
 __device__ __forceinline__ double* logit_row(const CacheArgs& a, int t, int h) {
   return a.scratch + ((int64_t)t * a.H + h) * select_pitch(a.max_pages);
 }
+__device__ __forceinline__ unsigned char* split_tile(const CacheArgs& a, int s, int hk, int jb, int bytes) {
+  return reinterpret_cast<unsigned char*>(a.scratch + (int64_t)a.T * a.H * select_pitch(a.max_pages)) +
+         (((int64_t)s * a.Hkv + hk) * (select_pitch(a.max_pages) / 128) + jb) * bytes;
+}
 __device__ __forceinline__ float* norm_row(const CacheArgs& a, int s, int hk) {
-  return reinterpret_cast<float*>(a.scratch + (int64_t)a.T * a.H * select_pitch(a.max_pages)) +
-         ((int64_t)s * a.Hkv + hk) * select_pitch(a.max_pages);
+  return reinterpret_cast<float*>(split_tile(a, a.S, 0, 0, 512 * a.d)) + ((int64_t)s * a.Hkv + hk) * select_pitch(a.max_pages);
+}
+__device__ __forceinline__ float* down_row(const CacheArgs& a, int s, int hk) {
+  return norm_row(a, a.S + s, hk);
+}
+__device__ __forceinline__ float* qnorm_row(const CacheArgs& a) { return norm_row(a, 2 * a.S, 0); }
+__device__ __forceinline__ int2* row_info(const CacheArgs& a) {
+  return reinterpret_cast<int2*>(qnorm_row(a) + (int64_t)(a.T + (a.T & 1)) * a.H);
 }
 
-// and, for each (row, query head), the query's norm.
-__device__ __forceinline__ float* qnorm_row(const CacheArgs& a) {
-  return norm_row(a, a.S, 0);
-}
+// Items (row, key head) that fp64 has to decide, and how many.
+__device__ __forceinline__ int2* again_list(const CacheArgs& a) { return row_info(a) + a.T + (a.T & 1) + 2; }
+__device__ __forceinline__ int* again_count(const CacheArgs& a) { return reinterpret_cast<int*>(again_list(a) - 1); }
 
 __device__ __forceinline__ void dmma(double (&c)[2], double a, double b) {
   asm volatile("mma.sync.aligned.m8n8k4.row.col.f64.f64.f64.f64 {%0, %1}, {%2}, {%3}, {%0, %1};"
                : "+d"(c[0]), "+d"(c[1])
                : "d"(a), "d"(b));
-}
-__device__ __forceinline__ void hmma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // Two floats as f16 parts: x = hi + lo + (at most 2^-22 |x|, or 2^-25).
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
@@ -559,179 +565,269 @@ __global__ void __launch_bounds__(kSelThreads, 3) cache_logits64_kernel(const Ca
   }
 }
 
-// Shared memory of the fast logits: queries (f16, padded columns), their
-// scales and rows, and 16 pages for each warp.
+// ---- fast logits ----
+// A first kernel writes the means as tiles of 128 pages in the layout that
+// the matrix instruction reads from shared memory (rows of 64 f16 elements,
+// 128-byte swizzle): the leading parts, then the rest.
 template <int D>
-__host__ __device__ constexpr int logits_stage_off(int cols) {
-  return ((cols + 7) / 8 * 8 * (D * 2 + 32 + 8) + 15) / 16 * 16;
+struct SplitTile {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kHalf = 128 * 128;          // bytes of 128 rows by 64 elements
+  static constexpr int kPart = kHalves * kHalf;
+  static constexpr int kBytes = 2 * kPart;
+};
+
+// Last page + 1 that any row of sequence s lets compete, 0 where no row has a
+// choice to make.
+__device__ __forceinline__ int pages_competing(const CacheArgs& a, int s) {
+  const int t = min(a.cu[s + 1], rows_used(a)) - 1;
+  if (t < max(a.cu[s], 0)) return 0;
+  const RowPages r = row_pages(a, t, s);
+  return r.n <= a.n_select ? 0 : r.c1;
 }
 
-// fp32 logits (in log2 units) of a tile of many rows: a warp takes 16 pages
-// at a time and all columns of the tile.
 template <int D>
-__global__ void __launch_bounds__(kSelThreads, 2) cache_logits_kernel(const CacheArgs a, int tile_rows,
-                                                                      int pages) {
-  extern __shared__ __align__(16) unsigned char sel_smem[];
-  constexpr int QB = D * 2 + 32;       // bytes of a column, padded against bank conflicts
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tg = lane & 3;
+__global__ void __launch_bounds__(kSelThreads) cache_split_kernel(const CacheArgs a) {
+  using T = SplitTile<D>;
+  constexpr int E = D / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int jb = blockIdx.x / 4, hk = blockIdx.y, s = blockIdx.z;
+  if (blockIdx.x == 0 && hk == 0 && s == 0 && threadIdx.x == 0) *again_count(a) = 0;
+  const int end = pages_competing(a, s);
+  if ((int)blockIdx.x * 32 >= end) return;
+  unsigned char* tile = split_tile(a, s, hk, jb, T::kBytes);
+  float* down = down_row(a, s, hk) + jb * 128;
+  float* norm = norm_row(a, s, hk) + jb * 128;
+  const int row0 = (blockIdx.x & 3) * 32 + warp * 4;
+  int ids = -1;                                    // lane l < 4: the warp's page l
+  {
+    const int j = jb * 128 + row0 + lane;
+    if (lane < 4 && j < end && j >= a.n_first) ids = page_of(a, s, j);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = row0 + i, page = __shfl_sync(0xffffffffu, ids, i);
+    float x[E];
+    const float* src = a.k_mean + ((int64_t)max(page, 0) * a.Hkv + hk) * D + E * lane;
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = page >= 0 ? __ldg(src + e) : __int_as_float(0x7fffffff);
+    float am = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) am = fmaxf(am, fabsf(x[e]));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+    const float up = unit_scale(am);
+    float n2 = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      x[e] *= up;
+      n2 += x[e] * x[e];
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) n2 += __shfl_xor_sync(0xffffffffu, n2, o);
+    if (lane == 0) {
+      down[row] = tiny(am) ? __int_as_float(0x7fffffff) : 1.0f / up;
+      norm[row] = sqrtf(n2) / up;
+    }
+    const int d = E * lane, half = d / 64, chunk = (d % 64) / 8;
+    unsigned char* at = tile + half * T::kHalf + row * 128 + ((chunk ^ (row & 7)) << 4) + (d % 8) * 2;
+    uint32_t hi[E / 2], lo[E / 2];
+#pragma unroll
+    for (int e = 0; e < E; e += 2) split2(x[e], x[e + 1], hi[e / 2], lo[e / 2]);
+    if constexpr (E == 4) {
+      *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(at + T::kPart) = make_uint2(lo[0], lo[1]);
+    } else {
+      *reinterpret_cast<uint32_t*>(at) = hi[0];
+      *reinterpret_cast<uint32_t*>(at + T::kPart) = lo[0];
+    }
+  }
+}
+
+// fp32 logits (in log2 units) of a tile of many rows: pages are the 128 rows of
+// tcgen05.mma, the tile's (row, query head) columns its N = 128, so that a
+// thread of the epilogue has one page and neighbouring threads write
+// neighbouring logits.  Two sums of 64 elements each stand in TMEM (the rest
+// parts' products go first, into the first of them); two blocks share an SM,
+// one multiplying or loading while the other writes.
+template <int D>
+struct LogitsSmem {
+  static constexpr int oA = 0;
+  static constexpr int oB = SplitTile<D>::kBytes;
+  static constexpr int oCol = oB + SplitTile<D>::kPart;      // scale and logit row of each column
+  static constexpr int oBar = oCol + kSelCols * 8;
+  static constexpr int kBytes = oBar + 64 + 1024;            // 1024 to align
+  static constexpr int kCols = (D / 64) * kSelCols;          // TMEM columns
+};
+
+template <int D>
+__global__ void __launch_bounds__(288, 2) cache_logits_kernel(const CacheArgs a, int tile_rows) {
+  using T = SplitTile<D>;
+  using L = LogitsSmem<D>;
+  extern __shared__ unsigned char sel_raw[];
+  unsigned char* smem = sel_raw + ((1024 - (smem_u32(sel_raw) & 1023)) & 1023);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hk = blockIdx.y;
   const RowTile tile = row_tile(a, blockIdx.x, tile_rows);
   const int s = tile.s, t0 = tile.t0, t1 = tile.t1;
   if (t0 >= t1) return;
+  if (hk == 0)
+    for (int t = t0 + threadIdx.x; t < t1; t += 288) row_info(a)[t] = make_int2(s, row_pages(a, t, s).n);
   const RowPages last = row_pages(a, t1 - 1, s);   // the tile's longest row
-  const int j0 = blockIdx.z * pages;
-  const int j_end = min(last.c1, j0 + pages);
-  if (j0 >= j_end || j_end <= a.n_first || last.n <= a.n_select) return;
-  const int cols = (t1 - t0) * a.G, tiles = (cols + 7) / 8;
-  unsigned char* qs = sel_smem;                    // f16 queries, [column][D]
-  float* qsc = reinterpret_cast<float*>(sel_smem + ((tile_rows * a.G + 7) / 8 * 8) * QB);
-  int* qat = reinterpret_cast<int*>(qsc) + (tile_rows * a.G + 7) / 8 * 8;   // a column's logit row
+  if (last.n <= a.n_select || last.c1 <= a.n_first) return;
+  const int nb = (last.c1 + 127) / 128;
+  const int cols = (t1 - t0) * a.G;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::oBar);
+  uint64_t *full = bars, *done = bars + 1, *freed = bars + 2;
+  uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 3);
+  int* flag = reinterpret_cast<int*>(bars + 4);
+  const AbortCtx abort{flag, a.status};
+  float2* col = reinterpret_cast<float2*>(smem + L::oCol);   // (scale, row as bits)
 
-  // each warp has its next 16 pages on their way to shared memory while it
-  // multiplies the last ones
-  constexpr int PR = D * 4 + 64;                   // bytes of a page there (half a line off)
-  unsigned char* stage = sel_smem + logits_stage_off<D>(tile_rows * a.G) + warp * (16 * PR);
-  constexpr int CH = D / 4;                        // 16-byte chunks of a page
-  int pg_next = -1;                                // lane l < 16: page l of the next batch
-  auto page_ids = [&](int j) {
-    pg_next = -1;
-    if (lane < 16 && j + lane < j_end && j + lane >= a.n_first) pg_next = page_of(a, s, j + lane);
+  if (threadIdx.x == 0) {
+    mbar_init(full, 1);
+    mbar_init(done, 1);
+    mbar_init(freed, 8);
+    *flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(slot, L::kCols);
+    tmem_relinquish();
+  }
+  auto load = [&](int jb) {            // one thread: the tile of 128 pages, in 16 KB pieces
+    const unsigned char* src = split_tile(a, s, hk, jb, T::kBytes);
+    mbar_arrive_expect_tx(full, T::kBytes);
+    for (int i = 0; i < T::kBytes; i += T::kHalf)
+      asm volatile(
+          "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+              "r"(smem_u32(smem + L::oA + i)),
+          "l"(src + i), "r"(T::kHalf), "r"(smem_u32(full))
+          : "memory");
   };
-  auto fetch = [&](int j) {
-    if (j < j_end) {
-#pragma unroll 4
-      for (int i = 0; i < CH / 2; ++i) {           // 16 pages of CH chunks
-        const int c = i * 32 + lane, p = c / CH, x = c - p * CH;
-        const int page = __shfl_sync(0xffffffffu, pg_next, p);
-        unsigned char* dst = stage + p * PR + x * 16;
-        if (page >= 0)
-          cp_async16(dst, a.k_mean + ((int64_t)page * a.Hkv + hk) * D + x * 4, 16);
-        else
-          *reinterpret_cast<uint4*>(dst) = make_uint4(0x7fffffffu, 0u, 0u, 0u);   // NaN: no such page
-      }
-    }
-  };
-  page_ids(j0 + warp * 16);
-  fetch(j0 + warp * 16);
-  page_ids(j0 + warp * 16 + 128);
-
-  // queries: D / 8 lanes hold a column, 8 elements each
-  constexpr int LPC = D / 8, CPB = kSelThreads / LPC;
+  __syncthreads();
+  if (warp == 8 && lane == 0) load(0);
+  if (warp < 8) {
+    // queries: D / 8 lanes hold a column, 8 elements each
+    constexpr int LPC = D / 8, CPB = 256 / LPC;
+    const int part = threadIdx.x % LPC;
 #pragma unroll 1
-  for (int cb = 0; cb < tiles * 8; cb += 4 * CPB) {
-    uint4 w[4];
+    for (int cb = 0; cb < kSelCols; cb += 4 * CPB) {
+      uint4 w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = cb + i * CPB + threadIdx.x / LPC;
-      w[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (c < cols) {
-        const int r = c / a.G, h = hk * a.G + (c - r * a.G);
-        w[i] = *reinterpret_cast<const uint4*>(a.q + (int64_t)(t0 + r) * a.sq_t + (int64_t)h * a.sq_h + 8 * (threadIdx.x % LPC));
+      for (int i = 0; i < 4; ++i) {
+        const int c = cb + i * CPB + threadIdx.x / LPC;
+        w[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (c < cols) {
+          const int r = c / a.G, h = hk * a.G + (c - r * a.G);
+          w[i] = *reinterpret_cast<const uint4*>(a.q + (int64_t)(t0 + r) * a.sq_t + (int64_t)h * a.sq_h + 8 * part);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = cb + i * CPB + threadIdx.x / LPC;
+        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        float am = 0.0f, n2 = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float x = bf_lo(u[k]), y = bf_hi(u[k]);
+          am = fmax3(am, fabsf(x), fabsf(y));
+          n2 += x * x + y * y;
+        }
+#pragma unroll
+        for (int o = 1; o < LPC; o <<= 1) {
+          am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+          n2 += __shfl_xor_sync(0xffffffffu, n2, o);
+        }
+        const float up = unit_scale(am);
+        uint32_t y[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const __half2 z = __floats2half2_rn(bf_lo(u[k]) * up, bf_hi(u[k]) * up);
+          y[k] = *reinterpret_cast<const uint32_t*>(&z);
+        }
+        *reinterpret_cast<uint4*>(smem + L::oB + (part / 8) * T::kHalf + c * 128 + (((part % 8) ^ (c & 7)) << 4)) =
+            make_uint4(y[0], y[1], y[2], y[3]);
+        if (part == 0) {
+          const int r = c / a.G, row = c < cols ? r * a.H + c - r * a.G : -1;
+          col[c] = make_float2(tiny(am) ? __int_as_float(0x7fffffff) : (float)(a.scale * 1.4426950408889634) / up,
+                               __int_as_float(row));
+          if (row >= 0) qnorm_row(a)[(int64_t)t0 * a.H + hk * a.G + row] = sqrtf(n2);
+        }
       }
     }
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *slot;
+
+  if (warp == 8) {
+    if (lane == 0) {
+      const uint32_t sa = smem_u32(smem + L::oA), sb = smem_u32(smem + L::oB);
+      constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(kSelCols >> 3) << 17) | ((128u >> 4) << 24);   // f16 x f16
+      bool ok = true;
+      int i = 0;
+      for (; i < nb && ok; ++i) {
+        ok = mbar_wait(full, i & 1, abort, 3) && (i == 0 || mbar_wait(freed, (i - 1) & 1, abort, 4));
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = cb + i * CPB + threadIdx.x / LPC;
-      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-      float am = 0.0f, n2 = 0.0f;
+        for (int part = 1; part >= 0; --part)      // the rest parts first
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float x = bf_lo(u[k]), y = bf_hi(u[k]);
-        am = fmax3(am, fabsf(x), fabsf(y));
-        n2 += x * x + y * y;
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t ad = smem_desc_sw128(sa + part * T::kPart + (kk >> 2) * T::kHalf + (kk & 3) * 32, 16, 1024);
+            const uint64_t bd = smem_desc_sw128(sb + (kk >> 2) * T::kHalf + (kk & 3) * 32, 16, 1024);
+            const bool fresh = part ? kk == 0 : (kk >= 4 && (kk & 3) == 0);
+            mma_f16_ss(tmem + (part ? 0 : (kk >> 2) * kSelCols), ad, bd, idesc, fresh ? 0u : 1u);
+          }
+        tc_commit(done);
+        ok = mbar_wait(done, i & 1, abort, 5);
+        if (ok && i + 1 < nb) load(i + 1);
       }
-#pragma unroll
-      for (int o = 1; o < LPC; o <<= 1) {
-        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-        n2 += __shfl_xor_sync(0xffffffffu, n2, o);
+      if (!ok) {
+        // nothing may still be on its way when the block ends
+        mbar_wait_drain(full, i & 1);
+        mbar_wait_drain(done, i & 1);
       }
-      const float up = unit_scale(am);
-      uint32_t y[4];
+    }
+  } else {
+    const int64_t pitch2 = select_pitch(a.max_pages) * 2;
+    const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const int c_lo = (warp >> 2) * 64, c_hi = min(cols, c_lo + 64);   // this warp's columns
+    float* out = reinterpret_cast<float*>(logit_row(a, t0, hk * a.G));
+    for (int i = 0; i < nb; ++i) {
+      const int j = i * 128 + (threadIdx.x & 127);
+      const float down = down_row(a, s, hk)[j];
+      if (!mbar_wait(done, i & 1, abort, 6)) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int c0 = c_lo; c0 < max(c_hi, c_lo + 1); c0 += 32) {
+        uint32_t x[D / 64][32];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const __half2 z = __floats2half2_rn(bf_lo(u[k]) * up, bf_hi(u[k]) * up);
-        y[k] = *reinterpret_cast<const uint32_t*>(&z);
-      }
-      if (c < tiles * 8) {
-        *reinterpret_cast<uint4*>(qs + c * QB + 16 * (threadIdx.x % LPC)) = make_uint4(y[0], y[1], y[2], y[3]);
-        if (threadIdx.x % LPC == 0) {
-          const int r = c / a.G, row = c < cols ? r * a.H + c - r * a.G : -1;
-          qsc[c] = tiny(am) ? __int_as_float(0x7fffffff) : (float)(a.scale * 1.4426950408889634) / up;
-          qat[c] = row;
-          if (row >= 0 && blockIdx.z == 0) qnorm_row(a)[(int64_t)t0 * a.H + hk * a.G + row] = sqrtf(n2);
+        for (int u = 0; u < D / 64; ++u) tmem_ld32_nw(lane_addr + u * kSelCols + c0, x[u]);
+        tmem_wait_ld();
+        if (c0 + 32 >= c_hi) {         // all read: the next product may come
+          tc_fence_before();
+          if (lane == 0) mbar_arrive(freed);
+        }
+        if (j < last.c1) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const float2 f = col[c0 + c];
+            const int row = __float_as_int(f.y);
+            float y = __uint_as_float(x[0][c]);
+            if (D == 128) y += __uint_as_float(x[D / 64 - 1][c]);
+            if (row >= 0) out[(int64_t)row * pitch2 + j] = y * (down * f.x);
+          }
         }
       }
     }
   }
+  tc_fence_before();
   __syncthreads();
-
-  const int64_t pitch2 = select_pitch(a.max_pages) * 2;
-  for (int j = j0 + warp * 16; j < j_end; j += kSelThreads / 32 * 16) {
-    cp_async_wait_all();
-    __syncwarp();
-    // A fragments: a lane's four k indices of a step are four consecutive
-    // elements of its rows g and g + 8
-    uint32_t hi[D / 16][4], lo[D / 16][4];
-    float down[2];
-    float am[2] = {0.0f, 0.0f}, n2[2] = {0.0f, 0.0f};
-    const unsigned char* pages_s = stage + g * PR + tg * 16;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        const float4 x = *reinterpret_cast<const float4*>(pages_s + 8 * e * PR + 64 * c);
-        am[e] = fmaxf(fmax3(am[e], fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
-      }
-#pragma unroll
-      for (int o = 1; o < 4; o <<= 1) am[e] = fmaxf(am[e], __shfl_xor_sync(0xffffffffu, am[e], o));
-      const float up = unit_scale(am[e]);
-      down[e] = tiny(am[e]) ? __int_as_float(0x7fffffff) : 1.0f / up;
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        const float4 x = *reinterpret_cast<const float4*>(pages_s + 8 * e * PR + 64 * c);
-        const float y0 = x.x * up, y1 = x.y * up, y2 = x.z * up, y3 = x.w * up;
-        n2[e] += y0 * y0 + y1 * y1 + y2 * y2 + y3 * y3;
-        split2(y0, y1, hi[c][e], lo[c][e]);
-        split2(y2, y3, hi[c][e + 2], lo[c][e + 2]);
-      }
-#pragma unroll
-      for (int o = 1; o < 4; o <<= 1) n2[e] += __shfl_xor_sync(0xffffffffu, n2[e], o);
-    }
-    if (t1 == tile.t_end && tg == 0) {   // the sequence's last tile sees all of its pages
-      float* nr = norm_row(a, s, hk);
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (j + g + 8 * e < j_end) nr[j + g + 8 * e] = sqrtf(n2[e]) * down[e];
-    }
-    __syncwarp();                        // all lanes have read: the next batch may come
-    fetch(j + kSelThreads / 32 * 16);
-    page_ids(j + 2 * (kSelThreads / 32 * 16));
-    float* out = reinterpret_cast<float*>(logit_row(a, t0, hk * a.G)) + j + g;
-    for (int ct = 0; ct < tiles; ++ct) {
-      float sum[4] = {0.f, 0.f, 0.f, 0.f}, cl[4] = {0.f, 0.f, 0.f, 0.f};
-      const unsigned char* q = qs + (ct * 8 + g) * QB + 8 * tg;
-#pragma unroll
-      for (int c = 0; c < D / 16; c += 2) {
-        const uint2 b0 = *reinterpret_cast<const uint2*>(q + 32 * c);
-        const uint2 b1 = *reinterpret_cast<const uint2*>(q + 32 * c + 32);
-        float ch[4] = {0.f, 0.f, 0.f, 0.f};
-        hmma(ch, hi[c], b0.x, b0.y);
-        hmma(cl, lo[c], b0.x, b0.y);
-        hmma(ch, hi[c + 1], b1.x, b1.y);
-        hmma(cl, lo[c + 1], b1.x, b1.y);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) sum[u] += ch[u];
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int c = ct * 8 + 2 * tg + u, row = qat[c];
-        const float f = qsc[c];
-        float* o = out + (int64_t)row * pitch2;
-        if (row >= 0 && j + g < j_end) o[0] = (sum[u] + cl[u]) * (down[0] * f);
-        if (row >= 0 && j + g + 8 < j_end) o[8] = (sum[u + 2] + cl[u + 2]) * (down[1] * f);
-      }
-    }
-  }
+  if (warp == 8) tmem_dealloc(tmem, L::kCols);
 }
 
 // Reductions over the threads of an item: one warp, or the block.
@@ -1106,13 +1202,10 @@ __device__ __noinline__ void logits64_item(const CacheArgs& a, int t, int hk, do
 
 // WPI warps choose for one (row, key head), each thread holding E of its
 // pages; a block has 8 / WPI items.
-template <int D, int WPI, int E>
+template <int WPI, int E>
 __global__ void __launch_bounds__(kSelThreads) cache_choose_kernel(const CacheArgs a) {
-  __shared__ __align__(16) double qs[8 * (D + 8)];
-  __shared__ ExactSmem sm;
   __shared__ float red[kSelThreads / 32];
   __shared__ uint32_t bits[WPI > 1 ? WPI * E : 1];
-  __shared__ int todo[8 / WPI];
   __shared__ float few_mass[WPI == 1 ? 8 : 1][64];
   constexpr int IPB = 8 / WPI, GS = 32 * WPI;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1123,8 +1216,12 @@ __global__ void __launch_bounds__(kSelThreads) cache_choose_kernel(const CacheAr
   bool again = false;                                      // the item needs fp64
 
   if (t < rows_used(a)) {
-    const int s = row_seq(a, t);
-    const RowPages r = row_pages(a, t, s);
+    const int2 info = row_info(a)[t];
+    const int s = info.x;
+    RowPages r;
+    r.n = info.y;
+    r.c0 = min(a.n_first, r.n);
+    r.c1 = max(r.c0, r.n - a.n_recent);
     int* sel = a.sel + item * a.n_select;
     const int nc = r.c1 - r.c0, want = a.n_select - a.n_first - a.n_recent;
     if (fixed_pages(a, r, item, lid, GS)) {                // 0 < want < nc
@@ -1289,15 +1386,19 @@ __global__ void __launch_bounds__(kSelThreads) cache_choose_kernel(const CacheAr
       }
     }
   }
-  // ---- items that fp64 decides, one after the other ----
-  if (lid == 0) todo[WPI == 1 ? warp : 0] = again;
-  __syncthreads();
-#pragma unroll 1
-  for (int i = 0; i < IPB; ++i) {
-    if (!todo[i]) continue;
-    const int64_t it = (int64_t)blockIdx.x * IPB + i;
-    logits64_item<D>(a, (int)(it / a.Hkv), (int)(it % a.Hkv), qs);
-    choose64<E * WPI / 8 < 1 ? 1 : E * WPI / 8>(a, (int)(it / a.Hkv), (int)(it % a.Hkv), sm);
+  if (again && lid == 0) again_list(a)[atomicAdd(again_count(a), 1)] = make_int2(t, hk);
+}
+
+// The items that the fast choice left, a block each at a time.
+template <int D, int E>
+__global__ void __launch_bounds__(kSelThreads) cache_again_kernel(const CacheArgs a) {
+  __shared__ __align__(16) double qs[8 * (D + 8)];
+  __shared__ ExactSmem sm;
+  const int n = *again_count(a);
+  for (int i = blockIdx.x; i < n; i += gridDim.x) {
+    const int2 it = again_list(a)[i];
+    logits64_item<D>(a, it.x, it.y, qs);
+    choose64<E>(a, it.x, it.y, sm);
     __syncthreads();
   }
 }
@@ -1332,45 +1433,54 @@ static cudaError_t select_d(const CacheArgs& a, cudaStream_t s) {
   int dev = 0, sms = 0;
   cudaError_t e = device_sms(dev, sms);
   if (e != cudaSuccess) return e;
-  // two rows of a sequence or more on average: the fast logits
-  const bool fast = a.cu && a.T >= 2 * (int64_t)a.S;
+  // two rows of a sequence or more on average (and a key head's queries fit a
+  // tile): the fast logits
+  const bool fast = a.cu && a.T >= 2 * (int64_t)a.S && a.G <= kSelCols;
   const int most = fast ? kSelCols : 8;
   const int tile_rows = !a.cu || a.G >= most ? 1 : most / a.G;
   const int64_t tiles = a.cu ? (int64_t)(a.T / tile_rows) + a.S : a.S;
-  const int cols = (tile_rows * a.G + 7) / 8 * 8;
-  // pages of a logits block: all of them, or so few that every SM has blocks,
-  // a multiple of what a block's warps take at a time
-  const int step = fast ? 128 : 64;
-  int pages = (a.max_pages + step - 1) / step * step;
-  while (pages > 2 * step && tiles * a.Hkv * ((a.max_pages + pages - 1) / pages) < 4ll * sms)
-    pages = (pages / 2 + step - 1) / step * step;
-  const dim3 grid((unsigned)tiles, a.Hkv, (a.max_pages + pages - 1) / pages);
-  const int lb = fast ? logits_stage_off<D>(cols) + kSelThreads / 32 * 16 * (D * 4 + 64) : (cols + 3) / 4 * 4 * D * 8 + kSelThreads / 32 * 16 * D * 4;
   static OncePerDevice once_f, once_d;
-  auto go = [&](auto kernel, OncePerDevice& once) {
-    if (lb > 48 * 1024) {
-      const cudaError_t r = once.allow(reinterpret_cast<const void*>(kernel), dev, 232448);
-      if (r != cudaSuccess) return r;
-    }
-    kernel<<<grid, kSelThreads, lb, s>>>(a, tile_rows, pages);
-    return cudaGetLastError();
-  };
-  e = fast ? go(cache_logits_kernel<D>, once_f) : go(cache_logits64_kernel<D>, once_d);
-  if (e != cudaSuccess) return e;
+  if (fast) {
+    cache_split_kernel<D><<<dim3((unsigned)(select_pitch(a.max_pages) / 32), a.Hkv, a.S), kSelThreads, 0, s>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = once_f.allow(reinterpret_cast<const void*>(cache_logits_kernel<D>), dev, LogitsSmem<D>::kBytes);
+    if (e != cudaSuccess) return e;
+    cache_logits_kernel<D><<<dim3((unsigned)tiles, a.Hkv), 288, LogitsSmem<D>::kBytes, s>>>(a, tile_rows);
+  } else {
+    // pages of a block: all of them, or so few that every SM has blocks, a
+    // multiple of what a block's warps take at a time
+    const int step = 64, groups = (tile_rows * a.G + 3) / 4;
+    int pages = (a.max_pages + step - 1) / step * step;
+    while (pages > 2 * step && tiles * a.Hkv * ((a.max_pages + pages - 1) / pages) < 4ll * sms)
+      pages = (pages / 2 + step - 1) / step * step;
+    const int bytes = groups * 4 * D * 8 + kSelThreads / 32 * 16 * D * 4;
+    e = once_d.allow(reinterpret_cast<const void*>(cache_logits64_kernel<D>), dev, 232448);
+    if (e != cudaSuccess) return e;
+    cache_logits64_kernel<D><<<dim3((unsigned)tiles, a.Hkv, (a.max_pages + pages - 1) / pages), kSelThreads,
+                               bytes, s>>>(a, tile_rows, pages);
+  }
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int64_t items = (int64_t)a.T * a.Hkv;
   if (!fast) {
     const dim3 all(a.T, a.Hkv);
     if (a.max_pages <= 512) cache_choose64_kernel<2><<<all, kSelThreads, 0, s>>>(a);
     else if (a.max_pages <= 2048) cache_choose64_kernel<8><<<all, kSelThreads, 0, s>>>(a);
     else cache_choose64_kernel<64><<<all, kSelThreads, 0, s>>>(a);
-  } else if (a.max_pages <= 512) {
-    cache_choose_kernel<D, 1, 16><<<(unsigned)((items + 7) / 8), kSelThreads, 0, s>>>(a);
+    return cudaGetLastError();
+  }
+  const int again = (int)(items < 4ll * sms ? items : 4ll * sms);
+  if (a.max_pages <= 512) {
+    cache_choose_kernel<1, 16><<<(unsigned)((items + 7) / 8), kSelThreads, 0, s>>>(a);
+    cache_again_kernel<D, 2><<<again, kSelThreads, 0, s>>>(a);
   } else if (a.max_pages <= 1024) {
-    cache_choose_kernel<D, 1, 32><<<(unsigned)((items + 7) / 8), kSelThreads, 0, s>>>(a);
+    cache_choose_kernel<1, 32><<<(unsigned)((items + 7) / 8), kSelThreads, 0, s>>>(a);
+    cache_again_kernel<D, 4><<<again, kSelThreads, 0, s>>>(a);
   } else if (a.max_pages <= 8192) {
-    cache_choose_kernel<D, 8, 32><<<(unsigned)items, kSelThreads, 0, s>>>(a);
+    cache_choose_kernel<8, 32><<<(unsigned)items, kSelThreads, 0, s>>>(a);
+    cache_again_kernel<D, 32><<<again, kSelThreads, 0, s>>>(a);
   } else {
-    cache_choose_kernel<D, 8, 64><<<(unsigned)items, kSelThreads, 0, s>>>(a);
+    cache_choose_kernel<8, 64><<<(unsigned)items, kSelThreads, 0, s>>>(a);
+    cache_again_kernel<D, 64><<<again, kSelThreads, 0, s>>>(a);
   }
   return cudaGetLastError();
 }

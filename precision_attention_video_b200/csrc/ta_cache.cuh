@@ -57,8 +57,8 @@ struct CacheArgs {
   double* scratch;
 };
 
-// Doubles of a row of the choice's scratch: whole 128-byte lines of floats.
-__host__ __device__ inline int64_t select_pitch(int max_pages) { return (max_pages + 31) / 32 * 32; }
+// Doubles of a row of the choice's scratch: whole tiles of 128 pages.
+__host__ __device__ inline int64_t select_pitch(int max_pages) { return ((int64_t)max_pages + 127) / 128 * 128; }
 
 cudaError_t launch_cache_append(const CacheArgs& a, cudaStream_t s);
 cudaError_t launch_cache_select(const CacheArgs& a, cudaStream_t s);

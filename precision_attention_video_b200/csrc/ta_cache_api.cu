@@ -35,8 +35,11 @@ ta_status validate(const ta_cache_params* p) {
 
 size_t scratch_bytes(const ta_cache_params* p) {
   if (p->n_select <= 0) return 0;
-  return (size_t)ta::select_pitch(p->max_pages) * ((size_t)p->T * p->H * 8 + (size_t)p->S * p->Hkv * 4) +
-         (size_t)p->T * p->H * 4;
+  // logits; split means, their norms and scales; the queries' norms; the rows;
+  // the list of items to do again
+  const size_t pitch = (size_t)ta::select_pitch(p->max_pages), T = (size_t)p->T + (p->T & 1);
+  return pitch * ((size_t)p->T * p->H * 8 + (size_t)p->S * p->Hkv * (4 * p->d + 8)) + T * p->H * 4 + (T + 2) * 8 +
+         (size_t)p->T * p->Hkv * 8;
 }
 
 ta_status check_ws(const void* ws, size_t have, size_t need) {
