@@ -677,6 +677,22 @@ __global__ void __launch_bounds__(288, 2) cache_logits_kernel(const CacheArgs a,
   if (last.n <= a.n_select || last.c1 <= a.n_first) return;
   const int nb = (last.c1 + 127) / 128;
   const int cols = (t1 - t0) * a.G;
+  // queries: D / 8 lanes hold a column, 8 elements each; on their way while
+  // the block sets up
+  constexpr int LPC = D / 8, CPB = 256 / LPC, QL = kSelCols / CPB;
+  const int part = threadIdx.x % LPC;
+  uint4 w[QL];
+  if (warp < 8) {
+#pragma unroll
+    for (int i = 0; i < QL; ++i) {
+      const int c = i * CPB + threadIdx.x / LPC;
+      w[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (c < cols) {
+        const int r = c / a.G, h = hk * a.G + (c - r * a.G);
+        w[i] = *reinterpret_cast<const uint4*>(a.q + (int64_t)(t0 + r) * a.sq_t + (int64_t)h * a.sq_h + 8 * part);
+      }
+    }
+  }
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::oBar);
   uint64_t *full = bars, *done = bars + 1, *freed = bars + 2;
   uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 3);
@@ -708,52 +724,36 @@ __global__ void __launch_bounds__(288, 2) cache_logits_kernel(const CacheArgs a,
   __syncthreads();
   if (warp == 8 && lane == 0) load(0);
   if (warp < 8) {
-    // queries: D / 8 lanes hold a column, 8 elements each
-    constexpr int LPC = D / 8, CPB = 256 / LPC;
-    const int part = threadIdx.x % LPC;
-#pragma unroll 1
-    for (int cb = 0; cb < kSelCols; cb += 4 * CPB) {
-      uint4 w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = cb + i * CPB + threadIdx.x / LPC;
-        w[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (c < cols) {
-          const int r = c / a.G, h = hk * a.G + (c - r * a.G);
-          w[i] = *reinterpret_cast<const uint4*>(a.q + (int64_t)(t0 + r) * a.sq_t + (int64_t)h * a.sq_h + 8 * part);
-        }
+    for (int i = 0; i < QL; ++i) {
+      const int c = i * CPB + threadIdx.x / LPC;
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+      float am = 0.0f, n2 = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float x = bf_lo(u[k]), y = bf_hi(u[k]);
+        am = fmax3(am, fabsf(x), fabsf(y));
+        n2 += x * x + y * y;
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = cb + i * CPB + threadIdx.x / LPC;
-        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-        float am = 0.0f, n2 = 0.0f;
+      for (int o = 1; o < LPC; o <<= 1) {
+        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+        n2 += __shfl_xor_sync(0xffffffffu, n2, o);
+      }
+      const float up = unit_scale(am);
+      uint32_t y[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float x = bf_lo(u[k]), y = bf_hi(u[k]);
-          am = fmax3(am, fabsf(x), fabsf(y));
-          n2 += x * x + y * y;
-        }
-#pragma unroll
-        for (int o = 1; o < LPC; o <<= 1) {
-          am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-          n2 += __shfl_xor_sync(0xffffffffu, n2, o);
-        }
-        const float up = unit_scale(am);
-        uint32_t y[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const __half2 z = __floats2half2_rn(bf_lo(u[k]) * up, bf_hi(u[k]) * up);
-          y[k] = *reinterpret_cast<const uint32_t*>(&z);
-        }
-        *reinterpret_cast<uint4*>(smem + L::oB + (part / 8) * T::kHalf + c * 128 + (((part % 8) ^ (c & 7)) << 4)) =
-            make_uint4(y[0], y[1], y[2], y[3]);
-        if (part == 0) {
-          const int r = c / a.G, row = c < cols ? r * a.H + c - r * a.G : -1;
-          col[c] = make_float2(tiny(am) ? __int_as_float(0x7fffffff) : (float)(a.scale * 1.4426950408889634) / up,
-                               __int_as_float(row));
-          if (row >= 0) qnorm_row(a)[(int64_t)t0 * a.H + hk * a.G + row] = sqrtf(n2);
-        }
+      for (int k = 0; k < 4; ++k) {
+        const __half2 z = __floats2half2_rn(bf_lo(u[k]) * up, bf_hi(u[k]) * up);
+        y[k] = *reinterpret_cast<const uint32_t*>(&z);
+      }
+      *reinterpret_cast<uint4*>(smem + L::oB + (part / 8) * T::kHalf + c * 128 + (((part % 8) ^ (c & 7)) << 4)) =
+          make_uint4(y[0], y[1], y[2], y[3]);
+      if (part == 0) {
+        const int r = c / a.G, row = c < cols ? r * a.H + c - r * a.G : -1;
+        col[c] = make_float2(tiny(am) ? __int_as_float(0x7fffffff) : (float)(a.scale * 1.4426950408889634) / up,
+                             __int_as_float(row));
+        if (row >= 0) qnorm_row(a)[(int64_t)t0 * a.H + hk * a.G + row] = sqrtf(n2);
       }
     }
     fence_proxy_async_smem();
@@ -1203,7 +1203,7 @@ __device__ __noinline__ void logits64_item(const CacheArgs& a, int t, int hk, do
 // WPI warps choose for one (row, key head), each thread holding E of its
 // pages; a block has 8 / WPI items.
 template <int WPI, int E>
-__global__ void __launch_bounds__(kSelThreads) cache_choose_kernel(const CacheArgs a) {
+__global__ void __launch_bounds__(kSelThreads, WPI == 1 && E == 16 ? 4 : 1) cache_choose_kernel(const CacheArgs a) {
   __shared__ float red[kSelThreads / 32];
   __shared__ uint32_t bits[WPI > 1 ? WPI * E : 1];
   __shared__ float few_mass[WPI == 1 ? 8 : 1][64];
