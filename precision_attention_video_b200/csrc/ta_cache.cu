@@ -435,31 +435,6 @@ __device__ __forceinline__ int q_slot(int d) {
   return (d & ~15) + ((d >> 1) & 1) * 8 + ((d >> 2) & 3) * 2 + (d & 1);
 }
 
-// Rows of a logits block: up to tile_rows of one sequence.
-struct RowTile {
-  int s, t0, t1, t_end;
-};
-__device__ __forceinline__ RowTile row_tile(const CacheArgs& a, int tile, int tile_rows) {
-  RowTile r;
-  if (a.cu) {
-    // tiles of sequence s start at cu[s] / tile_rows + s
-    int lo = 0, hi = a.S - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (max(a.cu[mid], 0) / tile_rows + mid <= tile) lo = mid; else hi = mid - 1;
-    }
-    r.s = lo;
-    const int c0 = max(a.cu[lo], 0);
-    r.t0 = c0 + (tile - (c0 / tile_rows + lo)) * tile_rows;
-    r.t_end = min(a.cu[lo + 1], rows_used(a));
-    r.t1 = min(r.t_end, r.t0 + tile_rows);
-  } else {
-    r.s = r.t0 = tile;
-    r.t1 = r.t_end = tile + 1;
-  }
-  return r;
-}
-
 // fp64 logits of a tile of few rows.  A warp takes 8 pages at a time, the next
 // 8 on their way to shared memory: 8 lanes hold a page and multiply it with 4 columns, two
 // pages for each column element read from shared memory, and 7 exchanges with

@@ -55,7 +55,21 @@ struct CacheArgs {
   float* part_ml;
   float* part_o;
   double* scratch;
+  // sparse attention of many rows (parts of scratch)
+  int tile_rows;                  // rows that share their pages' loads
+  int list_cap;                   // entries of a tile's page list
+  int* row_flags;                 // [T] rows to do again on their own; null: all rows
+  int* list_n;                    // [tile, Hkv] entries of the joint lists
+  int2* lists;                    // [tile, Hkv, list_cap] (page, bits of the rows that read it)
 };
+
+// Sparse attention takes rows of a sequence together where there are rows
+// enough: 32 (row, query head) columns to a tile.  0: rows on their own.
+constexpr int kGroupCols = 32;
+inline int group_rows(int G, int64_t T, int64_t S, int max_pages) {
+  return G <= kGroupCols / 2 && T >= 4 * S && max_pages <= kMaxSelectPages ? kGroupCols / G : 0;
+}
+inline int64_t group_tiles(int rows, int64_t T, int64_t S) { return T / rows + S; }
 
 // Doubles of a row of the choice's scratch: whole tiles of 128 pages.
 __host__ __device__ inline int64_t select_pitch(int max_pages) { return ((int64_t)max_pages + 127) / 128 * 128; }
@@ -138,6 +152,31 @@ __device__ __forceinline__ int page_of(const CacheArgs& a, int s, int e) {
     return -1;
   }
   return pg;
+}
+
+// Rows that a block takes together: up to tile_rows of one sequence.
+struct RowTile {
+  int s, t0, t1, t_end;
+};
+__device__ __forceinline__ RowTile row_tile(const CacheArgs& a, int tile, int tile_rows) {
+  RowTile r;
+  if (a.cu) {
+    // tiles of sequence s start at cu[s] / tile_rows + s
+    int lo = 0, hi = a.S - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (max(a.cu[mid], 0) / tile_rows + mid <= tile) lo = mid; else hi = mid - 1;
+    }
+    r.s = lo;
+    const int c0 = max(a.cu[lo], 0);
+    r.t0 = c0 + (tile - (c0 / tile_rows + lo)) * tile_rows;
+    r.t_end = min(a.cu[lo + 1], rows_used(a));
+    r.t1 = min(r.t_end, r.t0 + tile_rows);
+  } else {
+    r.s = r.t0 = tile;
+    r.t1 = r.t_end = tile + 1;
+  }
+  return r;
 }
 
 #endif  // __CUDACC__

@@ -33,13 +33,25 @@ ta_status validate(const ta_cache_params* p) {
   return TA_OK;
 }
 
-size_t scratch_bytes(const ta_cache_params* p) {
+// The choice's scratch: logits; split means, their norms and scales; the
+// queries' norms; the rows; the list of items to do again.
+size_t select_bytes(const ta_cache_params* p) {
   if (p->n_select <= 0) return 0;
-  // logits; split means, their norms and scales; the queries' norms; the rows;
-  // the list of items to do again
   const size_t pitch = (size_t)ta::select_pitch(p->max_pages), T = (size_t)p->T + (p->T & 1);
   return pitch * ((size_t)p->T * p->H * 8 + (size_t)p->S * p->Hkv * (4 * p->d + 8)) + T * p->H * 4 + (T + 2) * 8 +
          (size_t)p->T * p->Hkv * 8;
+}
+// Sparse attention's: joint page lists and their lengths, the rows' flags.
+size_t sparse_bytes(const ta_cache_params* p) {
+  if (p->n_select <= 0) return 0;
+  const int rows = ta::group_rows(p->H / p->Hkv, p->T, p->S, p->max_pages);
+  if (!rows) return 0;
+  const size_t items = (size_t)ta::group_tiles(rows, p->T, p->S) * p->Hkv;
+  return items * ((size_t)rows * p->n_select * 8 + 4) + (size_t)p->T * 4;
+}
+size_t scratch_bytes(const ta_cache_params* p) {
+  const size_t a = select_bytes(p), b = sparse_bytes(p);
+  return a > b ? a : b;
 }
 
 ta_status check_ws(const void* ws, size_t have, size_t need) {
@@ -176,7 +188,7 @@ ta_status attend(const ta_cache_params* p, const ta_cache* cache, const void* Q,
   if (!rows_ok(Q, p->stride_q_t, p->stride_q_h) || !rows_ok(O, p->stride_o_t, p->stride_o_h) ||
       (lse && !aligned(lse, 4)))
     return TA_ERR_INVALID_ARG;
-  if ((st = check_ws(ws, ws_bytes, ta::kWsScratch)) != TA_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, ta::kWsScratch + (sparse ? sparse_bytes(p) : 0))) != TA_OK) return st;
   CacheArgs a;
   fill(p, cache, cu, lens, table, ws, a);
   a.q = static_cast<const __nv_bfloat16*>(Q);
@@ -260,7 +272,7 @@ ta_status tiered_attn_cache_select(const ta_cache_params* p, const ta_cache* cac
   if ((st = check_cache(p, cache, false, true)) != TA_OK) return st;
   if ((st = check_index(p, cu, lens, table)) != TA_OK) return st;
   if (!rows_ok(Q, p->stride_q_t, p->stride_q_h) || !aligned(sel, 4)) return TA_ERR_INVALID_ARG;
-  if ((st = check_ws(ws, ws_bytes, ta::kWsScratch + scratch_bytes(p))) != TA_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, ta::kWsScratch + select_bytes(p))) != TA_OK) return st;
   CacheArgs a;
   fill(p, cache, cu, lens, table, ws, a);
   a.q = static_cast<const __nv_bfloat16*>(Q);

@@ -42,11 +42,12 @@ namespace {
 constexpr int kWarps = 8;                // computing warps
 constexpr int kThreads = 32 * (kWarps + 1);
 
-template <int D, bool FP8, int NT>
+template <int D, bool FP8, int NT, bool GROUP = false>
 struct Cfg {
   static constexpr int kRow = D * (FP8 ? 1 : 2);          // bytes of a key
-  static constexpr int kKT = kRow > 128 ? 1 : 2;          // 16-key tiles of a warp
-  static constexpr int kUnit = kWarps * 16 * kKT;         // keys of a unit (one stage)
+  static constexpr int kKT = !GROUP && kRow > 128 ? 1 : 2;   // 16-key tiles of a warp
+  static constexpr int kKeyWarps = GROUP ? 4 : kWarps;    // warps side by side along the keys
+  static constexpr int kUnit = kKeyWarps * 16 * kKT;      // keys of a unit (one stage)
   static constexpr int kCols = kRow > 128 ? 2 : 1;        // 128-byte columns of a row
   static constexpr int kColB = kRow / kCols;              // 128 or 64
   static constexpr int kTile = kUnit * kRow;               // 16 or 32 KB
@@ -55,10 +56,11 @@ struct Cfg {
   static constexpr int kStages = kStage > 40000 ? 3 : 6;
   static constexpr int kRegs = D / 16 * NT * 4;           // accumulators of a lane
   static constexpr int oJoin = kStages * ((kStage + 1023) / 1024 * 1024);
-  static constexpr int kJoin = NT == 1 ? 4 : 2;           // warps that join at a time
-  static constexpr int oML = oJoin + kJoin * kRegs * 32 * 4;
+  static constexpr int kJoin = GROUP ? 1 : (NT == 1 ? 4 : 2);   // key warps that join at a time
+  static constexpr int kColGroups = kWarps / kKeyWarps;
+  static constexpr int oML = oJoin + kColGroups * kJoin * kRegs * 32 * 4;
   static constexpr int oCnt = oML + 2 * 2 * kWarps * kMaxTileHeads * 4;  // m, l; items take turns
-  static constexpr int oBar = oCnt + kStages * (kUnit / 16) * 4;
+  static constexpr int oBar = oCnt + kStages * (kUnit / 16) * (GROUP ? 16 : 4);
   static constexpr int oMisc = oBar + 2 * kStages * 8;
   static constexpr int oPre = oMisc + 128;
   static constexpr int kBytes = oPre + 1024;              // 1024 to align; + a decode's prefix
@@ -179,6 +181,356 @@ struct Cursor {
   }
 };
 
+// The softmax state of a warp: 8 NT columns (query heads), D numerators each.
+template <int D, int NT>
+struct Fold {
+  uint32_t qf[D / 16][NT][2];    // the queries, as B fragments
+  float acc[D / 16][NT][4];
+  float m[NT][2], l[NT][2];      // running maximum (of s * sq, log2 units) and sum
+  float sq[NT][2];               // what a raw product counts for, in log2 units
+  float vmax;                    // FP8: the numerators' unit, the largest V scale so far
+};
+
+// Column nt * 8 + g's query into the fragments (`on`: the column is in use),
+// and the state of an item without keys.
+template <int D, bool FP8, int NT>
+__device__ __forceinline__ void fold_query(Fold<D, NT>& f, int nt, const __nv_bfloat16* qh, bool on, float sc) {
+  const int lane = threadIdx.x & 31, tg = lane & 3;
+  auto& qf = f.qf;
+  auto& sq = f.sq;
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c) {
+    // bf16 keys: k index of the fragment = head element; FP8: a lane's
+    // four k indices are four consecutive elements (as its keys load)
+    const int d0 = c * 16 + (FP8 ? 4 * tg : 2 * tg), d1 = d0 + (FP8 ? 2 : 8);
+    qf[c][nt][0] = on ? *reinterpret_cast<const uint32_t*>(qh + d0) : 0u;
+    qf[c][nt][1] = on ? *reinterpret_cast<const uint32_t*>(qh + d1) : 0u;
+  }
+  if constexpr (FP8) {
+    // FP8 keys are f16 operands, so the query is one too, its largest
+    // element scaled to [2^8, 2^9) by a power of two: what falls below
+    // f16's smallest step is under 2^-33 of that element
+    uint32_t am = 0;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        am = max(am, max((qf[c][nt][e] & 0x7FFFu) << 16, qf[c][nt][e] & 0x7FFF0000u));
+    am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+    am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+    // (a head of zeros or with values that are not finite is left as it is)
+    const float ax = __uint_as_float(am);
+    const bool plain = ax >= 1e-35f && ax <= 3.4e38f;
+    const float up = plain ? 256.0f / pow2_of(ax) : 1.0f;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t w = qf[c][nt][e];
+        qf[c][nt][e] = pack_f16(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xFFFF0000u) * up);
+      }
+    const float down = plain ? pow2_of(ax) * 0.00390625f : 1.0f;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)                // from the lanes that hold head 2 tg + j
+      sq[nt][j] = sc * __shfl_sync(0xffffffffu, down, (2 * tg + j) * 4);
+  } else {
+    sq[nt][0] = sq[nt][1] = sc;
+  }
+  f.m[nt][0] = f.m[nt][1] = -__int_as_float(0x7f800000);
+  f.l[nt][0] = f.l[nt][1] = 0.0f;
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f.acc[c][nt][j] = 0.0f;
+}
+
+// Folds a warp's 16 KT keys (from key0 of the stage on) into its state.
+// cn[kt]: keys of tile kt that exist; seen(kt, e, nt, j): whether key g + 8 e
+// of it is visible to column nt * 8 + 2 tg + j.
+template <class C, int D, bool FP8, int NT, typename Seen>
+__device__ __forceinline__ void fold_unit(Fold<D, NT>& f, const unsigned char* stage, int key0,
+                                          const int (&cn)[C::kKT], Seen seen) {
+  constexpr int KT = C::kKT, kUnit = C::kUnit;
+  const int lane = threadIdx.x & 31, g = lane >> 2, tg = lane & 3;
+  const float kNegInf = -__int_as_float(0x7f800000);
+  auto& qf = f.qf;
+  auto& acc = f.acc;
+  auto& m = f.m;
+  auto& l = f.l;
+  auto& sq = f.sq;
+  auto& vmax = f.vmax;
+  const uint32_t kbase = smem_u32(stage);
+  const uint32_t vbase = kbase + C::kTile;
+  float s[KT][NT][4];
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[kt][nt][j] = 0.0f;
+  // address of 16-byte chunk c of key r (swizzled as TMA stored it)
+  auto chunk = [&](uint32_t base, int r, int c) -> uint32_t {
+    if constexpr (C::kColB == 128)
+      return base + (c >> 3) * (kUnit * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    else
+      return base + r * 64 + (((c & 3) ^ ((r >> 1) & 3)) << 4);
+  };
+  if constexpr (!FP8) {
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) {
+        uint32_t r[4];
+        ldsm4(r, chunk(kbase, key0 + kt * 16 + (lane & 15), 2 * c + (lane >> 4)));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma16816<false>(s[kt][nt], r[0], r[1], r[2], r[3], qf[c][nt][0], qf[c][nt][1]);
+      }
+  } else {
+#pragma unroll
+    for (int c = 0; c < D / 16; c += 2)
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) {
+        uint32_t r[4];   // rows 0-7 and 8-15 of chunk c, then of chunk c + 1
+        ldsm4(r, chunk(kbase, key0 + kt * 16 + (lane & 15), c + (lane >> 4)));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t x = r[2 * e], y = r[2 * e + 1];
+          const uint32_t a0 = e4m3_f16x2_lo(x), a2 = e4m3_f16x2_hi(x);
+          const uint32_t a1 = e4m3_f16x2_lo(y), a3 = e4m3_f16x2_hi(y);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816<true>(s[kt][nt], a0, a1, a2, a3, qf[c + e][nt][0], qf[c + e][nt][1]);
+        }
+      }
+  }
+  // scores in log2 units, hidden keys out, running maximum
+  float vs[KT][2], vm = vmax;
+  float mx[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = kNegInf;
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt) {
+    float ks[2] = {1.0f, 1.0f};
+    if constexpr (FP8) {
+      const float* kss = reinterpret_cast<const float*>(stage + 2 * C::kTile);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = key0 + kt * 16 + g + 8 * e;
+        ks[e] = kss[r];
+        vs[kt][e] = g + 8 * e < cn[kt] ? kss[kUnit + r] : 0.0f;
+        vm = fmaxf(vm, vs[kt][e]);
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float x = FP8 ? s[kt][nt][j] * ks[j >> 1] : s[kt][nt][j];
+        s[kt][nt][j] = seen(kt, j >> 1, nt, j & 1) ? x * sq[nt][j & 1] : kNegInf;
+      }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) mx[nt][j] = fmax3(mx[nt][j], s[kt][nt][j], s[kt][nt][j + 2]);
+  }
+  bool up = false;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1)
+        mx[nt][j] = fmaxf(mx[nt][j], __shfl_xor_sync(0xffffffffu, mx[nt][j], o));
+      mx[nt][j] = fmaxf(mx[nt][j], m[nt][j]);
+      up |= mx[nt][j] > m[nt][j];
+    }
+  if constexpr (FP8) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+    up |= vm > vmax;
+  }
+  if (__any_sync(0xffffffffu, up)) {
+    const float fv = FP8 && vmax > 0.0f ? vmax / vm : 1.0f;   // powers of two
+    vmax = vm;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float f = m[nt][j] == kNegInf ? 0.0f : ex2(m[nt][j] - mx[nt][j]);
+        m[nt][j] = mx[nt][j];
+        l[nt][j] *= f;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          acc[c][nt][j] *= f * fv;
+          acc[c][nt][j + 2] *= f * fv;
+        }
+      }
+  }
+  // weights, their sums, and P^T as the second product's B operand
+  uint32_t pf[KT][NT][2];
+  float vf[KT][2];
+  if constexpr (FP8) {
+    // f16 weights, the largest V scale's at 2^15: a weight keeps its 11
+    // bits down to 2^-29 of that scale
+    const float iv = vmax > 0.0f ? 1.0f / vmax : 1.0f;
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) vf[kt][e] = vs[kt][e] * iv * 32768.0f;
+  }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    float mm[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) mm[j] = m[nt][j] == kNegInf ? 0.0f : m[nt][j];
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) {
+      float p[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        p[j] = ex2(s[kt][nt][j] - mm[j & 1]);
+        l[nt][j & 1] += p[j];
+        if (FP8) p[j] *= vf[kt][j >> 1];
+      }
+      pf[kt][nt][0] = movm(FP8 ? pack_f16(p[0], p[1]) : pack_bf16(p[0], p[1]));
+      pf[kt][nt][1] = movm(FP8 ? pack_f16(p[2], p[3]) : pack_bf16(p[2], p[3]));
+    }
+  }
+  // O^T += V^T P^T; slots behind the last key hold anything, NaN included
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt) {
+    const int c = cn[kt];
+    if (c == 0) continue;
+    auto product = [&](auto whole) {
+      uint32_t m0 = 0xFFFFFFFFu, m1 = 0xFFFFFFFFu;
+      if constexpr (!decltype(whole)::value) {
+        m0 = (2 * tg < c ? 0xFFFFu : 0u) | (2 * tg + 1 < c ? 0xFFFF0000u : 0u);
+        m1 = (2 * tg + 8 < c ? 0xFFFFu : 0u) | (2 * tg + 9 < c ? 0xFFFF0000u : 0u);
+      }
+      if constexpr (!FP8) {
+#pragma unroll
+        for (int cd = 0; cd < D / 16; ++cd) {
+          uint32_t r[4];   // keys 0-7 by d 0-7 and 8-15, then keys 8-15
+          ldsm4t(r, chunk(vbase, key0 + kt * 16 + (lane & 7) + ((lane >> 4) << 3),
+                          2 * cd + ((lane >> 3) & 1)));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816<false>(acc[cd][nt], r[0] & m0, r[1] & m0, r[2] & m1, r[3] & m1,
+                            pf[kt][nt][0], pf[kt][nt][1]);
+        }
+      } else {
+#pragma unroll
+        for (int cd = 0; cd < D / 16; cd += 2) {
+          uint32_t r[4];   // chunk cd by keys 0-7 and 8-15, then chunk cd + 1
+          ldsm4t(r, chunk(vbase, key0 + kt * 16 + (lane & 15), cd + (lane >> 4)));
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            // bytes (key, d), (key, d + 1), (key + 1, d), (key + 1, d + 1)
+            // to the pairs of keys at d and at d + 1
+            const uint32_t x = __byte_perm(r[2 * e], 0, 0x3120);
+            const uint32_t y = __byte_perm(r[2 * e + 1], 0, 0x3120);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816<true>(acc[cd + e][nt], e4m3_f16x2_lo(x) & m0, e4m3_f16x2_hi(x) & m0,
+                             e4m3_f16x2_lo(y) & m1, e4m3_f16x2_hi(y) & m1, pf[kt][nt][0],
+                             pf[kt][nt][1]);
+          }
+        }
+      }
+    };
+    if (c == 16)
+      product(std::true_type{});
+    else
+      product(std::false_type{});
+  }
+}
+
+// Joins the key warps of each column group, whose columns and numerators the
+// readers below then give.  sm: maxima and sums, [warp][16] each; an item's may
+// still be read while the next one's are written, so items take turns.
+template <class C, int D, bool FP8, int NT>
+__device__ __forceinline__ void join_warps(Fold<D, NT>& f, float* join, float* sm) {
+  constexpr int KW = C::kKeyWarps;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tg = lane & 3;
+  const int kw = warp % KW, cg = warp / KW;
+  const float kNegInf = -__int_as_float(0x7f800000);
+  float* sm_m = sm;
+  float* sm_l = sm + kWarps * kMaxTileHeads;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) f.l[nt][j] += __shfl_xor_sync(0xffffffffu, f.l[nt][j], o);
+      if (g == 0) {
+        sm_m[warp * kMaxTileHeads + nt * 8 + 2 * tg + j] = f.m[nt][j];
+        sm_l[warp * kMaxTileHeads + nt * 8 + 2 * tg + j] = f.l[nt][j];
+      }
+    }
+  compute_sync();
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float mm = kNegInf;
+      for (int w = 0; w < KW; ++w)
+        mm = fmaxf(mm, sm_m[(cg * KW + w) * kMaxTileHeads + nt * 8 + 2 * tg + j]);
+      float x = f.m[nt][j] == kNegInf ? 0.0f : ex2(f.m[nt][j] - mm);
+      if (FP8) x *= f.vmax * 3.0517578125e-5f;     // back to V's own units
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        f.acc[c][nt][j] *= x;
+        f.acc[c][nt][j + 2] *= x;
+      }
+    }
+  float* mine = join + (cg * C::kJoin + (kw & (C::kJoin - 1))) * (C::kRegs * 32) + lane;
+  for (int r = KW / C::kJoin - 1; r >= 0; --r) {
+    if (kw / C::kJoin == r) {
+      const bool put_first = r == KW / C::kJoin - 1;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float* at = mine + ((c * NT + nt) * 4 + j) * 32;
+            *at = put_first ? f.acc[c][nt][j] : *at + f.acc[c][nt][j];
+          }
+    }
+    compute_sync();
+  }
+}
+// Numerator d of column nn (8 NT of them in a group).
+template <class C, int D, bool FP8, int NT>
+__device__ __forceinline__ float joined_at(const float* join, int nn, int d) {
+  const int cg = nn / (8 * NT), n = nn % (8 * NT), dd = d & 15;
+  const int gg = FP8 ? dd >> 1 : dd & 7, hi = FP8 ? dd & 1 : dd >> 3;
+  const int at = (((d >> 4) * NT + (n >> 3)) * 4 + hi * 2 + (n & 1)) * 32 + gg * 4 + ((n & 7) >> 1);
+  const float* b = join + cg * C::kJoin * (C::kRegs * 32) + at;
+  float x = b[0];
+#pragma unroll
+  for (int k = 1; k < C::kJoin; ++k) x += b[k * (C::kRegs * 32)];
+  return x;
+}
+// Maximum and sum of column nn, 16 at most in a group.
+template <class C>
+__device__ __forceinline__ void joined_state(const float* sm, int nn, float& mm, float& ll) {
+  constexpr int KW = C::kKeyWarps;
+  const float kNegInf = -__int_as_float(0x7f800000);
+  const float* sm_m = sm + (nn / kMaxTileHeads) * KW * kMaxTileHeads + nn % kMaxTileHeads;
+  const float* sm_l = sm_m + kWarps * kMaxTileHeads;
+  mm = kNegInf;
+  ll = 0.0f;
+#pragma unroll
+  for (int w = 0; w < KW; ++w) mm = fmaxf(mm, sm_m[w * kMaxTileHeads]);
+#pragma unroll
+  for (int w = 0; w < KW; ++w) {
+    const float mw = sm_m[w * kMaxTileHeads];
+    ll += mw == kNegInf ? 0.0f : ex2(mw - mm) * sm_l[w * kMaxTileHeads];
+  }
+}
+
 template <int D, bool FP8, int NT, bool SPARSE>
 __global__ void __launch_bounds__(kThreads, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
@@ -257,13 +609,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   Cursor<SPARSE, kUnit> cur;
   cur.start(a, pre, rows, HX, u0);
 
+  // with row flags, items of rows without one are passed over
+  auto skip = [&](int& i) -> bool {
+    if (!SPARSE || !a.row_flags || a.row_flags[cur.row]) return false;
+    i += cur.units - 1 - cur.k;
+    cur.k = cur.units - 1;
+    if (i + 1 < n_units) cur.next(a, pre, HX);
+    return true;
+  };
+
   if (warp == kWarps) {
     // ---- loads: lane i brings page i of the unit ----
     const int ppu = kUnit >> a.ps_log2;
     int row = -1, s = 0, len = 0;
     int issued = 0;
     for (int i = 0; i < n_units; ++i) {
-      const int st = i % C::kStages;
+      if (skip(i)) continue;
+      const int st = issued % C::kStages;
       if (cur.row != row) {
         row = cur.row;
         s = SPARSE ? row_seq(a, row) : row;
@@ -281,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const uint32_t live = __ballot_sync(0xffffffffu, vc > 0);
-      if (i >= C::kStages && !mbar_wait(&empty[st], ((i / C::kStages) - 1) & 1, abort, 1)) break;
+      if (issued >= C::kStages && !mbar_wait(&empty[st], ((issued / C::kStages) - 1) & 1, abort, 1)) break;
       unsigned char* stage = smem + st * C::kStageStep;
       const int v16 = __shfl_sync(0xffffffffu, vc, (lane & (kGroups - 1)) >> (a.ps_log2 - 4));
       if (lane < kGroups)
@@ -307,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     &full[st]);
         }
       }
-      issued = i + 1;
+      ++issued;
       if (i + 1 < n_units) cur.next(a, pre, HX);
     }
     if (*abort.abort) {
@@ -319,13 +681,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // ---- compute ----
-  const int g = lane >> 2, tg = lane & 3;
+  const int g = lane >> 2;
   const float sc = a.scale_log2;
-  uint32_t qf[D / 16][NT][2];
-  float acc[D / 16][NT][4];
-  float m[NT][2], l[NT][2];      // running maximum (of s * sq, log2 units) and sum
-  float sq[NT][2];               // what a raw product counts for, in log2 units
-  float vmax = 1.0f;             // FP8: the numerators' unit, the largest V scale so far
+  Fold<D, NT> f;
   float* join = reinterpret_cast<float*>(smem + C::oJoin);
   const float kNegInf = -__int_as_float(0x7f800000);
   bool fresh = true;                               // no unit of the item taken yet
@@ -333,66 +691,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   int turn = 0;
   float* sm_m = sm_m0;
 
+  int taken = 0;
   for (int i = 0; i < n_units; ++i) {
-    const int st = i % C::kStages;
+    if (skip(i)) continue;
+    const int st = taken % C::kStages;
     const int hk = cur.hx / HG, h0 = hk * a.G + (cur.hx - hk * HG) * NH;
     const int nh = min(NH, (hk + 1) * a.G - h0);   // heads in use
     if (fresh) {
       fresh = false;
       k_first = cur.k;
-      vmax = 0.0f;
+      f.vmax = 0.0f;
       const __nv_bfloat16* q = a.q + (int64_t)cur.row * a.sq_t + (int64_t)h0 * a.sq_h;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const bool on = nt * 8 + g < nh;
-        const __nv_bfloat16* qh = q + (int64_t)(nt * 8 + g) * a.sq_h;
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          // bf16 keys: k index of the fragment = head element; FP8: a lane's
-          // four k indices are four consecutive elements (as its keys load)
-          const int d0 = c * 16 + (FP8 ? 4 * tg : 2 * tg), d1 = d0 + (FP8 ? 2 : 8);
-          qf[c][nt][0] = on ? *reinterpret_cast<const uint32_t*>(qh + d0) : 0u;
-          qf[c][nt][1] = on ? *reinterpret_cast<const uint32_t*>(qh + d1) : 0u;
-        }
-        if constexpr (FP8) {
-          // FP8 keys are f16 operands, so the query is one too, its largest
-          // element scaled to [2^8, 2^9) by a power of two: what falls below
-          // f16's smallest step is under 2^-33 of that element
-          uint32_t am = 0;
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              am = max(am, max((qf[c][nt][e] & 0x7FFFu) << 16, qf[c][nt][e] & 0x7FFF0000u));
-          am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
-          am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
-          // (a head of zeros or with values that are not finite is left as it is)
-          const float ax = __uint_as_float(am);
-          const bool plain = ax >= 1e-35f && ax <= 3.4e38f;
-          const float up = plain ? 256.0f / pow2_of(ax) : 1.0f;
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t w = qf[c][nt][e];
-              qf[c][nt][e] = pack_f16(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xFFFF0000u) * up);
-            }
-          const float down = plain ? pow2_of(ax) * 0.00390625f : 1.0f;
-#pragma unroll
-          for (int j = 0; j < 2; ++j)                // from the lanes that hold head 2 tg + j
-            sq[nt][j] = sc * __shfl_sync(0xffffffffu, down, (2 * tg + j) * 4);
-        } else {
-          sq[nt][0] = sq[nt][1] = sc;
-        }
-        m[nt][0] = m[nt][1] = kNegInf;
-        l[nt][0] = l[nt][1] = 0.0f;
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[c][nt][j] = 0.0f;
-      }
+      for (int nt = 0; nt < NT; ++nt)
+        fold_query<D, FP8, NT>(f, nt, q + (int64_t)(nt * 8 + g) * a.sq_h, nt * 8 + g < nh, sc);
     }
-    const bool ok = mbar_wait(&full[st], (i / C::kStages) & 1, abort, 2);
+    const bool ok = mbar_wait(&full[st], (taken / C::kStages) & 1, abort, 2);
+    ++taken;
     int cn[KT], any = 0;                           // keys of this warp's tiles
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) {
@@ -400,264 +715,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       any |= cn[kt];
     }
     if (any) {
-      const uint32_t kbase = smem_u32(smem + st * C::kStageStep);
-      const uint32_t vbase = kbase + C::kTile;
-      const int key0 = warp * 16 * KT;
-      float s[KT][NT][4];
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) s[kt][nt][j] = 0.0f;
-      // address of 16-byte chunk c of key r (swizzled as TMA stored it)
-      auto chunk = [&](uint32_t base, int r, int c) -> uint32_t {
-        if constexpr (C::kColB == 128)
-          return base + (c >> 3) * (kUnit * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-        else
-          return base + r * 64 + (((c & 3) ^ ((r >> 1) & 3)) << 4);
-      };
-      if constexpr (!FP8) {
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-          for (int kt = 0; kt < KT; ++kt) {
-            uint32_t r[4];
-            ldsm4(r, chunk(kbase, key0 + kt * 16 + (lane & 15), 2 * c + (lane >> 4)));
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma16816<false>(s[kt][nt], r[0], r[1], r[2], r[3], qf[c][nt][0], qf[c][nt][1]);
-          }
-      } else {
-#pragma unroll
-        for (int c = 0; c < D / 16; c += 2)
-#pragma unroll
-          for (int kt = 0; kt < KT; ++kt) {
-            uint32_t r[4];   // rows 0-7 and 8-15 of chunk c, then of chunk c + 1
-            ldsm4(r, chunk(kbase, key0 + kt * 16 + (lane & 15), c + (lane >> 4)));
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t x = r[2 * e], y = r[2 * e + 1];
-              const uint32_t a0 = e4m3_f16x2_lo(x), a2 = e4m3_f16x2_hi(x);
-              const uint32_t a1 = e4m3_f16x2_lo(y), a3 = e4m3_f16x2_hi(y);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma16816<true>(s[kt][nt], a0, a1, a2, a3, qf[c + e][nt][0], qf[c + e][nt][1]);
-            }
-          }
-      }
-      // scores in log2 units, hidden keys out, running maximum
-      float vs[KT][2], vm = vmax;
-      float mx[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = kNegInf;
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt) {
-        float ks[2] = {1.0f, 1.0f};
-        if constexpr (FP8) {
-          const float* kss = reinterpret_cast<const float*>(smem + st * C::kStageStep + 2 * C::kTile);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = key0 + kt * 16 + g + 8 * e;
-            ks[e] = kss[r];
-            vs[kt][e] = g + 8 * e < cn[kt] ? kss[kUnit + r] : 0.0f;
-            vm = fmaxf(vm, vs[kt][e]);
-          }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float x = FP8 ? s[kt][nt][j] * ks[j >> 1] : s[kt][nt][j];
-            s[kt][nt][j] = g + 8 * (j >> 1) < cn[kt] ? x * sq[nt][j & 1] : kNegInf;
-          }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) mx[nt][j] = fmax3(mx[nt][j], s[kt][nt][j], s[kt][nt][j + 2]);
-      }
-      bool up = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1)
-            mx[nt][j] = fmaxf(mx[nt][j], __shfl_xor_sync(0xffffffffu, mx[nt][j], o));
-          mx[nt][j] = fmaxf(mx[nt][j], m[nt][j]);
-          up |= mx[nt][j] > m[nt][j];
-        }
-      if constexpr (FP8) {
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
-        up |= vm > vmax;
-      }
-      if (__any_sync(0xffffffffu, up)) {
-        const float fv = FP8 && vmax > 0.0f ? vmax / vm : 1.0f;   // powers of two
-        vmax = vm;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float f = m[nt][j] == kNegInf ? 0.0f : ex2(m[nt][j] - mx[nt][j]);
-            m[nt][j] = mx[nt][j];
-            l[nt][j] *= f;
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-              acc[c][nt][j] *= f * fv;
-              acc[c][nt][j + 2] *= f * fv;
-            }
-          }
-      }
-      // weights, their sums, and P^T as the second product's B operand
-      uint32_t pf[KT][NT][2];
-      float vf[KT][2];
-      if constexpr (FP8) {
-        // f16 weights, the largest V scale's at 2^15: a weight keeps its 11
-        // bits down to 2^-29 of that scale
-        const float iv = vmax > 0.0f ? 1.0f / vmax : 1.0f;
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) vf[kt][e] = vs[kt][e] * iv * 32768.0f;
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float mm[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) mm[j] = m[nt][j] == kNegInf ? 0.0f : m[nt][j];
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt) {
-          float p[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            p[j] = ex2(s[kt][nt][j] - mm[j & 1]);
-            l[nt][j & 1] += p[j];
-            if (FP8) p[j] *= vf[kt][j >> 1];
-          }
-          pf[kt][nt][0] = movm(FP8 ? pack_f16(p[0], p[1]) : pack_bf16(p[0], p[1]));
-          pf[kt][nt][1] = movm(FP8 ? pack_f16(p[2], p[3]) : pack_bf16(p[2], p[3]));
-        }
-      }
-      // O^T += V^T P^T; slots behind the last key hold anything, NaN included
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt) {
-        const int c = cn[kt];
-        if (c == 0) continue;
-        auto product = [&](auto whole) {
-          uint32_t m0 = 0xFFFFFFFFu, m1 = 0xFFFFFFFFu;
-          if constexpr (!decltype(whole)::value) {
-            m0 = (2 * tg < c ? 0xFFFFu : 0u) | (2 * tg + 1 < c ? 0xFFFF0000u : 0u);
-            m1 = (2 * tg + 8 < c ? 0xFFFFu : 0u) | (2 * tg + 9 < c ? 0xFFFF0000u : 0u);
-          }
-          if constexpr (!FP8) {
-#pragma unroll
-            for (int cd = 0; cd < D / 16; ++cd) {
-              uint32_t r[4];   // keys 0-7 by d 0-7 and 8-15, then keys 8-15
-              ldsm4t(r, chunk(vbase, key0 + kt * 16 + (lane & 7) + ((lane >> 4) << 3),
-                              2 * cd + ((lane >> 3) & 1)));
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma16816<false>(acc[cd][nt], r[0] & m0, r[1] & m0, r[2] & m1, r[3] & m1,
-                                pf[kt][nt][0], pf[kt][nt][1]);
-            }
-          } else {
-#pragma unroll
-            for (int cd = 0; cd < D / 16; cd += 2) {
-              uint32_t r[4];   // chunk cd by keys 0-7 and 8-15, then chunk cd + 1
-              ldsm4t(r, chunk(vbase, key0 + kt * 16 + (lane & 15), cd + (lane >> 4)));
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                // bytes (key, d), (key, d + 1), (key + 1, d), (key + 1, d + 1)
-                // to the pairs of keys at d and at d + 1
-                const uint32_t x = __byte_perm(r[2 * e], 0, 0x3120);
-                const uint32_t y = __byte_perm(r[2 * e + 1], 0, 0x3120);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                  mma16816<true>(acc[cd + e][nt], e4m3_f16x2_lo(x) & m0, e4m3_f16x2_hi(x) & m0,
-                                 e4m3_f16x2_lo(y) & m1, e4m3_f16x2_hi(y) & m1, pf[kt][nt][0],
-                                 pf[kt][nt][1]);
-              }
-            }
-          }
-        };
-        if (c == 16)
-          product(std::true_type{});
-        else
-          product(std::false_type{});
-      }
+      fold_unit<C, D, FP8, NT>(f, smem + st * C::kStageStep, warp * 16 * KT, cn,
+                               [&](int kt, int e, int, int) { return g + 8 * e < cn[kt]; });
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[st]);
 
     if (cur.k + 1 == cur.units || i + 1 == n_units) {
       // ---- join the four warps ----
-      // (the state of an item may still be read while the next one is written)
-      float* sm_l = sm_m + kWarps * kMaxTileHeads;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], o);
-          if (g == 0) {
-            sm_m[warp * kMaxTileHeads + nt * 8 + 2 * tg + j] = m[nt][j];
-            sm_l[warp * kMaxTileHeads + nt * 8 + 2 * tg + j] = l[nt][j];
-          }
-        }
-      compute_sync();
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float mm = kNegInf;
-          for (int w = 0; w < kWarps; ++w)
-            mm = fmaxf(mm, sm_m[w * kMaxTileHeads + nt * 8 + 2 * tg + j]);
-          float f = m[nt][j] == kNegInf ? 0.0f : ex2(m[nt][j] - mm);
-          if (FP8) f *= vmax * 3.0517578125e-5f;     // back to V's own units
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            acc[c][nt][j] *= f;
-            acc[c][nt][j + 2] *= f;
-          }
-        }
-      float* mine = join + (warp & (C::kJoin - 1)) * (C::kRegs * 32) + lane;
-      for (int r = kWarps / C::kJoin - 1; r >= 0; --r) {
-        if (warp / C::kJoin == r) {
-          const bool put_first = r == kWarps / C::kJoin - 1;
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                float* at = mine + ((c * NT + nt) * 4 + j) * 32;
-                *at = put_first ? acc[c][nt][j] : *at + acc[c][nt][j];
-              }
-        }
-        compute_sync();
-      }
-      // element (head n, pair of d) of the joined numerators
-      auto joined = [&](int nn, int d) -> float {
-        const int dd = d & 15;
-        const int gg = FP8 ? dd >> 1 : dd & 7, hi = FP8 ? dd & 1 : dd >> 3;
-        const int at = (((d >> 4) * NT + (nn >> 3)) * 4 + hi * 2 + (nn & 1)) * 32 + gg * 4 + ((nn & 7) >> 1);
-        float x = join[at];
-#pragma unroll
-        for (int b = 1; b < C::kJoin; ++b) x += join[b * (C::kRegs * 32) + at];
-        return x;
-      };
-      auto state = [&](int nn, float& mm, float& ll) {
-        mm = kNegInf;
-        ll = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm_m[w * kMaxTileHeads + nn]);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float mw = sm_m[w * kMaxTileHeads + nn];
-          ll += mw == kNegInf ? 0.0f : ex2(mw - mm) * sm_l[w * kMaxTileHeads + nn];
-        }
-      };
+      join_warps<C, D, FP8, NT>(f, join, sm_m);
+      auto joined = [&](int nn, int d) { return joined_at<C, D, FP8, NT>(join, nn, d); };
+      auto state = [&](int nn, float& mm, float& ll) { joined_state<C>(sm_m, nn, mm, ll); };
       __nv_bfloat16* out = a.o + (int64_t)cur.row * a.so_t + (int64_t)h0 * a.so_h;
       auto put = [&](int nn, int d, float x, float y, float mm, float ll) {
         const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
@@ -728,6 +796,237 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// ---------------------------------------------------------------------------
+// Sparse attention of many rows
+// ---------------------------------------------------------------------------
+// Rows next to each other read mostly the same pages, and one at a time they
+// are bound by what the L2 cache delivers (5.6 GB for 1300 rows of 1024 keys,
+// 571 us).  So up to 32 (row, query head) columns of a sequence share their
+// loads: a first kernel joins their lists, each page with the bits of the
+// rows that read it, and the columns of the others see none of its keys.
+//
+// A weight of zero times a value that is not finite would spoil the columns
+// that do not see it.  Rows with a result that is not finite are therefore
+// flagged and done again on their own, where hidden keys are never multiplied.
+
+// Joint page lists, pages in order.  Where a row lists a page twice, the
+// tile's lists stand one after the other instead, so that it counts twice.
+__global__ void __launch_bounds__(256) cache_lists_kernel(const CacheArgs a) {
+  extern __shared__ uint32_t bits[];   // rows that read a page, for each page
+  __shared__ int wsum[8];
+  __shared__ int twice;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hk = blockIdx.y;
+  const RowTile tile = row_tile(a, blockIdx.x, a.tile_rows);
+  const int64_t item = (int64_t)blockIdx.x * a.Hkv + hk;
+  if (hk == 0)
+    for (int t = tile.t0 + tid; t < tile.t1; t += 256) {
+      a.row_flags[t] = 0;
+      row_pos(a, t, tile.s);           // (reports a row without a position)
+    }
+  if (tile.t0 >= tile.t1) return;
+  const int len = seq_len(a, tile.s);
+  const int pages = (len + a.page_size - 1) >> a.ps_log2, rows = tile.t1 - tile.t0;
+  for (int j = tid; j < pages; j += 256) bits[j] = 0;
+  if (tid == 0) twice = 0;
+  __syncthreads();
+  // row r sees the pages up to its own
+  const int64_t pos0 = (int64_t)len - (a.cu[tile.s + 1] - tile.t0);
+  auto entry = [&](int i, int& r) -> int {
+    r = i / a.n_select;
+    const int e = a.sel[((int64_t)(tile.t0 + r) * a.Hkv + hk) * a.n_select + (i - r * a.n_select)];
+    return e >= 0 && e < pages && (int64_t)e << a.ps_log2 <= pos0 + r ? e : -1;
+  };
+  for (int i = tid; i < rows * a.n_select; i += 256) {
+    int r;
+    const int e = entry(i, r);
+    if (e >= 0 && atomicOr(&bits[e], 1u << r) >> r & 1) twice = 1;
+  }
+  __syncthreads();
+  int2* out = a.lists + item * a.list_cap;
+  if (twice) {
+    for (int i = tid; i < rows * a.n_select; i += 256) {
+      int r;
+      const int e = entry(i, r);
+      out[i] = make_int2(max(e, 0), e >= 0 ? 1 << r : 0);
+    }
+    if (tid == 0) a.list_n[item] = rows * a.n_select;
+    return;
+  }
+  int at = 0;
+  for (int base = 0; base < pages; base += 256) {
+    const int j = base + tid;
+    const uint32_t m = j < pages ? bits[j] : 0u;
+    const uint32_t b = __ballot_sync(0xffffffffu, m != 0);
+    __syncthreads();
+    if (lane == 0) wsum[warp] = __popc(b);
+    __syncthreads();
+    int k = at;
+    for (int w = 0; w < 8; ++w) {
+      if (w < warp) k += wsum[w];
+      at += wsum[w];
+    }
+    if (m) out[k + __popc(b & ((1u << lane) - 1))] = make_int2(j, (int)m);
+  }
+  if (tid == 0) a.list_n[item] = at;
+}
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__(kThreads, 1)
+    cache_group_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                       const CacheArgs a, int tiles) {
+  constexpr int NT = 2;                // column tiles of a warp; two column groups
+  using C = Cfg<D, FP8, NT, true>;
+  constexpr int KT = C::kKT, KW = C::kKeyWarps, kGroups = C::kUnit / 16;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // of each 16 keys of a stage: their first position, the rows that read them,
+  // how many exist
+  int4* info = reinterpret_cast<int4*>(smem + C::oCnt);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::oBar);
+  uint64_t* empty = full + C::kStages;
+  int* misc = reinterpret_cast<int*>(smem + C::oMisc);
+  const AbortCtx abort{misc, a.status};
+  if (tid == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kWarps);
+    }
+    misc[0] = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const int items = tiles * a.Hkv, ppu = C::kUnit >> a.ps_log2;
+  auto units_of = [&](int n) { return max(1, (n + ppu - 1) / ppu); };
+
+  if (warp == kWarps) {
+    // ---- loads: lane i brings page i of the unit ----
+    int issued = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+      const RowTile tile = row_tile(a, item / a.Hkv, a.tile_rows);
+      if (tile.t0 >= tile.t1) continue;
+      const int hk = item % a.Hkv, n = a.list_n[item], units = units_of(n), len = seq_len(a, tile.s);
+      const int2* list = a.lists + (int64_t)item * a.list_cap;
+      int2 next = lane < ppu && lane < n ? list[lane] : make_int2(0, 0);
+      for (int u = 0; u < units; ++u) {
+        const int2 e = next;
+        const int at = (u + 1) * ppu + lane;
+        next = lane < ppu && at < n ? list[at] : make_int2(0, 0);
+        int vc = e.y ? min(a.page_size, max(0, len - (e.x << a.ps_log2))) : 0, page = 0;
+        if (vc > 0) {
+          page = page_of(a, tile.s, e.x);
+          if (page < 0) vc = 0;
+        }
+        const uint32_t live = __ballot_sync(0xffffffffu, vc > 0);
+        const int st = issued % C::kStages;
+        if (issued >= C::kStages && !mbar_wait(&empty[st], ((issued / C::kStages) - 1) & 1, abort, 1)) {
+          ok = false;
+          break;
+        }
+        unsigned char* stage = smem + st * C::kStageStep;
+        const int src = (lane & (kGroups - 1)) >> (a.ps_log2 - 4);
+        const int first = 16 * (lane & ((1 << (a.ps_log2 - 4)) - 1));
+        const int4 w = make_int4((__shfl_sync(0xffffffffu, e.x, src) << a.ps_log2) + first,
+                                 __shfl_sync(0xffffffffu, e.y, src),
+                                 min(16, max(0, __shfl_sync(0xffffffffu, vc, src) - first)), 0);
+        if (lane < kGroups) info[st * kGroups + lane] = w;
+        __syncwarp();
+        if (lane == 0)
+          mbar_arrive_expect_tx(&full[st], (uint32_t)a.page_size * (2 * C::kRow + (FP8 ? 8 : 0)) * __popc(live));
+        __syncwarp();
+        if (vc > 0) {
+          const int off = lane << a.ps_log2;
+#pragma unroll
+          for (int c = 0; c < C::kCols; ++c) {
+            unsigned char* dst = stage + c * (C::kUnit * C::kColB) + off * C::kColB;
+            tma_load_4d(dst, &mk, &full[st], c * 64, 0, hk, page);
+            tma_load_4d(dst + C::kTile, &mv, &full[st], c * 64, 0, hk, page);
+          }
+          if (FP8) {
+            const int64_t so = ((int64_t)page * a.Hkv + hk) << a.ps_log2;
+            bulk_load(stage + 2 * C::kTile + off * 4, a.k_scale + so, a.page_size * 4, &full[st]);
+            bulk_load(stage + 2 * C::kTile + C::kScales + off * 4, a.v_scale + so, a.page_size * 4, &full[st]);
+          }
+        }
+        ++issued;
+      }
+    }
+    if (!ok)                           // nothing may still be writing shared memory
+      for (int i = max(0, issued - C::kStages); i < issued; ++i)
+        mbar_wait_drain(&full[i % C::kStages], (i / C::kStages) & 1);
+    return;
+  }
+
+  // ---- compute: 4 warps along the keys, 2 along the columns ----
+  const int g = lane >> 2, tg = lane & 3, kw = warp % KW, cg = warp / KW;
+  Fold<D, NT> f;
+  float* join = reinterpret_cast<float*>(smem + C::oJoin);
+  float* const sm0 = reinterpret_cast<float*>(smem + C::oML);
+  int turn = 0, taken = 0;
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const RowTile tile = row_tile(a, item / a.Hkv, a.tile_rows);
+    if (tile.t0 >= tile.t1) continue;
+    const int hk = item % a.Hkv, units = units_of(a.list_n[item]), len = seq_len(a, tile.s);
+    const int cols = (tile.t1 - tile.t0) * a.G, t0 = tile.t0;
+    const int pos0 = len - (a.cu[tile.s + 1] - t0);        // position of the tile's first row
+    f.vmax = 0.0f;
+    int last[NT][2];                                       // last position that a lane's columns see
+    uint32_t bit[NT][2];                                   // and their rows' bits
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int c = cg * 16 + nt * 8 + g, r = c / a.G;
+      fold_query<D, FP8, NT>(f, nt, a.q + (int64_t)(t0 + r) * a.sq_t + (int64_t)(hk * a.G + c - r * a.G) * a.sq_h,
+                             c < cols, a.scale_log2);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int cc = cg * 16 + nt * 8 + 2 * tg + j, rr = cc / a.G;
+        last[nt][j] = min(pos0 + rr, len - 1);
+        bit[nt][j] = cc < cols ? 1u << rr : 0u;
+      }
+    }
+    uint32_t mine = 0;                                     // rows of this warp's columns
+    for (int c = cg * 16; c < min(cols, cg * 16 + 16); ++c) mine |= 1u << (c / a.G);
+
+    for (int u = 0; u < units; ++u, ++taken) {
+      const int st = taken % C::kStages;
+      const bool ok = mbar_wait(&full[st], (taken / C::kStages) & 1, abort, 2);
+      int cn[KT], kb[KT], any = 0;
+      uint32_t rows[KT];
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) {
+        const int4 w = info[st * kGroups + KT * kw + kt];
+        kb[kt] = w.x;
+        rows[kt] = w.y & mine;
+        cn[kt] = ok && rows[kt] ? w.z : 0;
+        any |= cn[kt];
+      }
+      if (any)
+        fold_unit<C, D, FP8, NT>(f, smem + st * C::kStageStep, kw * 16 * KT, cn, [&](int kt, int e, int nt, int j) {
+          return (rows[kt] & bit[nt][j]) != 0 && g + 8 * e < cn[kt] && kb[kt] + g + 8 * e <= last[nt][j];
+        });
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+    }
+
+    float* sm = sm0 + turn * (2 * kWarps * kMaxTileHeads);
+    join_warps<C, D, FP8, NT>(f, join, sm);
+    for (int e = tid; e < cols * (D / 2); e += 32 * kWarps) {
+      const int c = e / (D / 2), d = 2 * (e - c * (D / 2)), r = c / a.G, h = hk * a.G + c - r * a.G;
+      float mm, ll;
+      joined_state<C>(sm, c, mm, ll);
+      const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+      const float x = joined_at<C, D, FP8, NT>(join, c, d) * inv, y = joined_at<C, D, FP8, NT>(join, c, d + 1) * inv;
+      const float big = __int_as_float(0x7f800000);
+      if (!(fabsf(x) < big && fabsf(y) < big && ll < big && (mm < big))) a.row_flags[t0 + r] = 1;
+      *reinterpret_cast<uint32_t*>(a.o + (int64_t)(t0 + r) * a.so_t + (int64_t)h * a.so_h + d) = pack_bf16(x, y);
+      if (d == 0 && a.lse)
+        a.lse[(int64_t)(t0 + r) * a.H + h] = ll == 0.0f ? -big : (mm + log2f(ll)) * 0.6931471805599453f;
+    }
+    turn ^= 1;
+  }
+}
+
 template <int D, bool FP8, int NT, bool SPARSE>
 cudaError_t run(const CacheArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
   using C = Cfg<D, FP8, NT>;
@@ -763,8 +1062,48 @@ cudaError_t pick(const CacheArgs& a, const CUtensorMap& mk, const CUtensorMap& m
 
 }  // namespace
 
-cudaError_t launch_cache_attn(const CacheArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
+template <int D, bool FP8>
+static cudaError_t run_group(const CacheArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int64_t tiles,
+                             int sms, int dev, cudaStream_t s) {
+  using C = Cfg<D, FP8, 2, true>;
+  static_assert(C::kBytes <= 232448, "shared memory");
+  static OncePerDevice once_l, once_g;
+  cudaError_t e = once_l.allow(reinterpret_cast<const void*>(cache_lists_kernel), dev, kMaxSelectPages * 4);
+  if (e != cudaSuccess) return e;
+  cache_lists_kernel<<<dim3((unsigned)tiles, a.Hkv), 256, a.max_pages * 4, s>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  auto k = cache_group_kernel<D, FP8>;
+  if ((e = once_g.allow(reinterpret_cast<const void*>(k), dev, C::kBytes)) != cudaSuccess) return e;
+  k<<<(unsigned)(tiles * a.Hkv < sms ? tiles * a.Hkv : sms), kThreads, C::kBytes, s>>>(mk, mv, a, (int)tiles);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_attn(const CacheArgs& args, const CUtensorMap& mk, const CUtensorMap& mv,
                               bool sparse, cudaStream_t s) {
+  CacheArgs a = args;
+  a.row_flags = nullptr;
+  // rows together where two tiles or more fall on each SM (fewer leave the
+  // GPU idle: the rows' own items split over it)
+  const int rows = sparse && a.cu ? group_rows(a.G, a.T, a.S, a.max_pages) : 0;
+  if (rows) {
+    int dev = 0, sms = 0;
+    cudaError_t e = device_sms(dev, sms);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = group_tiles(rows, a.T, a.S);
+    if ((int64_t)a.T / rows * a.Hkv >= 2 * sms && tiles * a.Hkv < 0x7fffffff) {
+      a.tile_rows = rows;
+      a.list_cap = rows * a.n_select;
+      char* w = reinterpret_cast<char*>(a.scratch);
+      a.lists = reinterpret_cast<int2*>(w);
+      a.list_n = reinterpret_cast<int*>(a.lists + tiles * a.Hkv * a.list_cap);
+      a.row_flags = a.list_n + tiles * a.Hkv;
+      if (a.d == 128)
+        e = a.fp8 ? run_group<128, true>(a, mk, mv, tiles, sms, dev, s) : run_group<128, false>(a, mk, mv, tiles, sms, dev, s);
+      else
+        e = a.fp8 ? run_group<64, true>(a, mk, mv, tiles, sms, dev, s) : run_group<64, false>(a, mk, mv, tiles, sms, dev, s);
+      if (e != cudaSuccess) return e;
+    }
+  }
   if (a.d == 128)
     return a.fp8 ? pick<128, true>(a, mk, mv, sparse, s) : pick<128, false>(a, mk, mv, sparse, s);
   return a.fp8 ? pick<64, true>(a, mk, mv, sparse, s) : pick<64, false>(a, mk, mv, sparse, s);

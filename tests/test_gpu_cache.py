@@ -477,6 +477,101 @@ def test_sparse(cuda_ok, case, fp8):
     st.check(O, lse, lists.tolist())
 
 
+# enough rows for tiles that share their pages' loads
+MANY = [
+    ([300, 40], [400, 333], dict(H=16, Hkv=4, pad=5)),
+    ([0, 500, 3], [510, 0, 300], dict(H=40, Hkv=8, d=64, ps=16, n_select=7, layout="nhd")),
+    ([2000], [640], dict(H=32, Hkv=2, ps=128, n_select=5)),
+    ([10, 70], [2400, 100], dict(H=2, Hkv=2, d=64, ps=32, n_select=3)),
+]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_sparse_many_rows(cuda_ok, case, fp8):
+    old, new, kw = MANY[case]
+    st = Step(old, new, fp8=fp8, seed=400 + case, **kw)
+    st.append()
+    # neighbours agree on most pages
+    K, W = st.p.n_select, st.W
+    base = torch.randint(-1, W + 1, (st.T // 16 + 1, st.Hkv, K), generator=st.g, dtype=torch.int32)
+    lists = base.repeat_interleave(16, 0)[:st.T].clone()
+    own = torch.randint(-1, W + 1, (st.T, st.Hkv, K), generator=st.g, dtype=torch.int32)
+    lists = torch.where(torch.rand(st.T, st.Hkv, K, generator=st.g) < 0.3, own, lists)
+    lists[5] = -1
+    O, lse = st.sparse(lists.to(DEV))
+    assert st.status() == 0
+    assert torch.equal(O, st.sparse(lists.to(DEV))[0])
+    check_some(st, O, lse, lists.tolist(), every=7)
+
+
+def check_some(st, O, lse, lists, every):
+    """`check` for every `every`-th row, and the padding."""
+    rows = [x for x in OC.rows_of(st.lens, st.cu, st.S)]
+    keep = {t for t, _, _ in rows if t % every == 0 or t in (5, rows[-1][0])}
+    real = OC.rows_of
+    try:
+        OC.rows_of = lambda *a: [x for x in rows if x[0] in keep]
+        T = st.T
+        used = {t for t, _, _ in rows}
+        for t in range(T):
+            if t not in used:
+                assert (O[t] == 7).all() and (lse[t] == 7).all()
+        st.T = 0
+        st.check(O, lse, lists)
+    finally:
+        OC.rows_of, st.T = real, T
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_sparse_many_rows_hidden_values_that_are_not_finite(cuda_ok, fp8):
+    # a page with a NaN in V (a NaN scale, FP8): rows that do not list it, and
+    # rows before that key, must not see it
+    st = Step([0], [800], H=16, Hkv=4, d=64, ps=16, fp8=fp8, n_select=3, seed=7)
+    st.append()
+    bad_pos = 411
+    pg, slot = st.table[0][bad_pos // 16], bad_pos % 16
+    if fp8:
+        st.cache.v_scale[pg, 2, slot] = float("nan")
+    else:
+        st.cache.v[pg, 2, slot, 9] = float("nan")
+        st.cache.v[pg, 1, slot, 3] = float("inf")
+    lists = torch.randint(0, 50, (800, 4, 3), generator=st.g, dtype=torch.int32)
+    lists[400:500, :, 0] = 25                        # page 25 holds key 411
+    lists[:, :, 1] = torch.where(lists[:, :, 1] == 25, 26, lists[:, :, 1])
+    O, lse = st.sparse(lists.to(DEV))
+    L = lists.tolist()
+    sees = [t >= bad_pos and 25 in L[t][2] for t in range(800)]
+    got = O[:, 8:12].isnan().any(-1).any(-1).tolist()
+    assert got == sees
+    if not fp8:
+        sees1 = [t >= bad_pos and 25 in L[t][1] for t in range(800)]
+        assert O[:, 4:8].isinf().any(-1).any(-1).tolist() == sees1
+        assert O[:, 4:8].isnan().sum() == 0
+    clean = [t for t in range(800) if not any(t >= bad_pos and 25 in L[t][h] for h in range(4))]
+    for x in (st.cache.v,) if not fp8 else ():
+        x[pg, 2, slot, 9] = 0.0
+        x[pg, 1, slot, 3] = 0.0
+    if fp8:
+        st.cache.v_scale[pg, 2, slot] = 1.0
+    real = OC.rows_of
+    try:
+        OC.rows_of = lambda *a: [(t, 0, t) for t in clean[::9]]
+        st.T = 0
+        st.check(O, lse, L)
+    finally:
+        OC.rows_of = real
+
+
+def test_sparse_many_rows_a_page_twice(cuda_ok):
+    st = Step([100], [700], H=8, Hkv=8, d=64, ps=32, n_select=4, seed=8)
+    st.append()
+    lists = torch.randint(0, 20, (700, 8, 4), generator=st.g, dtype=torch.int32)
+    lists[100:130, 3, 2] = lists[100:130, 3, 0]
+    O, lse = st.sparse(lists.to(DEV))
+    check_some(st, O, lse, lists.tolist(), every=10)
+
+
 def test_sparse_over_every_page_is_dense_causal(cuda_ok):
     st = Step([70, 0], [50, 90], n_select=4, seed=11)
     st.append()
