@@ -39,14 +39,13 @@
 namespace ta {
 namespace {
 
-constexpr int kWarps = 8;                // computing warps
-constexpr int kThreads = 32 * (kWarps + 1);
-
 template <int D, bool FP8, int NT, bool GROUP = false>
 struct Cfg {
   static constexpr int kRow = D * (FP8 ? 1 : 2);          // bytes of a key
   static constexpr int kKT = !GROUP && kRow > 128 ? 1 : 2;   // 16-key tiles of a warp
-  static constexpr int kKeyWarps = GROUP ? 4 : kWarps;    // warps side by side along the keys
+  static constexpr int kWarps = GROUP ? 16 : 8;           // computing warps, one more loads
+  static constexpr int kThreads = 32 * (kWarps + 1);
+  static constexpr int kKeyWarps = GROUP ? 4 : 8;         // of these, side by side along the keys
   static constexpr int kUnit = kKeyWarps * 16 * kKT;      // keys of a unit (one stage)
   static constexpr int kCols = kRow > 128 ? 2 : 1;        // 128-byte columns of a row
   static constexpr int kColB = kRow / kCols;              // 128 or 64
@@ -59,7 +58,7 @@ struct Cfg {
   static constexpr int kJoin = GROUP ? 1 : (NT == 1 ? 4 : 2);   // key warps that join at a time
   static constexpr int kColGroups = kWarps / kKeyWarps;
   static constexpr int oML = oJoin + kColGroups * kJoin * kRegs * 32 * 4;
-  static constexpr int oCnt = oML + 2 * 2 * kWarps * kMaxTileHeads * 4;  // m, l; items take turns
+  static constexpr int oCnt = oML + 2 * 2 * kWarps * 8 * NT * 4;         // m, l; items take turns
   static constexpr int oBar = oCnt + kStages * (kUnit / 16) * (GROUP ? 16 : 4);
   static constexpr int oMisc = oBar + 2 * kStages * 8;
   static constexpr int oPre = oMisc + 128;
@@ -136,8 +135,9 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       "l"(src), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
 }
+template <int WARPS>
 __device__ __forceinline__ void compute_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * WARPS) : "memory");
 }
 
 // Where a run of units stands: row, head group, and unit of that item.
@@ -447,7 +447,7 @@ __device__ __forceinline__ void fold_unit(Fold<D, NT>& f, const unsigned char* s
 }
 
 // Joins the key warps of each column group, whose columns and numerators the
-// readers below then give.  sm: maxima and sums, [warp][16] each; an item's may
+// readers below then give.  sm: maxima and sums, [warp][8 NT] each; an item's may
 // still be read while the next one's are written, so items take turns.
 template <class C, int D, bool FP8, int NT>
 __device__ __forceinline__ void join_warps(Fold<D, NT>& f, float* join, float* sm) {
@@ -456,7 +456,7 @@ __device__ __forceinline__ void join_warps(Fold<D, NT>& f, float* join, float* s
   const int kw = warp % KW, cg = warp / KW;
   const float kNegInf = -__int_as_float(0x7f800000);
   float* sm_m = sm;
-  float* sm_l = sm + kWarps * kMaxTileHeads;
+  float* sm_l = sm + C::kWarps * 8 * NT;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -464,18 +464,18 @@ __device__ __forceinline__ void join_warps(Fold<D, NT>& f, float* join, float* s
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) f.l[nt][j] += __shfl_xor_sync(0xffffffffu, f.l[nt][j], o);
       if (g == 0) {
-        sm_m[warp * kMaxTileHeads + nt * 8 + 2 * tg + j] = f.m[nt][j];
-        sm_l[warp * kMaxTileHeads + nt * 8 + 2 * tg + j] = f.l[nt][j];
+        sm_m[warp * 8 * NT + nt * 8 + 2 * tg + j] = f.m[nt][j];
+        sm_l[warp * 8 * NT + nt * 8 + 2 * tg + j] = f.l[nt][j];
       }
     }
-  compute_sync();
+  compute_sync<C::kWarps>();
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       float mm = kNegInf;
       for (int w = 0; w < KW; ++w)
-        mm = fmaxf(mm, sm_m[(cg * KW + w) * kMaxTileHeads + nt * 8 + 2 * tg + j]);
+        mm = fmaxf(mm, sm_m[(cg * KW + w) * 8 * NT + nt * 8 + 2 * tg + j]);
       float x = f.m[nt][j] == kNegInf ? 0.0f : ex2(f.m[nt][j] - mm);
       if (FP8) x *= f.vmax * 3.0517578125e-5f;     // back to V's own units
 #pragma unroll
@@ -498,7 +498,7 @@ __device__ __forceinline__ void join_warps(Fold<D, NT>& f, float* join, float* s
             *at = put_first ? f.acc[c][nt][j] : *at + f.acc[c][nt][j];
           }
     }
-    compute_sync();
+    compute_sync<C::kWarps>();
   }
 }
 // Numerator d of column nn (8 NT of them in a group).
@@ -513,29 +513,30 @@ __device__ __forceinline__ float joined_at(const float* join, int nn, int d) {
   for (int k = 1; k < C::kJoin; ++k) x += b[k * (C::kRegs * 32)];
   return x;
 }
-// Maximum and sum of column nn, 16 at most in a group.
-template <class C>
+// Maximum and sum of column nn.
+template <class C, int NT>
 __device__ __forceinline__ void joined_state(const float* sm, int nn, float& mm, float& ll) {
-  constexpr int KW = C::kKeyWarps;
+  constexpr int KW = C::kKeyWarps, N = 8 * NT;
   const float kNegInf = -__int_as_float(0x7f800000);
-  const float* sm_m = sm + (nn / kMaxTileHeads) * KW * kMaxTileHeads + nn % kMaxTileHeads;
-  const float* sm_l = sm_m + kWarps * kMaxTileHeads;
+  const float* sm_m = sm + (nn / N) * KW * N + nn % N;
+  const float* sm_l = sm_m + C::kWarps * N;
   mm = kNegInf;
   ll = 0.0f;
 #pragma unroll
-  for (int w = 0; w < KW; ++w) mm = fmaxf(mm, sm_m[w * kMaxTileHeads]);
+  for (int w = 0; w < KW; ++w) mm = fmaxf(mm, sm_m[w * N]);
 #pragma unroll
   for (int w = 0; w < KW; ++w) {
-    const float mw = sm_m[w * kMaxTileHeads];
-    ll += mw == kNegInf ? 0.0f : ex2(mw - mm) * sm_l[w * kMaxTileHeads];
+    const float mw = sm_m[w * N];
+    ll += mw == kNegInf ? 0.0f : ex2(mw - mm) * sm_l[w * N];
   }
 }
 
 template <int D, bool FP8, int NT, bool SPARSE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, FP8, NT>::kThreads, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                       const CacheArgs a) {
   using C = Cfg<D, FP8, NT>;
+  constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
   constexpr int NH = 8 * NT;                       // query heads of an item
   constexpr int KT = C::kKT, kUnit = C::kUnit, kGroups = kUnit / 16;
   extern __shared__ unsigned char smem_raw[];
@@ -725,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- join the four warps ----
       join_warps<C, D, FP8, NT>(f, join, sm_m);
       auto joined = [&](int nn, int d) { return joined_at<C, D, FP8, NT>(join, nn, d); };
-      auto state = [&](int nn, float& mm, float& ll) { joined_state<C>(sm_m, nn, mm, ll); };
+      auto state = [&](int nn, float& mm, float& ll) { joined_state<C, NT>(sm_m, nn, mm, ll); };
       __nv_bfloat16* out = a.o + (int64_t)cur.row * a.so_t + (int64_t)h0 * a.so_h;
       auto put = [&](int nn, int d, float x, float y, float mm, float ll) {
         const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
@@ -762,11 +763,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         __threadfence();
-        compute_sync();
+        compute_sync<C::kWarps>();
         if (tid == 0)
           misc[1] = atomicInc(reinterpret_cast<unsigned int*>(a.counters) + cf, (unsigned)(cl - cf)) ==
                     (unsigned)(cl - cf);
-        compute_sync();
+        compute_sync<C::kWarps>();
         if (misc[1]) {
           __threadfence();
           for (int e = tid; e < nh * (D / 2); e += 32 * kWarps) {
@@ -790,7 +791,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fresh = true;
       turn ^= 1;
-      sm_m = sm_m0 + turn * (2 * kWarps * kMaxTileHeads);
+      sm_m = sm_m0 + turn * (2 * C::kWarps * 8 * NT);
     }
     if (i + 1 < n_units) cur.next(a, pre, HX);
   }
@@ -871,11 +872,12 @@ __global__ void __launch_bounds__(256) cache_lists_kernel(const CacheArgs a) {
 }
 
 template <int D, bool FP8>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, FP8, 1, true>::kThreads, 1)
     cache_group_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                        const CacheArgs a, int tiles) {
-  constexpr int NT = 2;                // column tiles of a warp; two column groups
+  constexpr int NT = 1;                // column tiles of a warp
   using C = Cfg<D, FP8, NT, true>;
+  constexpr int kWarps = C::kWarps;
   constexpr int KT = C::kKT, KW = C::kKeyWarps, kGroups = C::kUnit / 16;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -958,7 +960,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
 
-  // ---- compute: 4 warps along the keys, 2 along the columns ----
+  // ---- compute: 4 warps along the keys by 4 along the columns ----
   const int g = lane >> 2, tg = lane & 3, kw = warp % KW, cg = warp / KW;
   Fold<D, NT> f;
   float* join = reinterpret_cast<float*>(smem + C::oJoin);
@@ -975,18 +977,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t bit[NT][2];                                   // and their rows' bits
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int c = cg * 16 + nt * 8 + g, r = c / a.G;
+      const int c = cg * 8 * NT + nt * 8 + g, r = c / a.G;
       fold_query<D, FP8, NT>(f, nt, a.q + (int64_t)(t0 + r) * a.sq_t + (int64_t)(hk * a.G + c - r * a.G) * a.sq_h,
                              c < cols, a.scale_log2);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int cc = cg * 16 + nt * 8 + 2 * tg + j, rr = cc / a.G;
+        const int cc = cg * 8 * NT + nt * 8 + 2 * tg + j, rr = cc / a.G;
         last[nt][j] = min(pos0 + rr, len - 1);
         bit[nt][j] = cc < cols ? 1u << rr : 0u;
       }
     }
     uint32_t mine = 0;                                     // rows of this warp's columns
-    for (int c = cg * 16; c < min(cols, cg * 16 + 16); ++c) mine |= 1u << (c / a.G);
+    for (int c = cg * 8 * NT; c < min(cols, (cg + 1) * 8 * NT); ++c) mine |= 1u << (c / a.G);
 
     for (int u = 0; u < units; ++u, ++taken) {
       const int st = taken % C::kStages;
@@ -1009,12 +1011,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&empty[st]);
     }
 
-    float* sm = sm0 + turn * (2 * kWarps * kMaxTileHeads);
+    float* sm = sm0 + turn * (2 * C::kWarps * 8 * NT);
     join_warps<C, D, FP8, NT>(f, join, sm);
     for (int e = tid; e < cols * (D / 2); e += 32 * kWarps) {
       const int c = e / (D / 2), d = 2 * (e - c * (D / 2)), r = c / a.G, h = hk * a.G + c - r * a.G;
       float mm, ll;
-      joined_state<C>(sm, c, mm, ll);
+      joined_state<C, NT>(sm, c, mm, ll);
       const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
       const float x = joined_at<C, D, FP8, NT>(join, c, d) * inv, y = joined_at<C, D, FP8, NT>(join, c, d + 1) * inv;
       const float big = __int_as_float(0x7f800000);
@@ -1046,7 +1048,7 @@ cudaError_t run(const CacheArgs& a, const CUtensorMap& mk, const CUtensorMap& mv
   int64_t grid = (SPARSE ? a.T : a.S) * HX * per;
   if (grid > sms) grid = sms;
   if (grid > kMaxAttnCtas) grid = kMaxAttnCtas;
-  k<<<(int)grid, kThreads, bytes, s>>>(mk, mv, a);
+  k<<<(int)grid, C::kThreads, bytes, s>>>(mk, mv, a);
   return cudaGetLastError();
 }
 
@@ -1065,7 +1067,7 @@ cudaError_t pick(const CacheArgs& a, const CUtensorMap& mk, const CUtensorMap& m
 template <int D, bool FP8>
 static cudaError_t run_group(const CacheArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int64_t tiles,
                              int sms, int dev, cudaStream_t s) {
-  using C = Cfg<D, FP8, 2, true>;
+  using C = Cfg<D, FP8, 1, true>;
   static_assert(C::kBytes <= 232448, "shared memory");
   static OncePerDevice once_l, once_g;
   cudaError_t e = once_l.allow(reinterpret_cast<const void*>(cache_lists_kernel), dev, kMaxSelectPages * 4);
@@ -1074,7 +1076,7 @@ static cudaError_t run_group(const CacheArgs& a, const CUtensorMap& mk, const CU
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   auto k = cache_group_kernel<D, FP8>;
   if ((e = once_g.allow(reinterpret_cast<const void*>(k), dev, C::kBytes)) != cudaSuccess) return e;
-  k<<<(unsigned)(tiles * a.Hkv < sms ? tiles * a.Hkv : sms), kThreads, C::kBytes, s>>>(mk, mv, a, (int)tiles);
+  k<<<(unsigned)(tiles * a.Hkv < sms ? tiles * a.Hkv : sms), C::kThreads, C::kBytes, s>>>(mk, mv, a, (int)tiles);
   return cudaGetLastError();
 }
 
