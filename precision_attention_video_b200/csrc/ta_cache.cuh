@@ -69,6 +69,11 @@ constexpr int kGroupCols = 32;
 inline int group_rows(int G, int64_t T, int64_t S, int max_pages) {
   return G <= kGroupCols / 2 && T >= 4 * S && max_pages <= kMaxSelectPages ? kGroupCols / G : 0;
 }
+// The same in tiles of 128 columns, at most 32 rows (the bits of a list).
+inline int tile_rows(int G, int64_t T, int64_t S, int max_pages) {
+  if (G > 64 || T < 4 * S || max_pages > kMaxSelectPages) return 0;
+  return 128 / G < 32 ? 128 / G : 32;
+}
 inline int64_t group_tiles(int rows, int64_t T, int64_t S) { return T / rows + S; }
 
 // Doubles of a row of the choice's scratch: whole tiles of 128 pages.

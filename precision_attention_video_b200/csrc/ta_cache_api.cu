@@ -44,10 +44,15 @@ size_t select_bytes(const ta_cache_params* p) {
 // Sparse attention's: joint page lists and their lengths, the rows' flags.
 size_t sparse_bytes(const ta_cache_params* p) {
   if (p->n_select <= 0) return 0;
-  const int rows = ta::group_rows(p->H / p->Hkv, p->T, p->S, p->max_pages);
-  if (!rows) return 0;
-  const size_t items = (size_t)ta::group_tiles(rows, p->T, p->S) * p->Hkv;
-  return items * ((size_t)rows * p->n_select * 8 + 4) + (size_t)p->T * 4;
+  size_t most = 0;
+  for (const int rows : {ta::group_rows(p->H / p->Hkv, p->T, p->S, p->max_pages),
+                         ta::tile_rows(p->H / p->Hkv, p->T, p->S, p->max_pages)}) {
+    if (!rows) continue;
+    const size_t items = (size_t)ta::group_tiles(rows, p->T, p->S) * p->Hkv;
+    const size_t n = items * ((size_t)rows * p->n_select * 8 + 4) + (size_t)p->T * 4;
+    most = n > most ? n : most;
+  }
+  return most;
 }
 size_t scratch_bytes(const ta_cache_params* p) {
   const size_t a = select_bytes(p), b = sparse_bytes(p);

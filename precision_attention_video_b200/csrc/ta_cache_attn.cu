@@ -1029,6 +1029,276 @@ __global__ void __launch_bounds__(Cfg<D, FP8, 1, true>::kThreads, 1)
   }
 }
 
+// The same for bf16 caches and tiles of up to 128 (row, query head) pairs, on
+// tcgen05: the pairs are the 128 rows of S = Q K^T and O += P V, a thread of
+// the softmax has one of them, S and P (bf16, over S's own columns) and O
+// stand in TMEM.  A block has one K and one V buffer: K of the next unit loads
+// while this one's softmax runs, V while the next S does, and two blocks share
+// an SM.  With the mma.sync kernel above 1330 rows took 245 us, bound by its
+// instructions (32 columns for each key read); here a key serves 128 rows.
+//
+// The running maximum may lag: numerators and sums move to a new maximum only
+// when it is more than 2^8 above the old one (P then stays below 2^8, far from
+// any limit), so that O is seldom read back and rescaled.
+template <int D>
+struct TileSmem {
+  static constexpr int kRows = 128 * 128;          // bytes of 128 rows by 64 elements
+  static constexpr int kOp = D / 64 * kRows;       // one operand
+  static constexpr int oQ = 0, oK = kOp, oV = 2 * kOp;
+  static constexpr int oInfo = 3 * kOp;            // [2][8] int4: the pages of a unit
+  static constexpr int oBar = oInfo + 256;
+  static constexpr int kBytes = oBar + 64 + 1024;  // 1024 to align
+};
+
+template <int D>
+__global__ void __launch_bounds__(192, 2)
+    cache_tile_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                      const CacheArgs a) {
+  using L = TileSmem<D>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int hk = blockIdx.y;
+  const RowTile tile = row_tile(a, blockIdx.x, a.tile_rows);
+  if (tile.t0 >= tile.t1) return;
+  const int64_t item = (int64_t)blockIdx.x * a.Hkv + hk;
+  const int n = a.list_n[item], ppu = 128 >> a.ps_log2, units = max(1, (n + ppu - 1) / ppu);
+  const int len = seq_len(a, tile.s), t0 = tile.t0, pairs = (tile.t1 - t0) * a.G;
+
+  int4* info = reinterpret_cast<int4*>(smem + L::oInfo);   // first position, rows' bits, keys that exist
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::oBar);
+  uint64_t *full_k = bars, *full_v = bars + 1, *s_ready = bars + 2, *p_ready = bars + 3, *o_done = bars + 4;
+  uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 5);
+  int* flag = reinterpret_cast<int*>(bars + 6);
+  const AbortCtx abort{flag, a.status};
+  if (tid == 0) {
+    mbar_init(full_k, 1);
+    mbar_init(full_v, 1);
+    mbar_init(s_ready, 1);
+    mbar_init(p_ready, 128);
+    mbar_init(o_done, 1);
+    *flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 5) {
+    tmem_alloc(slot, 256);
+    tmem_relinquish();
+  }
+  // pair i of the tile: row i / G, query head i % G of the key head
+  const int r = tid / a.G, h = hk * a.G + tid - r * a.G;
+  if (tid < 128) {
+    const __nv_bfloat16* q = a.q + (int64_t)(t0 + r) * a.sq_t + (int64_t)h * a.sq_h;
+    uint4 w[D / 8];
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c)
+      w[c] = tid < pairs ? *reinterpret_cast<const uint4*>(q + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c)
+      *reinterpret_cast<uint4*>(smem + L::oQ + (c >> 3) * L::kRows + tid * 128 + (((c & 7) ^ (tid & 7)) << 4)) = w[c];
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tS = *slot, tO = tS + 128;
+
+  if (warp == 4) {
+    // ---- loads: lane i brings page i of the unit ----
+    const int2* list = a.lists + item * a.list_cap;
+    bool ok = true;
+    int i = 0;
+    for (; i < units && ok; ++i) {
+      const int at = i * ppu + lane;
+      const int2 e = lane < ppu && at < n ? list[at] : make_int2(0, 0);
+      int vc = e.y ? min(a.page_size, max(0, len - (e.x << a.ps_log2))) : 0, page = 0;
+      if (vc > 0) {
+        page = page_of(a, tile.s, e.x);
+        if (page < 0) vc = 0;
+      }
+      const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, vc > 0)) * a.page_size * (2 * D);
+      if (i > 0) ok = mbar_wait(s_ready, (i - 1) & 1, abort, 1);       // K is free
+      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      if (lane < ppu) info[(i & 1) * 8 + lane] = make_int4(e.x << a.ps_log2, e.y, vc, 0);
+      __syncwarp();
+      if (lane == 0) mbar_arrive_expect_tx(full_k, bytes);
+      __syncwarp();
+      const int off = lane << a.ps_log2;
+      if (vc > 0)
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_4d(smem + L::oK + c * L::kRows + off * 128, &mk, full_k, c * 64, 0, hk, page);
+      if (i > 0) ok = mbar_wait(o_done, (i - 1) & 1, abort, 2);        // V is free
+      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      if (lane == 0) mbar_arrive_expect_tx(full_v, bytes);
+      __syncwarp();
+      if (vc > 0)
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_4d(smem + L::oV + c * L::kRows + off * 128, &mv, full_v, c * 64, 0, hk, page);
+    }
+    if (!ok) {                         // nothing may still be writing shared memory
+      mbar_wait_drain(full_k, i & 1);
+      if (i > 0) mbar_wait_drain(full_v, (i - 1) & 1);
+    }
+  } else if (warp == 5) {
+    // ---- products ----
+    if (lane == 0) {
+      const uint32_t sq = smem_u32(smem + L::oQ), sk = smem_u32(smem + L::oK), sv = smem_u32(smem + L::oV);
+      constexpr uint32_t idesc_s = idesc_bf16(128, 128, false), idesc_o = idesc_bf16(128, D, true);
+      for (int i = 0; i < units; ++i) {
+        // (S's columns are free: they held P of the unit before, whose product
+        // is ahead in the pipe)
+        if (!mbar_wait(full_k, i & 1, abort, 3)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_f16_ss(tS, smem_desc_sw128(sq + (kk >> 2) * L::kRows + (kk & 3) * 32, 16, 1024),
+                     smem_desc_sw128(sk + (kk >> 2) * L::kRows + (kk & 3) * 32, 16, 1024), idesc_s, kk > 0 ? 1u : 0u);
+        tc_commit(s_ready);
+        if (!mbar_wait(p_ready, i & 1, abort, 4) || !mbar_wait(full_v, i & 1, abort, 5)) {
+          mbar_wait_drain(s_ready, i & 1);
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_f16_ts(tO, tS + kk * 8, smem_desc_sw128(sv + kk * 16 * 128, L::kRows, 1024), idesc_o,
+                     (i > 0 || kk > 0) ? 1u : 0u);
+        tc_commit(o_done);
+      }
+    }
+  } else {
+    // ---- softmax: a thread has one pair ----
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    const float sc = a.scale_log2, big = __int_as_float(0x7f800000);
+    const uint32_t bit = tid < pairs ? 1u << r : 0u;
+    const int pos0 = len - (a.cu[tile.s + 1] - t0);
+    const int sees = min(pos0 + r, len - 1) + 1;           // keys that the row sees
+    float m = -big, l = 0.0f;
+    bool ok = true;
+    for (int i = 0; i < units && ok; ++i) {
+      ok = mbar_wait(full_k, i & 1, abort, 6) && mbar_wait(s_ready, i & 1, abort, 7);
+      if (!ok) break;
+      tc_fence_after();
+      const int4* pages = info + (i & 1) * 8;
+      // visible keys of each 32
+      uint32_t vis[4];
+      bool whole = true;                                   // every slot of the unit holds a key
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        vis[c] = 0;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {                      // 16 keys at a time: one page
+          const int k = c * 32 + e * 16;
+          const int4 w = pages[k >> a.ps_log2];
+          const int first = k & (a.page_size - 1);
+          const int seen = (w.y & bit) ? min(w.z, sees - w.x) - first : 0;
+          vis[c] |= (seen >= 16 ? 0xFFFFu : seen > 0 ? (1u << seen) - 1 : 0u) << (16 * e);
+          whole &= w.z == a.page_size;
+        }
+      }
+      float mx = -big;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (!__any_sync(0xffffffffu, vis[c])) continue;
+        uint32_t x[32];
+        tmem_ld32(tS + lanes + c * 32, x);
+        if (__all_sync(0xffffffffu, vis[c] == 0xFFFFFFFFu)) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) mx = fmax3(mx, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) mx = fmaxf(mx, vis[c] >> k & 1 ? __uint_as_float(x[k]) : -big);
+        }
+      }
+      mx *= sc;
+      const bool move = mx > m + 8.0f || (m == -big && mx > -big);
+      if (__any_sync(0xffffffffu, move)) {
+        const float f = !move ? 1.0f : m == -big ? 0.0f : ex2(m - mx);
+        if (move) m = mx;
+        l *= f;
+        if (i > 0) {                   // (the last product is done: S came after it)
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t x[32];
+            tmem_ld32(tO + lanes + c * 32, x);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
+            tmem_st32(tO + lanes + c * 32, x);
+          }
+        }
+      }
+      const float mm = m == -big ? 0.0f : m;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t p[16];
+        if (!__any_sync(0xffffffffu, vis[c])) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) p[k] = 0u;
+        } else {
+          uint32_t x[32];
+          tmem_ld32(tS + lanes + c * 32, x);
+          const bool all = __all_sync(0xffffffffu, vis[c] == 0xFFFFFFFFu);
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            float u = ex2(fmaf(__uint_as_float(x[k]), sc, -mm)), v = ex2(fmaf(__uint_as_float(x[k + 1]), sc, -mm));
+            if (!all) {
+              u = vis[c] >> k & 1 ? u : 0.0f;
+              v = vis[c] >> (k + 1) & 1 ? v : 0.0f;
+            }
+            l += u + v;
+            p[k / 2] = pack_bf16(u, v);
+          }
+        }
+        tmem_st16(tS + lanes + c * 16, p);
+      }
+      tmem_wait_st();
+      if (!whole) {
+        // slots without a key hold anything: as zeros, P's zeros leave O alone
+        ok = mbar_wait(full_v, i & 1, abort, 8);
+        const int4 w = pages[tid >> a.ps_log2];
+        if (ok && (tid & (a.page_size - 1)) >= w.z)
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c)
+            *reinterpret_cast<uint4*>(smem + L::oV + (c >> 3) * L::kRows + tid * 128 + (c & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+      }
+      tc_fence_before();
+      mbar_arrive(p_ready);
+    }
+    if (ok && mbar_wait(o_done, (units - 1) & 1, abort, 9)) {
+      tc_fence_after();
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      bool fine = l < big && m < big;
+      __nv_bfloat16* out = a.o + (int64_t)(t0 + r) * a.so_t + (int64_t)h * a.so_h;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t x[32];
+        tmem_ld32(tO + lanes + c * 32, x);
+        uint32_t y[16];
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+          const float u = __uint_as_float(x[k]) * inv, v = __uint_as_float(x[k + 1]) * inv;
+          fine &= fabsf(u) < big && fabsf(v) < big;
+          y[k / 2] = pack_bf16(u, v);
+        }
+        if (tid < pairs)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4*>(out + c * 32 + k * 8) = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+      }
+      if (tid < pairs) {
+        if (!fine) a.row_flags[t0 + r] = 1;
+        if (a.lse) a.lse[(int64_t)(t0 + r) * a.H + h] = l == 0.0f ? -big : (m + log2f(l)) * 0.6931471805599453f;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) tmem_dealloc(tS, 256);
+}
+
 template <int D, bool FP8, int NT, bool SPARSE>
 cudaError_t run(const CacheArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
   using C = Cfg<D, FP8, NT>;
@@ -1064,19 +1334,35 @@ cudaError_t pick(const CacheArgs& a, const CUtensorMap& mk, const CUtensorMap& m
 
 }  // namespace
 
+static cudaError_t run_lists(const CacheArgs& a, int64_t tiles, int dev, cudaStream_t s) {
+  static OncePerDevice once;
+  const cudaError_t e = once.allow(reinterpret_cast<const void*>(cache_lists_kernel), dev, kMaxSelectPages * 4);
+  if (e != cudaSuccess) return e;
+  cache_lists_kernel<<<dim3((unsigned)tiles, a.Hkv), 256, a.max_pages * 4, s>>>(a);
+  return cudaGetLastError();
+}
+
 template <int D, bool FP8>
 static cudaError_t run_group(const CacheArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int64_t tiles,
                              int sms, int dev, cudaStream_t s) {
   using C = Cfg<D, FP8, 1, true>;
   static_assert(C::kBytes <= 232448, "shared memory");
-  static OncePerDevice once_l, once_g;
-  cudaError_t e = once_l.allow(reinterpret_cast<const void*>(cache_lists_kernel), dev, kMaxSelectPages * 4);
-  if (e != cudaSuccess) return e;
-  cache_lists_kernel<<<dim3((unsigned)tiles, a.Hkv), 256, a.max_pages * 4, s>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  static OncePerDevice once;
   auto k = cache_group_kernel<D, FP8>;
-  if ((e = once_g.allow(reinterpret_cast<const void*>(k), dev, C::kBytes)) != cudaSuccess) return e;
+  const cudaError_t e = once.allow(reinterpret_cast<const void*>(k), dev, C::kBytes);
+  if (e != cudaSuccess) return e;
   k<<<(unsigned)(tiles * a.Hkv < sms ? tiles * a.Hkv : sms), C::kThreads, C::kBytes, s>>>(mk, mv, a, (int)tiles);
+  return cudaGetLastError();
+}
+
+template <int D>
+static cudaError_t run_tiles(const CacheArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int64_t tiles,
+                             int dev, cudaStream_t s) {
+  static OncePerDevice once;
+  auto k = cache_tile_kernel<D>;
+  const cudaError_t e = once.allow(reinterpret_cast<const void*>(k), dev, TileSmem<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  k<<<dim3((unsigned)tiles, a.Hkv), 192, TileSmem<D>::kBytes, s>>>(mk, mv, a);
   return cudaGetLastError();
 }
 
@@ -1084,25 +1370,33 @@ cudaError_t launch_cache_attn(const CacheArgs& args, const CUtensorMap& mk, cons
                               bool sparse, cudaStream_t s) {
   CacheArgs a = args;
   a.row_flags = nullptr;
-  // rows together where two tiles or more fall on each SM (fewer leave the
-  // GPU idle: the rows' own items split over it)
-  const int rows = sparse && a.cu ? group_rows(a.G, a.T, a.S, a.max_pages) : 0;
-  if (rows) {
+  // rows together where there are tiles for every SM (fewer leave the GPU
+  // idle: the rows' own items split over it): bf16 in tiles of up to 128
+  // (row, query head) pairs and 32 rows, else in tiles of up to 32 pairs
+  if (sparse && a.cu) {
     int dev = 0, sms = 0;
     cudaError_t e = device_sms(dev, sms);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = group_tiles(rows, a.T, a.S);
-    if ((int64_t)a.T / rows * a.Hkv >= 2 * sms && tiles * a.Hkv < 0x7fffffff) {
+    int rows = a.fp8 ? 0 : tile_rows(a.G, a.T, a.S, a.max_pages);
+    const bool big = rows && (int64_t)a.T / rows * a.Hkv >= sms;
+    if (!big) rows = group_rows(a.G, a.T, a.S, a.max_pages);
+    const int64_t tiles = rows ? group_tiles(rows, a.T, a.S) : 0;
+    if (rows && (big || (int64_t)a.T / rows * a.Hkv >= 2 * sms) && tiles * a.Hkv < 0x7fffffff) {
       a.tile_rows = rows;
       a.list_cap = rows * a.n_select;
       char* w = reinterpret_cast<char*>(a.scratch);
       a.lists = reinterpret_cast<int2*>(w);
       a.list_n = reinterpret_cast<int*>(a.lists + tiles * a.Hkv * a.list_cap);
       a.row_flags = a.list_n + tiles * a.Hkv;
-      if (a.d == 128)
-        e = a.fp8 ? run_group<128, true>(a, mk, mv, tiles, sms, dev, s) : run_group<128, false>(a, mk, mv, tiles, sms, dev, s);
-      else
-        e = a.fp8 ? run_group<64, true>(a, mk, mv, tiles, sms, dev, s) : run_group<64, false>(a, mk, mv, tiles, sms, dev, s);
+      e = run_lists(a, tiles, dev, s);
+      if (e == cudaSuccess) {
+        if (big)
+          e = a.d == 128 ? run_tiles<128>(a, mk, mv, tiles, dev, s) : run_tiles<64>(a, mk, mv, tiles, dev, s);
+        else if (a.d == 128)
+          e = a.fp8 ? run_group<128, true>(a, mk, mv, tiles, sms, dev, s) : run_group<128, false>(a, mk, mv, tiles, sms, dev, s);
+        else
+          e = a.fp8 ? run_group<64, true>(a, mk, mv, tiles, sms, dev, s) : run_group<64, false>(a, mk, mv, tiles, sms, dev, s);
+      }
       if (e != cudaSuccess) return e;
     }
   }

@@ -118,8 +118,13 @@ class Step:
         """O and lse against the oracle within the bound of the arithmetic:
         O's rounding (2^-8 relative), P's rounding (2^-8 of sum p |v|), the
         scores' errors (d products in fp32 and the scaling, doubled through
-        exp), and the fp32 sums over n keys."""
+        exp), and the fp32 sums over n keys.  FP8: the weights are f16 with
+        2^15 for weight 1 at the largest V scale seen (of the sequence at
+        most), so half a subnormal step, 2^-25, is 2^-40 of that scale times
+        the key's code (448 at most); the sum of weights is 1 or more, since
+        the greatest weight is 1: n 2^-40 448 max(scale) on O."""
         kd, vd = self.decoded()
+        vs = np64(self.cache.v_scale) if self.fp8 else None
         O, lse, Q = np64(O), np64(lse), np64(self.Q)
         used = set()
         for t, s, pos in OC.rows_of(self.lens, self.cu, self.S):
@@ -137,6 +142,9 @@ class Step:
                 ds = (self.d + 8) * big * u
                 rest = 2 * ds + (K.shape[0] + 64) * u + 2.0 ** -20
                 tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -8 + rest) * A * (1 + 2.0 ** -7)
+                if self.fp8 and self.lens[s] > 0:
+                    top = OC.keys_of(vs[..., None], self.table[s], self.lens[s], hk).max()
+                    tol = tol + K.shape[0] * 2.0 ** -40 * 448 * top
                 assert (np.abs(O[t, h] - o) <= tol).all(), (t, h, np.abs(O[t, h] - o).max())
                 if math.isinf(z):
                     assert lse[t, h] == z
@@ -483,6 +491,11 @@ MANY = [
     ([0, 500, 3], [510, 0, 300], dict(H=40, Hkv=8, d=64, ps=16, n_select=7, layout="nhd")),
     ([2000], [640], dict(H=32, Hkv=2, ps=128, n_select=5)),
     ([10, 70], [2400, 100], dict(H=2, Hkv=2, d=64, ps=32, n_select=3)),
+    # and tiles of 128 (row, query head) pairs
+    ([100, 0], [900, 401], dict(H=32, Hkv=8, n_select=6, pad=3)),
+    ([700], [430], dict(H=64, Hkv=4, ps=128, n_select=3)),
+    ([64, 3, 90], [310, 0, 333], dict(H=64, Hkv=8, ps=16, n_select=9, layout="nhd")),
+    ([5000], [600], dict(H=24, Hkv=8, ps=32, n_select=40, scale=1.0)),
 ]
 
 
@@ -523,11 +536,12 @@ def check_some(st, O, lse, lists, every):
         OC.rows_of, st.T = real, T
 
 
+@pytest.mark.parametrize("Hkv,d", [(4, 64), (8, 128)])
 @pytest.mark.parametrize("fp8", [False, True])
-def test_sparse_many_rows_hidden_values_that_are_not_finite(cuda_ok, fp8):
+def test_sparse_many_rows_hidden_values_that_are_not_finite(cuda_ok, fp8, Hkv, d):
     # a page with a NaN in V (a NaN scale, FP8): rows that do not list it, and
     # rows before that key, must not see it
-    st = Step([0], [800], H=16, Hkv=4, d=64, ps=16, fp8=fp8, n_select=3, seed=7)
+    st = Step([0], [800], H=4 * Hkv, Hkv=Hkv, d=d, ps=16, fp8=fp8, n_select=3, seed=7)
     st.append()
     bad_pos = 411
     pg, slot = st.table[0][bad_pos // 16], bad_pos % 16
@@ -536,7 +550,7 @@ def test_sparse_many_rows_hidden_values_that_are_not_finite(cuda_ok, fp8):
     else:
         st.cache.v[pg, 2, slot, 9] = float("nan")
         st.cache.v[pg, 1, slot, 3] = float("inf")
-    lists = torch.randint(0, 50, (800, 4, 3), generator=st.g, dtype=torch.int32)
+    lists = torch.randint(0, 50, (800, Hkv, 3), generator=st.g, dtype=torch.int32)
     lists[400:500, :, 0] = 25                        # page 25 holds key 411
     lists[:, :, 1] = torch.where(lists[:, :, 1] == 25, 26, lists[:, :, 1])
     O, lse = st.sparse(lists.to(DEV))
@@ -548,7 +562,7 @@ def test_sparse_many_rows_hidden_values_that_are_not_finite(cuda_ok, fp8):
         sees1 = [t >= bad_pos and 25 in L[t][1] for t in range(800)]
         assert O[:, 4:8].isinf().any(-1).any(-1).tolist() == sees1
         assert O[:, 4:8].isnan().sum() == 0
-    clean = [t for t in range(800) if not any(t >= bad_pos and 25 in L[t][h] for h in range(4))]
+    clean = [t for t in range(800) if not any(t >= bad_pos and 25 in L[t][h] for h in range(Hkv))]
     for x in (st.cache.v,) if not fp8 else ():
         x[pg, 2, slot, 9] = 0.0
         x[pg, 1, slot, 3] = 0.0
