@@ -780,9 +780,10 @@ __global__ void __launch_bounds__(288, 2) cache_logits_kernel(const CacheArgs a,
 #pragma unroll 1
       for (int c0 = c_lo; c0 < max(c_hi, c_lo + 1); c0 += 32) {
         uint32_t x[D / 64][32];
-#pragma unroll
-        for (int u = 0; u < D / 64; ++u) tmem_ld32_nw(lane_addr + u * kSelCols + c0, x[u]);
-        tmem_wait_ld();
+        if constexpr (D == 128)
+          tmem_ld32x2(lane_addr + c0, lane_addr + kSelCols + c0, x[0], x[1]);
+        else
+          tmem_ld32(lane_addr + c0, x[0]);
         if (c0 + 32 >= c_hi) {         // all read: the next product may come
           tc_fence_before();
           if (lane == 0) mbar_arrive(freed);

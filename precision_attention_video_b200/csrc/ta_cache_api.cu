@@ -49,7 +49,7 @@ size_t sparse_bytes(const ta_cache_params* p) {
                          ta::tile_rows(p->H / p->Hkv, p->T, p->S, p->max_pages)}) {
     if (!rows) continue;
     const size_t items = (size_t)ta::group_tiles(rows, p->T, p->S) * p->Hkv;
-    const size_t n = items * ((size_t)rows * p->n_select * 8 + 4) + (size_t)p->T * 4;
+    const size_t n = items * ((size_t)rows * p->n_select * 8 + 4) + ((size_t)p->T + 1) * 4;
     most = n > most ? n : most;
   }
   return most;

@@ -550,6 +550,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT>::kThreads, 1)
   float* const sm_m0 = reinterpret_cast<float*>(smem + C::oML);
   const AbortCtx abort{misc, a.status};
 
+  if (SPARSE && a.row_flags && !a.row_flags[a.T]) return;   // no row to do again
   const int HG = (a.G + NH - 1) / NH;              // items of one key head
   const int HX = a.Hkv * HG;
   const int rows = SPARSE ? rows_used(a) : a.S;
@@ -819,6 +820,7 @@ __global__ void __launch_bounds__(256) cache_lists_kernel(const CacheArgs a) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hk = blockIdx.y;
   const RowTile tile = row_tile(a, blockIdx.x, a.tile_rows);
   const int64_t item = (int64_t)blockIdx.x * a.Hkv + hk;
+  if (hk == 0 && blockIdx.x == 0 && tid == 0) a.row_flags[a.T] = 0;
   if (hk == 0)
     for (int t = tile.t0 + tid; t < tile.t1; t += 256) {
       a.row_flags[t] = 0;
@@ -1020,7 +1022,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, 1, true>::kThreads, 1)
       const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
       const float x = joined_at<C, D, FP8, NT>(join, c, d) * inv, y = joined_at<C, D, FP8, NT>(join, c, d + 1) * inv;
       const float big = __int_as_float(0x7f800000);
-      if (!(fabsf(x) < big && fabsf(y) < big && ll < big && (mm < big))) a.row_flags[t0 + r] = 1;
+      if (!(fabsf(x) < big && fabsf(y) < big && ll < big && mm < big))
+        a.row_flags[t0 + r] = a.row_flags[a.T] = 1;
       *reinterpret_cast<uint32_t*>(a.o + (int64_t)(t0 + r) * a.so_t + (int64_t)h * a.so_h + d) = pack_bf16(x, y);
       if (d == 0 && a.lse)
         a.lse[(int64_t)(t0 + r) * a.H + h] = ll == 0.0f ? -big : (mm + log2f(ll)) * 0.6931471805599453f;
@@ -1198,18 +1201,25 @@ __global__ void __launch_bounds__(192, 2)
         }
       }
       float mx = -big;
+      bool all[4];                     // (uniform) every lane sees every key of the 32
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (!__any_sync(0xffffffffu, vis[c])) continue;
-        uint32_t x[32];
-        tmem_ld32(tS + lanes + c * 32, x);
-        if (__all_sync(0xffffffffu, vis[c] == 0xFFFFFFFFu)) {
+      for (int c = 0; c < 4; ++c) all[c] = __all_sync(0xffffffffu, vis[c] == 0xFFFFFFFFu);
+      auto top = [&](const uint32_t (&x)[32], uint32_t v) {
+        if (v == 0xFFFFFFFFu) {
 #pragma unroll
           for (int k = 0; k < 32; k += 2) mx = fmax3(mx, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-        } else {
+        } else if (v) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) mx = fmaxf(mx, vis[c] >> k & 1 ? __uint_as_float(x[k]) : -big);
+          for (int k = 0; k < 32; ++k) mx = fmaxf(mx, v >> k & 1 ? __uint_as_float(x[k]) : -big);
         }
+      };
+#pragma unroll
+      for (int c = 0; c < 4; c += 2) {
+        if (!__any_sync(0xffffffffu, vis[c] | vis[c + 1])) continue;
+        uint32_t x[32], y[32];
+        tmem_ld32x2(tS + lanes + c * 32, tS + lanes + c * 32 + 32, x, y);
+        top(x, vis[c]);
+        top(y, vis[c + 1]);
       }
       mx *= sc;
       const bool move = mx > m + 8.0f || (m == -big && mx > -big);
@@ -1220,37 +1230,44 @@ __global__ void __launch_bounds__(192, 2)
         if (i > 0) {                   // (the last product is done: S came after it)
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
-            uint32_t x[32];
-            tmem_ld32(tO + lanes + c * 32, x);
+            uint32_t o[32];
+            tmem_ld32(tO + lanes + c * 32, o);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
-            tmem_st32(tO + lanes + c * 32, x);
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tmem_st32(tO + lanes + c * 32, o);
           }
         }
       }
       const float mm = m == -big ? 0.0f : m;
+      auto weights = [&](const uint32_t (&x)[32], int c, uint32_t (&p)[16]) {
+        // (uniform) some row sees a part of the 32 keys, or there are slots
+        // without one; else a row sees all of them or none
+        const bool part = !all[c] && (!whole || __any_sync(0xffffffffu, vis[c] + 1u > 1u));
+        const float off = vis[c] ? mm : big;               // (none: 2^-inf)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t p[16];
-        if (!__any_sync(0xffffffffu, vis[c])) {
-#pragma unroll
-          for (int k = 0; k < 16; ++k) p[k] = 0u;
-        } else {
-          uint32_t x[32];
-          tmem_ld32(tS + lanes + c * 32, x);
-          const bool all = __all_sync(0xffffffffu, vis[c] == 0xFFFFFFFFu);
-#pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            float u = ex2(fmaf(__uint_as_float(x[k]), sc, -mm)), v = ex2(fmaf(__uint_as_float(x[k + 1]), sc, -mm));
-            if (!all) {
-              u = vis[c] >> k & 1 ? u : 0.0f;
-              v = vis[c] >> (k + 1) & 1 ? v : 0.0f;
-            }
-            l += u + v;
-            p[k / 2] = pack_bf16(u, v);
+        for (int k = 0; k < 32; k += 2) {
+          float u = ex2(fmaf(__uint_as_float(x[k]), sc, -off)), v = ex2(fmaf(__uint_as_float(x[k + 1]), sc, -off));
+          if (part) {
+            u = vis[c] >> k & 1 ? u : 0.0f;
+            v = vis[c] >> (k + 1) & 1 ? v : 0.0f;
           }
+          l += u + v;
+          p[k / 2] = pack_bf16(u, v);
+        }
+      };
+#pragma unroll
+      for (int c = 0; c < 4; c += 2) {
+        uint32_t p[16], q[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) p[k] = q[k] = 0u;
+        if (__any_sync(0xffffffffu, vis[c] | vis[c + 1])) {
+          uint32_t x[32], y[32];
+          tmem_ld32x2(tS + lanes + c * 32, tS + lanes + c * 32 + 32, x, y);
+          weights(x, c, p);
+          weights(y, c + 1, q);
         }
         tmem_st16(tS + lanes + c * 16, p);
+        tmem_st16(tS + lanes + c * 16 + 16, q);
       }
       tmem_wait_st();
       if (!whole) {
@@ -1289,7 +1306,7 @@ __global__ void __launch_bounds__(192, 2)
             *reinterpret_cast<uint4*>(out + c * 32 + k * 8) = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
       }
       if (tid < pairs) {
-        if (!fine) a.row_flags[t0 + r] = 1;
+        if (!fine) a.row_flags[t0 + r] = a.row_flags[a.T] = 1;
         if (a.lse) a.lse[(int64_t)(t0 + r) * a.H + h] = l == 0.0f ? -big : (m + log2f(l)) * 0.6931471805599453f;
       }
     }
