@@ -2,7 +2,9 @@
 
 Each CUDA source is compiled to an object in parallel, then linked into a
 shared library next to this file; the CUDA runtime is linked statically so
-the library needs nothing beyond the driver at run time.
+the library needs nothing beyond the driver at run time.  The Python entry of
+the cached-attention operators (_cache_call.so) is compiled by the host
+compiler against the installed torch.
 """
 
 from __future__ import annotations
@@ -18,6 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libtiered_attn.so")
+CALL = os.path.join(HERE, "_cache_call.so")
 
 SOURCES = ["ta_api.cu", "ta_prep.cu", "ta_route.cu", "ta_attn.cu", "ta_attn2.cu", "ta_static.cu",
            "ta_cache_api.cu", "ta_cache.cu", "ta_cache_attn.cu"]
@@ -40,9 +43,33 @@ def _deps_mtime() -> float:
     return max(os.path.getmtime(p) for p in paths)
 
 
+def _build_call() -> None:
+    """Compile _cache_call.so."""
+    import sysconfig
+
+    import torch
+    root = os.path.join(os.path.dirname(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(nvcc())) if os.path.sep in nvcc() else "/usr/local/cuda"
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE,
+           *[x for i in inc for x in ("-isystem", i)],
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           os.path.join(CSRC, "ta_cache_py.cpp"), "-o", CALL + ".tmp",
+           "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("compiler failed on ta_cache_py.cpp")
+    os.replace(CALL + ".tmp", CALL)
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
     """Compile and link the library if any source is newer than it; return its path."""
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
+    deps = _deps_mtime()
+    if force or not os.path.exists(CALL) or os.path.getmtime(CALL) < deps:
+        _build_call()
+    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= deps:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     extra = ["-Xptxas", "-v"] if ptxas_verbose else []

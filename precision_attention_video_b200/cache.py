@@ -2,7 +2,9 @@
 choice and sparse attention (the C ABI of include/tiered_attn_cache.h).
 
 Argument marshalling only, as in ``binding``: the operators run in the
-library's CUDA kernels, the caller owns every buffer.  Strides come from the
+library's CUDA kernels, the caller owns every buffer.  A call goes through
+``_cache_call`` (csrc/ta_cache_py.cpp), which checks and marshals in C++; what
+it refuses is checked again here, for the reason.  Strides come from the
 tensors of each call, sizes from the parameters::
 
     p = pav.make_cache_params(n_pages=P, page_size=64, H=32, Hkv=8, d=128, S=S, T=T,
@@ -44,6 +46,12 @@ class ta_cache(ctypes.Structure):
     _fields_ = [(n, _vp) for n in ("k", "v", "k_scale", "v_scale", "k_mean")]
 
 
+class _CacheView(ctypes.Structure):
+    """What ``_cache_call`` reads of a PagedCache (CacheView there)."""
+    _fields_ = [("c", ta_cache), ("stride", _i64 * 3), ("shape", _i64 * 4), ("format", _i32),
+                ("device", _i32), ("has_mean", _i32), ("pad", _i32)]
+
+
 _P = ctypes.POINTER(ta_cache_params)
 _C = ctypes.POINTER(ta_cache)
 _SIGS = {
@@ -64,6 +72,24 @@ def _fn(name):
         f.restype, f.argtypes = _SIGS[name]
         _fns[name] = f
     return f
+
+
+_call = None
+
+
+def _native():
+    """The C++ entry, bound to the library on first use; a missing one raises."""
+    global _call
+    if _call is None:
+        try:
+            from . import _cache_call as m
+        except ImportError as e:
+            raise ImportError("_cache_call.so is missing or does not load: build it with "
+                              "`python -m precision_attention_video_b200.build`") from e
+        m.init(*(ctypes.cast(_fn("tiered_attn_cache_" + n), _vp).value
+                 for n in ("append", "decode", "select", "sparse")))
+        _call = m
+    return _call
 
 
 def make_cache_params(*, n_pages: int, page_size: int, H: int, Hkv: int, d: int, S: int, T: int,
@@ -87,7 +113,7 @@ class PagedCache:
     page_size] for FP8, ``k_mean`` f32 [n_pages, Hkv, d] where pages are
     chosen.  ``k`` and ``v`` may be None for a cache that is only chosen from."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "k_mean", "_c", "_strides", "_shape", "_fmt",
+    __slots__ = ("k", "v", "k_scale", "v_scale", "k_mean", "_view", "_strides", "_shape", "_fmt",
                  "_dev")
 
     def __init__(self, k, v, k_scale=None, v_scale=None, k_mean=None):
@@ -118,8 +144,13 @@ class PagedCache:
             if t is not None and t.get_device() != self._dev:
                 raise ValueError(f"{name}: not on the cache's device")
         self.k, self.v, self.k_scale, self.v_scale, self.k_mean = k, v, k_scale, v_scale, k_mean
-        self._c = ta_cache(*(t.data_ptr() if t is not None else None
-                             for t in (k, v, k_scale, v_scale, k_mean)))
+        # without keys, the means' sizes (no page size)
+        n, h, ps, d = self._shape or (k_mean.shape[0], k_mean.shape[1], 0, k_mean.shape[2])
+        self._view = _CacheView(
+            ta_cache(*(t.data_ptr() if t is not None else None
+                       for t in (k, v, k_scale, v_scale, k_mean))),
+            self._strides, (n, h, ps, d), -1 if self._fmt is None else self._fmt, self._dev,
+            int(k_mean is not None))
 
 
 def make_cache(p: ta_cache_params, device="cuda", layout: str = "hnd",
@@ -252,6 +283,10 @@ def cache_append(p: ta_cache_params, cache: PagedCache, K, V, table, lens, ws, c
     by the table rows ``pos`` (their positions, where None) of ``cos`` and
     ``sin`` (f32 [rows, rot_dim / 2]); rotate Q [T, H, d] into ``Q_out`` (may
     be Q itself) with the same angles.  ``lens`` counts the new tokens."""
+    st = _native().append(p, cache._view, K, V, table, lens, ws, cu, cos, sin, pos, Q,
+                          Q_out, None if stream is None else _b._stream(stream))
+    if st is not None:
+        return _check("tiered_attn_cache_append", st)
     q, dev, tb, ln, c, w, n = _begin(p, cache, table, lens, ws, cu, True)
     T, d, rot = p.T, p.d, p.rot_dim
     shape = (T, p.Hkv, d)
@@ -275,39 +310,51 @@ def cache_append(p: ta_cache_params, cache: PagedCache, K, V, table, lens, ws, c
     if pos is not None:
         pp = _plain("pos", pos, torch.int32, (T,), dev)
     _check("tiered_attn_cache_append", _fn("tiered_attn_cache_append")(
-        q, cache._c, k, v, qi, qo, cp, sp, pp, c, ln, tb, w, n, _stream_of(stream, dev)))
+        q, cache._view.c, k, v, qi, qo, cp, sp, pp, c, ln, tb, w, n, _stream_of(stream, dev)))
 
 
 def cache_decode(p: ta_cache_params, cache: PagedCache, Q, table, lens, ws, O,
                  lse: Optional[torch.Tensor] = None, stream=None) -> None:
     """Attention of one new token for each sequence, Q bf16 [S, H, d], over
     its whole cache into O (and ``lse`` f32 [S, H])."""
+    st = _native().decode(p, cache._view, Q, table, lens, ws, O, lse,
+                          None if stream is None else _b._stream(stream))
+    if st is not None:
+        return _check("tiered_attn_cache_decode", st)
     q, dev, tb, ln, _, w, n = _begin(p, cache, table, lens, ws, None, True)
     shape = (p.T, p.H, p.d)
     qp, q.stride_q_t, q.stride_q_h = _rows("Q", Q, shape, dev)
     op, q.stride_o_t, q.stride_o_h = _rows("O", O, shape, dev)
     lp = None if lse is None else _plain("lse", lse, torch.float32, shape[:2], dev)
     _check("tiered_attn_cache_decode", _fn("tiered_attn_cache_decode")(
-        q, cache._c, qp, ln, tb, op, lp, w, n, _stream_of(stream, dev)))
+        q, cache._view.c, qp, ln, tb, op, lp, w, n, _stream_of(stream, dev)))
 
 
 def cache_select(p: ta_cache_params, cache: PagedCache, Q, table, lens, ws, sel, cu=None,
                  stream=None) -> None:
     """The pages that each row reads: ``sel`` int32 [T, Hkv, n_select], page
     indices of the row's sequence in ascending order, then -1."""
+    st = _native().select(p, cache._view, Q, table, lens, ws, sel, cu,
+                          None if stream is None else _b._stream(stream))
+    if st is not None:
+        return _check("tiered_attn_cache_select", st)
     q, dev, tb, ln, c, w, n = _begin(p, cache, table, lens, ws, cu, False)
     if cache.k_mean is None or cache.k_mean.shape != (p.n_pages, p.Hkv, p.d):
         raise ValueError(f"cache: expected k_mean of shape {(p.n_pages, p.Hkv, p.d)}")
     qp, q.stride_q_t, q.stride_q_h = _rows("Q", Q, (p.T, p.H, p.d), dev)
     sl = _plain("sel", sel, torch.int32, (p.T, p.Hkv, p.n_select), dev)
     _check("tiered_attn_cache_select", _fn("tiered_attn_cache_select")(
-        q, cache._c, qp, c, ln, tb, sl, w, n, _stream_of(stream, dev)))
+        q, cache._view.c, qp, c, ln, tb, sl, w, n, _stream_of(stream, dev)))
 
 
 def cache_sparse(p: ta_cache_params, cache: PagedCache, Q, sel, table, lens, ws, O, cu=None,
                  lse: Optional[torch.Tensor] = None, stream=None) -> None:
     """Attention of each row, Q bf16 [T, H, d], over the pages of its list
     ``sel`` into O (and ``lse`` f32 [T, H])."""
+    st = _native().sparse(p, cache._view, Q, sel, table, lens, ws, O, cu, lse,
+                          None if stream is None else _b._stream(stream))
+    if st is not None:
+        return _check("tiered_attn_cache_sparse", st)
     q, dev, tb, ln, c, w, n = _begin(p, cache, table, lens, ws, cu, True)
     shape = (p.T, p.H, p.d)
     qp, q.stride_q_t, q.stride_q_h = _rows("Q", Q, shape, dev)
@@ -315,4 +362,4 @@ def cache_sparse(p: ta_cache_params, cache: PagedCache, Q, sel, table, lens, ws,
     sl = _plain("sel", sel, torch.int32, (p.T, p.Hkv, p.n_select), dev)
     lp = None if lse is None else _plain("lse", lse, torch.float32, shape[:2], dev)
     _check("tiered_attn_cache_sparse", _fn("tiered_attn_cache_sparse")(
-        q, cache._c, qp, sl, c, ln, tb, op, lp, w, n, _stream_of(stream, dev)))
+        q, cache._view.c, qp, sl, c, ln, tb, op, lp, w, n, _stream_of(stream, dev)))

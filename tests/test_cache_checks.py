@@ -171,6 +171,23 @@ def test_the_binding_refuses_host_and_mis_shaped_caches():
         pav.init_cache_workspace(ws)
 
 
+def test_the_native_entry_refuses_without_work():
+    # host tensors, wrong kinds of arguments, the wrong number of them: None
+    # (the module's own checks then raise), never an exception or a call
+    m = C._native()
+    p, c = params(), pav.make_cache(params(), "cpu")
+    z = torch.zeros
+    Q, K = z(2, 8, 128, dtype=torch.bfloat16), z(2, 2, 128, dtype=torch.bfloat16)
+    table, lens = z(2, 4, dtype=torch.int32), z(2, dtype=torch.int32)
+    ws, sel = z(1 << 20, dtype=torch.uint8), z(2, 2, 3, dtype=torch.int32)
+    for args in ((p, c._view, Q, table, lens, ws, Q, None, None), (p, c._view, Q, table), (),
+                 (p, c, Q, table, lens, ws, Q, None, None), (b"x", b"y", 1, 2, 3, 4, 5, 6, 7),
+                 (p, c._view, None, None, None, None, None, None, "stream")):
+        assert m.decode(*args) is None and m.select(*args) is None
+    assert m.append(p, c._view, K, K, table, lens, ws, None, None, None, None, None, None, None) is None
+    assert m.sparse(p, c._view, Q, sel, table, lens, ws, Q, None, None, None) is None
+
+
 def test_the_bindings_tensor_checks():
     z = torch.zeros
     with pytest.raises(ValueError, match="lens: expected a tensor on device 0"):

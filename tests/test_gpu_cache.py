@@ -748,6 +748,39 @@ def test_bad_pages_and_lengths_are_reported_and_harmless(cuda_ok):
     np.testing.assert_array_equal(st.arrays()[1], want[1])
 
 
+def test_the_native_entry_takes_ordinary_calls(cuda_ok):
+    # 0, not None: the checks in C++ read the structures as Python wrote them
+    from precision_attention_video_b200 import cache as C
+    m = C._native()
+    st = Step([70, 200], [30, 1], rot=128, seed=71)
+    cos, sin = st.tables(300)
+    sel = torch.zeros((st.T, st.Hkv, 4), dtype=torch.int32, device=DEV)
+    O, lse = st.out()
+    a = (st.p, st.cache._view)
+    assert m.append(*a, st.K, st.V, st.t_table, st.t_lens, st.ws, st.t_cu, cos, sin, None, st.Q, O, None) == 0
+    assert m.select(*a, st.Q, st.t_table, st.t_lens, st.ws, sel, st.t_cu, None) == 0
+    assert m.sparse(*a, st.Q, sel, st.t_table, st.t_lens, st.ws, O, st.t_cu, lse, None) == 0
+    # refused: other devices' or shapes' tensors; then the reason
+    assert m.sparse(*a, st.Q, sel.cpu(), st.t_table, st.t_lens, st.ws, O, st.t_cu, lse, None) is None
+    assert m.sparse(*a, st.Q[1:], sel, st.t_table, st.t_lens, st.ws, O, st.t_cu, lse, None) is None
+    for bad, why in ((dict(sel=sel.cpu()), "sel: expected a tensor on device 0"),
+                     (dict(sel=sel[:, :, :3]), "sel: expected a contiguous tensor"),
+                     (dict(Q=st.Q.float()), "Q: expected torch.bfloat16"),
+                     (dict(table=st.t_table[:1]), "table: expected"),
+                     (dict(ws=st.ws.view(-1, 2)), "ws: expected"),
+                     (dict(lens=st.t_lens.long()), "lens: expected torch.int32")):
+        kw = {**dict(Q=st.Q, sel=sel, table=st.t_table, lens=st.t_lens, ws=st.ws, O=O), **bad}
+        with pytest.raises((ValueError, TypeError), match=why):
+            pav().cache_sparse(st.p, st.cache, **kw, cu=st.t_cu)
+    one = Step([100], [0], seed=72, cu=False)
+    O, lse = one.out()
+    assert m.decode(one.p, one.cache._view, one.Q, one.t_table, one.t_lens, one.ws, O, lse,
+                    torch.cuda.current_stream().cuda_stream) == 0
+    one.check(O, lse)
+    with pytest.raises(pav().TieredAttnError, match="workspace too small"):
+        pav().cache_decode(one.p, one.cache, one.Q, one.t_table, one.t_lens, one.ws[:4096], O)
+
+
 def test_far_pages_pass_32_bits(cuda_ok):
     # a cache of more than 2^31 elements: its last pages
     m = pav()
