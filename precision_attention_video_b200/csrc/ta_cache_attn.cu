@@ -562,6 +562,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT>::kThreads, 1)
     }
     misc[0] = 0;
     fence_mbar_init();
+    tma_prefetch_desc(&mk);
+    tma_prefetch_desc(&mv);
   }
 
   // ---- units of all items ----
@@ -774,17 +776,31 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT>::kThreads, 1)
           for (int e = tid; e < nh * (D / 2); e += 32 * kWarps) {
             const int nn = e / (D / 2), d = 2 * (e - nn * (D / 2));
             float mm = kNegInf, ll = 0.0f, x = 0.0f, y = 0.0f;
-            for (int c = cf; c <= cl; ++c)
-              mm = fmaxf(mm, __ldcg(a.part_ml + (2 * c + (c == cf)) * (2 * kMaxTileHeads) + nn));
-            for (int c = cf; c <= cl; ++c) {
-              const int sl = 2 * c + (c == cf);
-              const float mw = __ldcg(a.part_ml + sl * (2 * kMaxTileHeads) + nn);
-              const float f = mw == kNegInf ? 0.0f : ex2(mw - mm);
-              const float2 v = __ldcg(reinterpret_cast<const float2*>(
-                  a.part_o + (int64_t)sl * (kMaxTileHeads * 128) + nn * D + d));
-              ll += f * __ldcg(a.part_ml + sl * (2 * kMaxTileHeads) + kMaxTileHeads + nn);
-              x += f * v.x;
-              y += f * v.y;
+            for (int c0 = cf; c0 <= cl; c0 += 8) {         // 8 parts' loads in flight
+              float pm[8], pl[8];
+              float2 pv[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const int c = min(c0 + k, cl), sl = 2 * c + (c == cf);
+                pm[k] = __ldcg(a.part_ml + sl * (2 * kMaxTileHeads) + nn);
+                pl[k] = __ldcg(a.part_ml + sl * (2 * kMaxTileHeads) + kMaxTileHeads + nn);
+                pv[k] = __ldcg(reinterpret_cast<const float2*>(a.part_o + (int64_t)sl * (kMaxTileHeads * 128) + nn * D + d));
+              }
+              float top = mm;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) top = fmaxf(top, pm[k]);
+              const float old = mm == kNegInf ? 0.0f : ex2(mm - top);
+              mm = top;
+              ll *= old;
+              x *= old;
+              y *= old;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float f = pm[k] == kNegInf || c0 + k > cl ? 0.0f : ex2(pm[k] - mm);
+                ll += f * pl[k];
+                x += f * pv[k].x;
+                y += f * pv[k].y;
+              }
             }
             put(nn, d, x, y, mm, ll);
           }
@@ -1033,28 +1049,29 @@ __global__ void __launch_bounds__(Cfg<D, FP8, 1, true>::kThreads, 1)
 }
 
 // The same for bf16 caches and tiles of up to 128 (row, query head) pairs, on
-// tcgen05: the pairs are the 128 rows of S = Q K^T and O += P V, a thread of
-// the softmax has one of them, S and P (bf16, over S's own columns) and O
-// stand in TMEM.  A block has one K and one V buffer: K of the next unit loads
+// tcgen05: the pairs are the 128 rows of S = Q K^T and O += P V, two threads of
+// the softmax share one of them (64 keys each; one alone took 135 us where two
+// take TIME us), S and P (bf16, over S's own columns) and O stand in TMEM.  A block has one K and one V buffer: K of the next unit loads
 // while this one's softmax runs, V while the next S does, and two blocks share
 // an SM.  With the mma.sync kernel above 1330 rows took 245 us, bound by its
 // instructions (32 columns for each key read); here a key serves 128 rows.
 //
-// The running maximum may lag: numerators and sums move to a new maximum only
-// when it is more than 2^8 above the old one (P then stays below 2^8, far from
-// any limit), so that O is seldom read back and rescaled.
+// A row's greatest weight is exactly 1, so P's rounding spares it (letting the
+// maximum lag and O be rescaled seldom was 7 percent faster and a fifth less
+// exact where few keys carry a row).
 template <int D>
 struct TileSmem {
   static constexpr int kRows = 128 * 128;          // bytes of 128 rows by 64 elements
   static constexpr int kOp = D / 64 * kRows;       // one operand
   static constexpr int oQ = 0, oK = kOp, oV = 2 * kOp;
   static constexpr int oInfo = 3 * kOp;            // [2][8] int4: the pages of a unit
-  static constexpr int oBar = oInfo + 256;
+  static constexpr int oMax = oInfo + 256;         // [2][2][128] maxima of a row's halves, then sums
+  static constexpr int oBar = oMax + 2048;
   static constexpr int kBytes = oBar + 64 + 1024;  // 1024 to align
 };
 
 template <int D>
-__global__ void __launch_bounds__(192, 2)
+__global__ void __launch_bounds__(320, 2)
     cache_tile_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                       const CacheArgs a) {
   using L = TileSmem<D>;
@@ -1078,26 +1095,30 @@ __global__ void __launch_bounds__(192, 2)
     mbar_init(full_k, 1);
     mbar_init(full_v, 1);
     mbar_init(s_ready, 1);
-    mbar_init(p_ready, 128);
+    mbar_init(p_ready, 256);
     mbar_init(o_done, 1);
     *flag = 0;
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == 9) {
     tmem_alloc(slot, 256);
     tmem_relinquish();
   }
   // pair i of the tile: row i / G, query head i % G of the key head
-  const int r = tid / a.G, h = hk * a.G + tid - r * a.G;
-  if (tid < 128) {
+  const int pair = tid & 127, half = tid >> 7;             // (softmax threads)
+  const int r = pair / a.G, h = hk * a.G + pair - r * a.G;
+  if (tid < 256) {
     const __nv_bfloat16* q = a.q + (int64_t)(t0 + r) * a.sq_t + (int64_t)h * a.sq_h;
-    uint4 w[D / 8];
+    constexpr int N = D / 16;                              // chunks of half a row
+    uint4 w[N];
 #pragma unroll
-    for (int c = 0; c < D / 8; ++c)
-      w[c] = tid < pairs ? *reinterpret_cast<const uint4*>(q + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+    for (int c = 0; c < N; ++c)
+      w[c] = pair < pairs ? *reinterpret_cast<const uint4*>(q + 8 * (half * N + c)) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-    for (int c = 0; c < D / 8; ++c)
-      *reinterpret_cast<uint4*>(smem + L::oQ + (c >> 3) * L::kRows + tid * 128 + (((c & 7) ^ (tid & 7)) << 4)) = w[c];
+    for (int c = 0; c < N; ++c) {
+      const int x = half * N + c;
+      *reinterpret_cast<uint4*>(smem + L::oQ + (x >> 3) * L::kRows + pair * 128 + (((x & 7) ^ (pair & 7)) << 4)) = w[c];
+    }
     fence_proxy_async_smem();
   }
   tc_fence_before();
@@ -1105,7 +1126,7 @@ __global__ void __launch_bounds__(192, 2)
   tc_fence_after();
   const uint32_t tS = *slot, tO = tS + 128;
 
-  if (warp == 4) {
+  if (warp == 8) {
     // ---- loads: lane i brings page i of the unit ----
     const int2* list = a.lists + item * a.list_cap;
     bool ok = true;
@@ -1143,7 +1164,7 @@ __global__ void __launch_bounds__(192, 2)
       mbar_wait_drain(full_k, i & 1);
       if (i > 0) mbar_wait_drain(full_v, (i - 1) & 1);
     }
-  } else if (warp == 5) {
+  } else if (warp == 9) {
     // ---- products ----
     if (lane == 0) {
       const uint32_t sq = smem_u32(smem + L::oQ), sk = smem_u32(smem + L::oK), sv = smem_u32(smem + L::oV);
@@ -1171,28 +1192,32 @@ __global__ void __launch_bounds__(192, 2)
       }
     }
   } else {
-    // ---- softmax: a thread has one pair ----
-    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    // ---- softmax: two threads have a pair, 64 keys of a unit each ----
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tH = tS + lanes + half * 64;            // this half's scores
     const float sc = a.scale_log2, big = __int_as_float(0x7f800000);
-    const uint32_t bit = tid < pairs ? 1u << r : 0u;
+    const uint32_t bit = pair < pairs ? 1u << r : 0u;
     const int pos0 = len - (a.cu[tile.s + 1] - t0);
     const int sees = min(pos0 + r, len - 1) + 1;           // keys that the row sees
+    float* maxima = reinterpret_cast<float*>(smem + L::oMax);
+    // the two warps of 32 pairs meet (64 threads; every one of them passes here
+    // the same number of times, whatever a wait says)
+    auto meet = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory"); };
     float m = -big, l = 0.0f;
     bool ok = true;
-    for (int i = 0; i < units && ok; ++i) {
-      ok = mbar_wait(full_k, i & 1, abort, 6) && mbar_wait(s_ready, i & 1, abort, 7);
-      if (!ok) break;
+    for (int i = 0; i < units; ++i) {
+      ok = ok && mbar_wait(full_k, i & 1, abort, 6) && mbar_wait(s_ready, i & 1, abort, 7);
       tc_fence_after();
       const int4* pages = info + (i & 1) * 8;
       // visible keys of each 32
-      uint32_t vis[4];
-      bool whole = true;                                   // every slot of the unit holds a key
+      uint32_t vis[2];
+      bool whole = true;                                   // every slot of the half holds a key
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 2; ++c) {
         vis[c] = 0;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {                      // 16 keys at a time: one page
-          const int k = c * 32 + e * 16;
+          const int k = half * 64 + c * 32 + e * 16;
           const int4 w = pages[k >> a.ps_log2];
           const int first = k & (a.page_size - 1);
           const int seen = (w.y & bit) ? min(w.z, sees - w.x) - first : 0;
@@ -1200,10 +1225,9 @@ __global__ void __launch_bounds__(192, 2)
           whole &= w.z == a.page_size;
         }
       }
+      const bool live = __all_sync(0xffffffffu, ok);
+      const bool any = __any_sync(0xffffffffu, vis[0] | vis[1]) && live;
       float mx = -big;
-      bool all[4];                     // (uniform) every lane sees every key of the 32
-#pragma unroll
-      for (int c = 0; c < 4; ++c) all[c] = __all_sync(0xffffffffu, vis[c] == 0xFFFFFFFFu);
       auto top = [&](const uint32_t (&x)[32], uint32_t v) {
         if (v == 0xFFFFFFFFu) {
 #pragma unroll
@@ -1213,36 +1237,47 @@ __global__ void __launch_bounds__(192, 2)
           for (int k = 0; k < 32; ++k) mx = fmaxf(mx, v >> k & 1 ? __uint_as_float(x[k]) : -big);
         }
       };
-#pragma unroll
-      for (int c = 0; c < 4; c += 2) {
-        if (!__any_sync(0xffffffffu, vis[c] | vis[c + 1])) continue;
+      if (any) {
         uint32_t x[32], y[32];
-        tmem_ld32x2(tS + lanes + c * 32, tS + lanes + c * 32 + 32, x, y);
-        top(x, vis[c]);
-        top(y, vis[c + 1]);
+        tmem_ld32x2(tH, tH + 32, x, y);
+        top(x, vis[0]);
+        top(y, vis[1]);
       }
-      mx *= sc;
-      const bool move = mx > m + 8.0f || (m == -big && mx > -big);
+      float* mine = maxima + (i & 1) * 256;
+      mine[half * 128 + pair] = mx;
+      meet();
+      mx = fmaxf(mx, mine[(half ^ 1) * 128 + pair]) * sc;
+      const bool move = mx > m;
       if (__any_sync(0xffffffffu, move)) {
         const float f = !move ? 1.0f : m == -big ? 0.0f : ex2(m - mx);
         if (move) m = mx;
         l *= f;
-        if (i > 0) {                   // (the last product is done: S came after it)
+        if (i > 0 && live) {           // (the last product is done: S came after it)
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
+          for (int c = 0; c < D / 64; ++c) {
+            const uint32_t at = tO + lanes + half * (D / 2) + c * 32;
             uint32_t o[32];
-            tmem_ld32(tO + lanes + c * 32, o);
+            tmem_ld32(at, o);
 #pragma unroll
             for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-            tmem_st32(tO + lanes + c * 32, o);
+            tmem_st32(at, o);
           }
         }
       }
       const float mm = m == -big ? 0.0f : m;
-      auto weights = [&](const uint32_t (&x)[32], int c, uint32_t (&p)[16]) {
+      // P of both halves lies over S's first 64 columns: every score is read
+      // (into P's registers) before any P is written
+      uint32_t p[2][16];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) p[c][k] = 0u;
+        if (!any || !__any_sync(0xffffffffu, vis[c])) continue;
+        uint32_t x[32];
+        tmem_ld32(tH + c * 32, x);
         // (uniform) some row sees a part of the 32 keys, or there are slots
         // without one; else a row sees all of them or none
-        const bool part = !all[c] && (!whole || __any_sync(0xffffffffu, vis[c] + 1u > 1u));
+        const bool part = !whole || __any_sync(0xffffffffu, vis[c] + 1u > 1u);
         const float off = vis[c] ? mm : big;               // (none: 2^-inf)
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
@@ -1252,47 +1287,46 @@ __global__ void __launch_bounds__(192, 2)
             v = vis[c] >> (k + 1) & 1 ? v : 0.0f;
           }
           l += u + v;
-          p[k / 2] = pack_bf16(u, v);
+          p[c][k / 2] = pack_bf16(u, v);
         }
-      };
-#pragma unroll
-      for (int c = 0; c < 4; c += 2) {
-        uint32_t p[16], q[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) p[k] = q[k] = 0u;
-        if (__any_sync(0xffffffffu, vis[c] | vis[c + 1])) {
-          uint32_t x[32], y[32];
-          tmem_ld32x2(tS + lanes + c * 32, tS + lanes + c * 32 + 32, x, y);
-          weights(x, c, p);
-          weights(y, c + 1, q);
-        }
-        tmem_st16(tS + lanes + c * 16, p);
-        tmem_st16(tS + lanes + c * 16 + 16, q);
       }
+      tc_fence_before();
+      meet();
+      tc_fence_after();
+      tmem_st16(tS + lanes + half * 32, p[0]);
+      tmem_st16(tS + lanes + half * 32 + 16, p[1]);
       tmem_wait_st();
       if (!whole) {
         // slots without a key hold anything: as zeros, P's zeros leave O alone
-        ok = mbar_wait(full_v, i & 1, abort, 8);
-        const int4 w = pages[tid >> a.ps_log2];
-        if (ok && (tid & (a.page_size - 1)) >= w.z)
+        ok = ok && mbar_wait(full_v, i & 1, abort, 8);
+        const int key = half * 64 + (tid & 63);            // (two threads a key: half a row each)
+        const int4 w = pages[key >> a.ps_log2];
+        if (ok && (key & (a.page_size - 1)) >= w.z)
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c)
-            *reinterpret_cast<uint4*>(smem + L::oV + (c >> 3) * L::kRows + tid * 128 + (c & 7) * 16) =
+          for (int c = 0; c < D / 16; ++c) {
+            const int x = (pair >> 6) * (D / 16) + c;
+            *reinterpret_cast<uint4*>(smem + L::oV + (x >> 3) * L::kRows + key * 128 + (x & 7) * 16) =
                 make_uint4(0u, 0u, 0u, 0u);
+          }
         fence_proxy_async_smem();
       }
       tc_fence_before();
       mbar_arrive(p_ready);
     }
-    if (ok && mbar_wait(o_done, (units - 1) & 1, abort, 9)) {
+    ok = ok && mbar_wait(o_done, (units - 1) & 1, abort, 9);
+    float* sums = maxima + (units & 1) * 256;
+    sums[half * 128 + pair] = l;
+    meet();
+    l += sums[(half ^ 1) * 128 + pair];
+    if (__all_sync(0xffffffffu, ok)) {
       tc_fence_after();
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       bool fine = l < big && m < big;
-      __nv_bfloat16* out = a.o + (int64_t)(t0 + r) * a.so_t + (int64_t)h * a.so_h;
+      __nv_bfloat16* out = a.o + (int64_t)(t0 + r) * a.so_t + (int64_t)h * a.so_h + half * (D / 2);
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = 0; c < D / 64; ++c) {
         uint32_t x[32];
-        tmem_ld32(tO + lanes + c * 32, x);
+        tmem_ld32(tO + lanes + half * (D / 2) + c * 32, x);
         uint32_t y[16];
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
@@ -1300,20 +1334,21 @@ __global__ void __launch_bounds__(192, 2)
           fine &= fabsf(u) < big && fabsf(v) < big;
           y[k / 2] = pack_bf16(u, v);
         }
-        if (tid < pairs)
+        if (pair < pairs)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             *reinterpret_cast<uint4*>(out + c * 32 + k * 8) = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
       }
-      if (tid < pairs) {
+      if (pair < pairs) {
         if (!fine) a.row_flags[t0 + r] = a.row_flags[a.T] = 1;
-        if (a.lse) a.lse[(int64_t)(t0 + r) * a.H + h] = l == 0.0f ? -big : (m + log2f(l)) * 0.6931471805599453f;
+        if (half == 0 && a.lse)
+          a.lse[(int64_t)(t0 + r) * a.H + h] = l == 0.0f ? -big : (m + log2f(l)) * 0.6931471805599453f;
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) tmem_dealloc(tS, 256);
+  if (warp == 9) tmem_dealloc(tS, 256);
 }
 
 template <int D, bool FP8, int NT, bool SPARSE>
@@ -1379,7 +1414,7 @@ static cudaError_t run_tiles(const CacheArgs& a, const CUtensorMap& mk, const CU
   auto k = cache_tile_kernel<D>;
   const cudaError_t e = once.allow(reinterpret_cast<const void*>(k), dev, TileSmem<D>::kBytes);
   if (e != cudaSuccess) return e;
-  k<<<dim3((unsigned)tiles, a.Hkv), 192, TileSmem<D>::kBytes, s>>>(mk, mv, a);
+  k<<<dim3((unsigned)tiles, a.Hkv), 320, TileSmem<D>::kBytes, s>>>(mk, mv, a);
   return cudaGetLastError();
 }
 
