@@ -16,7 +16,9 @@
  * seq_lens[s] - (cu[s+1] - t).  cu = NULL means one row for each sequence
  * (row s is sequence s; T must equal S).  A row sees the keys at positions up
  * to its own.  Rows from cu[S] on are padding: neither read nor written.
- * Sequences may be empty (cu[s] = cu[s+1]).
+ * Sequences may be empty (cu[s] = cu[s+1]).  cu ascends from 0; with one that
+ * does not, results are undefined, but nothing outside the buffers is read or
+ * written.
  *
  * Conventions are those of tiered_attn.h: host-side validation before any
  * launch, asynchronous work on `stream`, no allocation, device-side errors in
@@ -152,8 +154,9 @@ ta_status tiered_attn_cache_decode(const ta_cache_params* p, const ta_cache* cac
  * that is not finite adds no mass.
  * sel_dev: int32 [T, Hkv, n_select], a row's page indices (in its sequence)
  * in ascending order, then -1.  Only k_mean of the cache is read.  At most
- * 16384 pages of a sequence and 128 query heads of a key head (else
- * TA_ERR_UNSUPPORTED). */
+ * 16384 pages of a sequence, 128 query heads of a key head, 65535 sequences and
+ * 2^31 - 1 (row, key head) pairs (else TA_ERR_UNSUPPORTED).  Two to four
+ * launches. */
 ta_status tiered_attn_cache_select(const ta_cache_params* p, const ta_cache* cache,
                                    const void* Q_dev, const int32_t* cu_dev,
                                    const int32_t* seq_lens_dev, const int32_t* table_dev,
@@ -163,7 +166,9 @@ ta_status tiered_attn_cache_select(const ta_cache_params* p, const ta_cache* cac
  * by tiered_attn_cache_select, or any lists: entries below 0 and pages past
  * the row's position are skipped, a page listed twice counts twice).  O_dev:
  * bf16 [T, H, d]; lse_dev: f32 [T, H], or NULL.  A row without keys gives 0
- * and -inf.  One launch. */
+ * and -inf.  Where sequences have many rows, neighbouring rows share the loads
+ * of the pages they have in common; a row's result does not depend on what
+ * other rows hold but for its rounding.  One launch, or three with many rows. */
 ta_status tiered_attn_cache_sparse(const ta_cache_params* p, const ta_cache* cache,
                                    const void* Q_dev, const int32_t* sel_dev,
                                    const int32_t* cu_dev, const int32_t* seq_lens_dev,

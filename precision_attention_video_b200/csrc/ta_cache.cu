@@ -1193,9 +1193,11 @@ __global__ void __launch_bounds__(kSelThreads, WPI == 1 && E == 16 ? 4 : 1) cach
 
   if (t < rows_used(a)) {
     const int2 info = row_info(a)[t];
-    const int s = info.x;
+    // (a row that a malformed cu gives to no tile has none: no pages)
+    const bool known = (unsigned)info.x < (unsigned)a.S && (unsigned)info.y <= (unsigned)a.max_pages;
+    const int s = known ? info.x : 0;
     RowPages r;
-    r.n = info.y;
+    r.n = known ? info.y : 0;
     r.c0 = min(a.n_first, r.n);
     r.c1 = max(r.c0, r.n - a.n_recent);
     int* sel = a.sel + item * a.n_select;

@@ -272,8 +272,11 @@ ta_status tiered_attn_cache_select(const ta_cache_params* p, const ta_cache* cac
   ta_status st = validate(p);
   if (st != TA_OK) return st;
   if (p->n_select < 1) return TA_ERR_INVALID_ARG;
-  // a row's masses, and the queries of a key head, stand in shared memory
-  if (p->max_pages > ta::kMaxSelectPages || p->H / p->Hkv > 128) return TA_ERR_UNSUPPORTED;
+  // a row's masses, and the queries of a key head, stand in shared memory;
+  // sequences and (row, key head) items are grid dimensions
+  if (p->max_pages > ta::kMaxSelectPages || p->H / p->Hkv > 128 || p->S > 65535 ||
+      (int64_t)p->T * p->Hkv > 0x7fffffff)
+    return TA_ERR_UNSUPPORTED;
   if ((st = check_cache(p, cache, false, true)) != TA_OK) return st;
   if ((st = check_index(p, cu, lens, table)) != TA_OK) return st;
   if (!rows_ok(Q, p->stride_q_t, p->stride_q_h) || !aligned(sel, 4)) return TA_ERR_INVALID_ARG;

@@ -101,6 +101,8 @@ def test_c_abi_refuses_on_the_host():
     assert select(sel=None) == INV and select(n=n - 256) == WS
     assert select(p=other(n_select=0)) == INV and sparse(p=other(n_select=0)) == INV
     assert select(p=other(max_pages=16385, stride_table=16385), n=1 << 40) == UNS
+    assert select(p=other(S=70000, T=70000), n=1 << 50) == UNS
+    assert select(p=other(H=258, Hkv=2), n=1 << 50) == UNS
     assert decode(p=other(S=5000, T=5000)) == UNS
     assert sparse(sel=None) == INV
     assert C._fn("tiered_attn_cache_init")(None, 1 << 30, None) == INV

@@ -374,6 +374,9 @@ SELECT = [
     ([2000], [5], dict(ps=16, H=10, Hkv=2, d=64, n_select=40)),
     ([300, 900], [70, 0], dict(ps=32, H=3, Hkv=3, n_select=3, n_first=0, n_recent=3)),
     ([5000, 4000], [1, 1], dict(ps=16, H=32, Hkv=2, n_select=100, n_first=0, n_recent=1)),
+    # few rows a sequence, given by cu
+    ([600, 300, 10], [1, 1, 2], dict(ps=16, H=6, Hkv=3, n_select=5, pad=1)),
+    ([900, 40, 0, 2000], [2, 0, 1, 3], dict(ps=32, d=64, H=20, Hkv=1, n_select=8)),
 ]
 
 
