@@ -60,21 +60,21 @@ struct CacheArgs {
   int list_cap;                   // entries of a tile's page list
   int* row_flags;                 // [T] rows to do again on their own, [T]: any; null: all rows
   int* list_n;                    // [tile, Hkv] entries of the joint lists
+  int* tile_arrived;              // [kMaxTileParts] parts of a cut tile that are done
+  float* tile_parts;              // and their results
   int2* lists;                    // [tile, Hkv, list_cap] (page, bits of the rows that read it)
 };
 
 // Sparse attention takes rows of a sequence together where there are rows
-// enough: 32 (row, query head) columns to a tile.  0: rows on their own.
-constexpr int kGroupCols = 32;
-inline int group_rows(int G, int64_t T, int64_t S, int max_pages) {
-  return G <= kGroupCols / 2 && T >= 4 * S && max_pages <= kMaxSelectPages ? kGroupCols / G : 0;
-}
-// The same in tiles of 128 columns, at most 32 rows (the bits of a list).
+// enough: up to 128 (row, query head) pairs to a tile, at most 32 rows (the bits
+// of a list).  0: rows on their own.
 inline int tile_rows(int G, int64_t T, int64_t S, int max_pages) {
   if (G > 64 || T < 4 * S || max_pages > kMaxSelectPages) return 0;
   return 128 / G < 32 ? 128 / G : 32;
 }
-inline int64_t group_tiles(int rows, int64_t T, int64_t S) { return T / rows + S; }
+constexpr int kMaxTileParts = 512;                // parts of cut tiles: 256 threads' 64 + 2 numbers each
+constexpr size_t kTilePartBytes = (size_t)kMaxTileParts * 256 * 66 * 4;
+inline int64_t tile_count(int rows, int64_t T, int64_t S) { return T / rows + S; }
 
 // Doubles of a row of the choice's scratch: whole tiles of 128 pages.
 __host__ __device__ inline int64_t select_pitch(int max_pages) { return ((int64_t)max_pages + 127) / 128 * 128; }

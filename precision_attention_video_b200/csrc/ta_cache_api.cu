@@ -41,18 +41,15 @@ size_t select_bytes(const ta_cache_params* p) {
   return pitch * ((size_t)p->T * p->H * 8 + (size_t)p->S * p->Hkv * (4 * p->d + 8)) + T * p->H * 4 + (T + 2) * 8 +
          (size_t)p->T * p->Hkv * 8;
 }
-// Sparse attention's: joint page lists and their lengths, the rows' flags.
+// Sparse attention's: parts of cut tiles, joint page lists and their lengths,
+// the rows' flags.
 size_t sparse_bytes(const ta_cache_params* p) {
   if (p->n_select <= 0) return 0;
-  size_t most = 0;
-  for (const int rows : {ta::group_rows(p->H / p->Hkv, p->T, p->S, p->max_pages),
-                         ta::tile_rows(p->H / p->Hkv, p->T, p->S, p->max_pages)}) {
-    if (!rows) continue;
-    const size_t items = (size_t)ta::group_tiles(rows, p->T, p->S) * p->Hkv;
-    const size_t n = items * ((size_t)rows * p->n_select * 8 + 4) + ((size_t)p->T + 1) * 4;
-    most = n > most ? n : most;
-  }
-  return most;
+  const int rows = ta::tile_rows(p->H / p->Hkv, p->T, p->S, p->max_pages);
+  if (!rows) return 0;
+  const size_t items = (size_t)ta::tile_count(rows, p->T, p->S) * p->Hkv;
+  return ta::kTilePartBytes + items * ((size_t)rows * p->n_select * 8 + 4) +
+         ((size_t)p->T + 1 + ta::kMaxTileParts) * 4;
 }
 size_t scratch_bytes(const ta_cache_params* p) {
   const size_t a = select_bytes(p), b = sparse_bytes(p);

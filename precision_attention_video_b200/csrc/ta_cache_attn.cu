@@ -39,14 +39,13 @@
 namespace ta {
 namespace {
 
-template <int D, bool FP8, int NT, bool GROUP = false>
+template <int D, bool FP8, int NT>
 struct Cfg {
   static constexpr int kRow = D * (FP8 ? 1 : 2);          // bytes of a key
-  static constexpr int kKT = !GROUP && kRow > 128 ? 1 : 2;   // 16-key tiles of a warp
-  static constexpr int kWarps = GROUP ? 16 : 8;           // computing warps, one more loads
+  static constexpr int kKT = kRow > 128 ? 1 : 2;          // 16-key tiles of a warp
+  static constexpr int kWarps = 8;                        // computing warps, one more loads
   static constexpr int kThreads = 32 * (kWarps + 1);
-  static constexpr int kKeyWarps = GROUP ? 4 : 8;         // of these, side by side along the keys
-  static constexpr int kUnit = kKeyWarps * 16 * kKT;      // keys of a unit (one stage)
+  static constexpr int kUnit = kWarps * 16 * kKT;         // keys of a unit (one stage)
   static constexpr int kCols = kRow > 128 ? 2 : 1;        // 128-byte columns of a row
   static constexpr int kColB = kRow / kCols;              // 128 or 64
   static constexpr int kTile = kUnit * kRow;               // 16 or 32 KB
@@ -55,11 +54,10 @@ struct Cfg {
   static constexpr int kStages = kStage > 40000 ? 3 : 6;
   static constexpr int kRegs = D / 16 * NT * 4;           // accumulators of a lane
   static constexpr int oJoin = kStages * ((kStage + 1023) / 1024 * 1024);
-  static constexpr int kJoin = GROUP ? 1 : (NT == 1 ? 4 : 2);   // key warps that join at a time
-  static constexpr int kColGroups = kWarps / kKeyWarps;
-  static constexpr int oML = oJoin + kColGroups * kJoin * kRegs * 32 * 4;
+  static constexpr int kJoin = NT == 1 ? 4 : 2;           // warps that join at a time
+  static constexpr int oML = oJoin + kJoin * kRegs * 32 * 4;
   static constexpr int oCnt = oML + 2 * 2 * kWarps * 8 * NT * 4;         // m, l; items take turns
-  static constexpr int oBar = oCnt + kStages * (kUnit / 16) * (GROUP ? 16 : 4);
+  static constexpr int oBar = oCnt + kStages * (kUnit / 16) * 4;
   static constexpr int oMisc = oBar + 2 * kStages * 8;
   static constexpr int oPre = oMisc + 128;
   static constexpr int kBytes = oPre + 1024;              // 1024 to align; + a decode's prefix
@@ -446,14 +444,12 @@ __device__ __forceinline__ void fold_unit(Fold<D, NT>& f, const unsigned char* s
   }
 }
 
-// Joins the key warps of each column group, whose columns and numerators the
-// readers below then give.  sm: maxima and sums, [warp][8 NT] each; an item's may
+// Joins the warps, whose columns and numerators the readers below then give.  sm: maxima and sums, [warp][8 NT] each; an item's may
 // still be read while the next one's are written, so items take turns.
 template <class C, int D, bool FP8, int NT>
 __device__ __forceinline__ void join_warps(Fold<D, NT>& f, float* join, float* sm) {
-  constexpr int KW = C::kKeyWarps;
+  constexpr int KW = C::kWarps;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tg = lane & 3;
-  const int kw = warp % KW, cg = warp / KW;
   const float kNegInf = -__int_as_float(0x7f800000);
   float* sm_m = sm;
   float* sm_l = sm + C::kWarps * 8 * NT;
@@ -475,7 +471,7 @@ __device__ __forceinline__ void join_warps(Fold<D, NT>& f, float* join, float* s
     for (int j = 0; j < 2; ++j) {
       float mm = kNegInf;
       for (int w = 0; w < KW; ++w)
-        mm = fmaxf(mm, sm_m[(cg * KW + w) * 8 * NT + nt * 8 + 2 * tg + j]);
+        mm = fmaxf(mm, sm_m[w * 8 * NT + nt * 8 + 2 * tg + j]);
       float x = f.m[nt][j] == kNegInf ? 0.0f : ex2(f.m[nt][j] - mm);
       if (FP8) x *= f.vmax * 3.0517578125e-5f;     // back to V's own units
 #pragma unroll
@@ -484,9 +480,9 @@ __device__ __forceinline__ void join_warps(Fold<D, NT>& f, float* join, float* s
         f.acc[c][nt][j + 2] *= x;
       }
     }
-  float* mine = join + (cg * C::kJoin + (kw & (C::kJoin - 1))) * (C::kRegs * 32) + lane;
+  float* mine = join + (warp & (C::kJoin - 1)) * (C::kRegs * 32) + lane;
   for (int r = KW / C::kJoin - 1; r >= 0; --r) {
-    if (kw / C::kJoin == r) {
+    if (warp / C::kJoin == r) {
       const bool put_first = r == KW / C::kJoin - 1;
 #pragma unroll
       for (int c = 0; c < D / 16; ++c)
@@ -501,13 +497,13 @@ __device__ __forceinline__ void join_warps(Fold<D, NT>& f, float* join, float* s
     compute_sync<C::kWarps>();
   }
 }
-// Numerator d of column nn (8 NT of them in a group).
+// Numerator d of column nn.
 template <class C, int D, bool FP8, int NT>
 __device__ __forceinline__ float joined_at(const float* join, int nn, int d) {
-  const int cg = nn / (8 * NT), n = nn % (8 * NT), dd = d & 15;
+  const int dd = d & 15;
   const int gg = FP8 ? dd >> 1 : dd & 7, hi = FP8 ? dd & 1 : dd >> 3;
-  const int at = (((d >> 4) * NT + (n >> 3)) * 4 + hi * 2 + (n & 1)) * 32 + gg * 4 + ((n & 7) >> 1);
-  const float* b = join + cg * C::kJoin * (C::kRegs * 32) + at;
+  const int at = (((d >> 4) * NT + (nn >> 3)) * 4 + hi * 2 + (nn & 1)) * 32 + gg * 4 + ((nn & 7) >> 1);
+  const float* b = join + at;
   float x = b[0];
 #pragma unroll
   for (int k = 1; k < C::kJoin; ++k) x += b[k * (C::kRegs * 32)];
@@ -516,10 +512,10 @@ __device__ __forceinline__ float joined_at(const float* join, int nn, int d) {
 // Maximum and sum of column nn.
 template <class C, int NT>
 __device__ __forceinline__ void joined_state(const float* sm, int nn, float& mm, float& ll) {
-  constexpr int KW = C::kKeyWarps, N = 8 * NT;
+  constexpr int KW = C::kWarps, N = 8 * NT;
   const float kNegInf = -__int_as_float(0x7f800000);
-  const float* sm_m = sm + (nn / N) * KW * N + nn % N;
-  const float* sm_l = sm_m + C::kWarps * N;
+  const float* sm_m = sm + nn;
+  const float* sm_l = sm_m + KW * N;
   mm = kNegInf;
   ll = 0.0f;
 #pragma unroll
@@ -818,10 +814,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT>::kThreads, 1)
 // Sparse attention of many rows
 // ---------------------------------------------------------------------------
 // Rows next to each other read mostly the same pages, and one at a time they
-// are bound by what the L2 cache delivers (5.6 GB for 1300 rows of 1024 keys,
-// 571 us).  So up to 32 (row, query head) columns of a sequence share their
-// loads: a first kernel joins their lists, each page with the bits of the
-// rows that read it, and the columns of the others see none of its keys.
+// are bound by what the L2 cache delivers (1332 rows of 1024 keys: 595 us).  So
+// up to 128 (row, query head) pairs of a sequence share their loads: a first
+// kernel joins their lists, each page with the bits of the rows that read it,
+// and the pairs of the other rows see none of its keys.
 //
 // A weight of zero times a value that is not finite would spoil the columns
 // that do not see it.  Rows with a result that is not finite are therefore
@@ -836,7 +832,10 @@ __global__ void __launch_bounds__(256) cache_lists_kernel(const CacheArgs a) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hk = blockIdx.y;
   const RowTile tile = row_tile(a, blockIdx.x, a.tile_rows);
   const int64_t item = (int64_t)blockIdx.x * a.Hkv + hk;
-  if (hk == 0 && blockIdx.x == 0 && tid == 0) a.row_flags[a.T] = 0;
+  if (hk == 0 && blockIdx.x == 0) {
+    for (int i = tid; i < kMaxTileParts; i += 256) a.tile_arrived[i] = 0;
+    if (tid == 0) a.row_flags[a.T] = 0;
+  }
   if (hk == 0)
     for (int t = tile.t0 + tid; t < tile.t1; t += 256) {
       a.row_flags[t] = 0;
@@ -889,172 +888,25 @@ __global__ void __launch_bounds__(256) cache_lists_kernel(const CacheArgs a) {
   if (tid == 0) a.list_n[item] = at;
 }
 
-template <int D, bool FP8>
-__global__ void __launch_bounds__(Cfg<D, FP8, 1, true>::kThreads, 1)
-    cache_group_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-                       const CacheArgs a, int tiles) {
-  constexpr int NT = 1;                // column tiles of a warp
-  using C = Cfg<D, FP8, NT, true>;
-  constexpr int kWarps = C::kWarps;
-  constexpr int KT = C::kKT, KW = C::kKeyWarps, kGroups = C::kUnit / 16;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // of each 16 keys of a stage: their first position, the rows that read them,
-  // how many exist
-  int4* info = reinterpret_cast<int4*>(smem + C::oCnt);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::oBar);
-  uint64_t* empty = full + C::kStages;
-  int* misc = reinterpret_cast<int*>(smem + C::oMisc);
-  const AbortCtx abort{misc, a.status};
-  if (tid == 0) {
-    for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], kWarps);
-    }
-    misc[0] = 0;
-    fence_mbar_init();
-  }
-  __syncthreads();
-  const int items = tiles * a.Hkv, ppu = C::kUnit >> a.ps_log2;
-  auto units_of = [&](int n) { return max(1, (n + ppu - 1) / ppu); };
-
-  if (warp == kWarps) {
-    // ---- loads: lane i brings page i of the unit ----
-    int issued = 0;
-    bool ok = true;
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      const RowTile tile = row_tile(a, item / a.Hkv, a.tile_rows);
-      if (tile.t0 >= tile.t1) continue;
-      const int hk = item % a.Hkv, n = a.list_n[item], units = units_of(n), len = seq_len(a, tile.s);
-      const int2* list = a.lists + (int64_t)item * a.list_cap;
-      int2 next = lane < ppu && lane < n ? list[lane] : make_int2(0, 0);
-      for (int u = 0; u < units; ++u) {
-        const int2 e = next;
-        const int at = (u + 1) * ppu + lane;
-        next = lane < ppu && at < n ? list[at] : make_int2(0, 0);
-        int vc = e.y ? min(a.page_size, max(0, len - (e.x << a.ps_log2))) : 0, page = 0;
-        if (vc > 0) {
-          page = page_of(a, tile.s, e.x);
-          if (page < 0) vc = 0;
-        }
-        const uint32_t live = __ballot_sync(0xffffffffu, vc > 0);
-        const int st = issued % C::kStages;
-        if (issued >= C::kStages && !mbar_wait(&empty[st], ((issued / C::kStages) - 1) & 1, abort, 1)) {
-          ok = false;
-          break;
-        }
-        unsigned char* stage = smem + st * C::kStageStep;
-        const int src = (lane & (kGroups - 1)) >> (a.ps_log2 - 4);
-        const int first = 16 * (lane & ((1 << (a.ps_log2 - 4)) - 1));
-        const int4 w = make_int4((__shfl_sync(0xffffffffu, e.x, src) << a.ps_log2) + first,
-                                 __shfl_sync(0xffffffffu, e.y, src),
-                                 min(16, max(0, __shfl_sync(0xffffffffu, vc, src) - first)), 0);
-        if (lane < kGroups) info[st * kGroups + lane] = w;
-        __syncwarp();
-        if (lane == 0)
-          mbar_arrive_expect_tx(&full[st], (uint32_t)a.page_size * (2 * C::kRow + (FP8 ? 8 : 0)) * __popc(live));
-        __syncwarp();
-        if (vc > 0) {
-          const int off = lane << a.ps_log2;
-#pragma unroll
-          for (int c = 0; c < C::kCols; ++c) {
-            unsigned char* dst = stage + c * (C::kUnit * C::kColB) + off * C::kColB;
-            tma_load_4d(dst, &mk, &full[st], c * 64, 0, hk, page);
-            tma_load_4d(dst + C::kTile, &mv, &full[st], c * 64, 0, hk, page);
-          }
-          if (FP8) {
-            const int64_t so = ((int64_t)page * a.Hkv + hk) << a.ps_log2;
-            bulk_load(stage + 2 * C::kTile + off * 4, a.k_scale + so, a.page_size * 4, &full[st]);
-            bulk_load(stage + 2 * C::kTile + C::kScales + off * 4, a.v_scale + so, a.page_size * 4, &full[st]);
-          }
-        }
-        ++issued;
-      }
-    }
-    if (!ok)                           // nothing may still be writing shared memory
-      for (int i = max(0, issued - C::kStages); i < issued; ++i)
-        mbar_wait_drain(&full[i % C::kStages], (i / C::kStages) & 1);
-    return;
-  }
-
-  // ---- compute: 4 warps along the keys by 4 along the columns ----
-  const int g = lane >> 2, tg = lane & 3, kw = warp % KW, cg = warp / KW;
-  Fold<D, NT> f;
-  float* join = reinterpret_cast<float*>(smem + C::oJoin);
-  float* const sm0 = reinterpret_cast<float*>(smem + C::oML);
-  int turn = 0, taken = 0;
-  for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    const RowTile tile = row_tile(a, item / a.Hkv, a.tile_rows);
-    if (tile.t0 >= tile.t1) continue;
-    const int hk = item % a.Hkv, units = units_of(a.list_n[item]), len = seq_len(a, tile.s);
-    const int cols = (tile.t1 - tile.t0) * a.G, t0 = tile.t0;
-    const int pos0 = len - (a.cu[tile.s + 1] - t0);        // position of the tile's first row
-    f.vmax = 0.0f;
-    int last[NT][2];                                       // last position that a lane's columns see
-    uint32_t bit[NT][2];                                   // and their rows' bits
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int c = cg * 8 * NT + nt * 8 + g, r = c / a.G;
-      fold_query<D, FP8, NT>(f, nt, a.q + (int64_t)(t0 + r) * a.sq_t + (int64_t)(hk * a.G + c - r * a.G) * a.sq_h,
-                             c < cols, a.scale_log2);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int cc = cg * 8 * NT + nt * 8 + 2 * tg + j, rr = cc / a.G;
-        last[nt][j] = min(pos0 + rr, len - 1);
-        bit[nt][j] = cc < cols ? 1u << rr : 0u;
-      }
-    }
-    uint32_t mine = 0;                                     // rows of this warp's columns
-    for (int c = cg * 8 * NT; c < min(cols, (cg + 1) * 8 * NT); ++c) mine |= 1u << (c / a.G);
-
-    for (int u = 0; u < units; ++u, ++taken) {
-      const int st = taken % C::kStages;
-      const bool ok = mbar_wait(&full[st], (taken / C::kStages) & 1, abort, 2);
-      int cn[KT], kb[KT], any = 0;
-      uint32_t rows[KT];
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt) {
-        const int4 w = info[st * kGroups + KT * kw + kt];
-        kb[kt] = w.x;
-        rows[kt] = w.y & mine;
-        cn[kt] = ok && rows[kt] ? w.z : 0;
-        any |= cn[kt];
-      }
-      if (any)
-        fold_unit<C, D, FP8, NT>(f, smem + st * C::kStageStep, kw * 16 * KT, cn, [&](int kt, int e, int nt, int j) {
-          return (rows[kt] & bit[nt][j]) != 0 && g + 8 * e < cn[kt] && kb[kt] + g + 8 * e <= last[nt][j];
-        });
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
-    }
-
-    float* sm = sm0 + turn * (2 * C::kWarps * 8 * NT);
-    join_warps<C, D, FP8, NT>(f, join, sm);
-    for (int e = tid; e < cols * (D / 2); e += 32 * kWarps) {
-      const int c = e / (D / 2), d = 2 * (e - c * (D / 2)), r = c / a.G, h = hk * a.G + c - r * a.G;
-      float mm, ll;
-      joined_state<C, NT>(sm, c, mm, ll);
-      const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-      const float x = joined_at<C, D, FP8, NT>(join, c, d) * inv, y = joined_at<C, D, FP8, NT>(join, c, d + 1) * inv;
-      const float big = __int_as_float(0x7f800000);
-      if (!(fabsf(x) < big && fabsf(y) < big && ll < big && mm < big))
-        a.row_flags[t0 + r] = a.row_flags[a.T] = 1;
-      *reinterpret_cast<uint32_t*>(a.o + (int64_t)(t0 + r) * a.so_t + (int64_t)h * a.so_h + d) = pack_bf16(x, y);
-      if (d == 0 && a.lse)
-        a.lse[(int64_t)(t0 + r) * a.H + h] = ll == 0.0f ? -big : (mm + log2f(ll)) * 0.6931471805599453f;
-    }
-    turn ^= 1;
-  }
-}
-
-// The same for bf16 caches and tiles of up to 128 (row, query head) pairs, on
-// tcgen05: the pairs are the 128 rows of S = Q K^T and O += P V, two threads of
-// the softmax share one of them (64 keys each; one alone took 135 us where two
-// take TIME us), S and P (bf16, over S's own columns) and O stand in TMEM.  A block has one K and one V buffer: K of the next unit loads
-// while this one's softmax runs, V while the next S does, and two blocks share
-// an SM.  With the mma.sync kernel above 1330 rows took 245 us, bound by its
-// instructions (32 columns for each key read); here a key serves 128 rows.
+// Tiles of up to 128 (row, query head) pairs on tcgen05: the pairs are the 128
+// rows of S = Q K^T and O += P V, two threads of the softmax share one of them
+// (64 keys each), S and P (bf16, over S's own columns) and O stand in TMEM.  A
+// block has one K and one V buffer: K of the next unit loads while this one's
+// softmax runs, V while the next S does, and two blocks share an SM.
+//
+// Codes of FP8 caches load into the upper half of their buffer, and the softmax
+// threads widen them in place to bf16 with the scale multiplied in, which is
+// exact (4 significant bits, scales are powers of two).
+//
+// The tiles that are left after whole rounds of the GPU's places are cut along
+// their keys, so that the last round is full too: their parts meet in the
+// workspace, and the block that arrives last joins them in order.
+//
+// 1332 rows of 32 query heads, 1024 keys each, bf16: 115 us with the lists (107
+// without), FP8 143; 131 without the cut, 145 with one thread a pair.  A tile's
+// blocks wait for one another's steps (S, softmax, O) and two blocks an SM
+// cover a part of it: the tensor pipe is busy a third of the time.  Units of 64
+// keys with a second S, multiplied ahead of the softmax, took 13 us more.
 //
 // A row's greatest weight is exactly 1, so P's rounding spares it (letting the
 // maximum lag and O be rescaled seldom was 7 percent faster and a fifth less
@@ -1066,30 +918,71 @@ struct TileSmem {
   static constexpr int oQ = 0, oK = kOp, oV = 2 * kOp;
   static constexpr int oInfo = 3 * kOp;            // [2][8] int4: the pages of a unit
   static constexpr int oMax = oInfo + 256;         // [2][2][128] maxima of a row's halves, then sums
-  static constexpr int oBar = oMax + 2048;
+  static constexpr int oScale = oMax + 2048;       // FP8: [2][128] scales of K and V
+  static constexpr int oBar = oScale + 1024;
   static constexpr int kBytes = oBar + 64 + 1024;  // 1024 to align
 };
 
+// This thread's half row of codes to bf16 times `scale` (zeros where !keep), in
+// place: the codes stand in the tile's upper half, all 256 threads read them
+// before any writes.
 template <int D>
+__device__ __forceinline__ void widen(unsigned char* tile, int key, int half, float scale, bool keep) {
+  using L = TileSmem<D>;
+  constexpr int N = D / 32;                        // chunks of 16 codes
+  uint4 w[N];
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    const int x = half * N + c;
+    w[c] = *reinterpret_cast<const uint4*>(tile + L::kOp / 2 + key * D +
+                                           ((x ^ (D == 128 ? key & 7 : (key >> 1) & 3)) << 4));
+  }
+  asm volatile("bar.sync 5, 256;" ::: "memory");
+  auto two = [&](uint32_t f16x2) -> uint32_t {
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f16x2));
+    return keep ? pack_bf16(v.x * scale, v.y * scale) : 0u;
+  };
+#pragma unroll
+  for (int c = 0; c < N; ++c)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int y = 2 * (half * N + c) + e;
+      const uint32_t u = e ? w[c].z : w[c].x, v = e ? w[c].w : w[c].y;
+      *reinterpret_cast<uint4*>(tile + (y >> 3) * L::kRows + key * 128 + (((y & 7) ^ (key & 7)) << 4)) =
+          make_uint4(two(e4m3_f16x2_lo(u)), two(e4m3_f16x2_hi(u)), two(e4m3_f16x2_lo(v)), two(e4m3_f16x2_hi(v)));
+    }
+  fence_proxy_async_smem();
+}
+
+template <int D, bool FP8>
 __global__ void __launch_bounds__(320, 2)
     cache_tile_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-                      const CacheArgs a) {
+                      const CacheArgs a, int whole_items, int cuts) {
   using L = TileSmem<D>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int hk = blockIdx.y;
-  const RowTile tile = row_tile(a, blockIdx.x, a.tile_rows);
+  const int over = max(0, (int)blockIdx.x - whole_items);
+  const int64_t item = (int)blockIdx.x < whole_items ? (int)blockIdx.x : whole_items + over / cuts;
+  const int hk = (int)(item % a.Hkv);
+  const RowTile tile = row_tile(a, (int)(item / a.Hkv), a.tile_rows);
   if (tile.t0 >= tile.t1) return;
-  const int64_t item = (int64_t)blockIdx.x * a.Hkv + hk;
-  const int n = a.list_n[item], ppu = 128 >> a.ps_log2, units = max(1, (n + ppu - 1) / ppu);
+  const int n = a.list_n[item], ppu = 128 >> a.ps_log2, all_units = max(1, (n + ppu - 1) / ppu);
+  // this block's units: all of them, or part `cut` of `parts`
+  const int parts = (int)blockIdx.x < whole_items ? 1 : min(cuts, all_units);
+  const int cut = (int)blockIdx.x < whole_items ? 0 : over % cuts;
+  if (cut >= parts) return;
+  const int unit0 = (int)((int64_t)all_units * cut / parts);
+  const int units = (int)((int64_t)all_units * (cut + 1) / parts) - unit0;
   const int len = seq_len(a, tile.s), t0 = tile.t0, pairs = (tile.t1 - t0) * a.G;
 
   int4* info = reinterpret_cast<int4*>(smem + L::oInfo);   // first position, rows' bits, keys that exist
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::oBar);
-  uint64_t *full_k = bars, *full_v = bars + 1, *s_ready = bars + 2, *p_ready = bars + 3, *o_done = bars + 4;
-  uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 5);
-  int* flag = reinterpret_cast<int*>(bars + 6);
+  uint64_t *full_k = bars, *full_v = bars + 1, *s_ready = bars + 2, *p_ready = bars + 3, *o_done = bars + 4,
+           *k_ready = FP8 ? bars + 5 : full_k;             // K in bf16
+  uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 6);
+  int* flag = reinterpret_cast<int*>(bars + 7);            // [0]: a wait gave up, [1]: the last part
+  float* scales = reinterpret_cast<float*>(smem + L::oScale);
   const AbortCtx abort{flag, a.status};
   if (tid == 0) {
     mbar_init(full_k, 1);
@@ -1097,6 +990,7 @@ __global__ void __launch_bounds__(320, 2)
     mbar_init(s_ready, 1);
     mbar_init(p_ready, 256);
     mbar_init(o_done, 1);
+    if (FP8) mbar_init(k_ready, 256);
     *flag = 0;
     fence_mbar_init();
   }
@@ -1132,14 +1026,14 @@ __global__ void __launch_bounds__(320, 2)
     bool ok = true;
     int i = 0;
     for (; i < units && ok; ++i) {
-      const int at = i * ppu + lane;
+      const int at = (unit0 + i) * ppu + lane;
       const int2 e = lane < ppu && at < n ? list[at] : make_int2(0, 0);
       int vc = e.y ? min(a.page_size, max(0, len - (e.x << a.ps_log2))) : 0, page = 0;
       if (vc > 0) {
         page = page_of(a, tile.s, e.x);
         if (page < 0) vc = 0;
       }
-      const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, vc > 0)) * a.page_size * (2 * D);
+      const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, vc > 0)) * a.page_size * (FP8 ? D + 4 : 2 * D);
       if (i > 0) ok = mbar_wait(s_ready, (i - 1) & 1, abort, 1);       // K is free
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
       if (lane < ppu) info[(i & 1) * 8 + lane] = make_int4(e.x << a.ps_log2, e.y, vc, 0);
@@ -1147,18 +1041,30 @@ __global__ void __launch_bounds__(320, 2)
       if (lane == 0) mbar_arrive_expect_tx(full_k, bytes);
       __syncwarp();
       const int off = lane << a.ps_log2;
-      if (vc > 0)
+      if (vc > 0) {
+        if constexpr (FP8) {
+          tma_load_4d(smem + L::oK + L::kOp / 2 + off * D, &mk, full_k, 0, 0, hk, page);
+          bulk_load(scales + off, a.k_scale + (((int64_t)page * a.Hkv + hk) << a.ps_log2), a.page_size * 4, full_k);
+        } else {
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-          tma_load_4d(smem + L::oK + c * L::kRows + off * 128, &mk, full_k, c * 64, 0, hk, page);
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(smem + L::oK + c * L::kRows + off * 128, &mk, full_k, c * 64, 0, hk, page);
+        }
+      }
       if (i > 0) ok = mbar_wait(o_done, (i - 1) & 1, abort, 2);        // V is free
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
       if (lane == 0) mbar_arrive_expect_tx(full_v, bytes);
       __syncwarp();
-      if (vc > 0)
+      if (vc > 0) {
+        if constexpr (FP8) {
+          tma_load_4d(smem + L::oV + L::kOp / 2 + off * D, &mv, full_v, 0, 0, hk, page);
+          bulk_load(scales + 128 + off, a.v_scale + (((int64_t)page * a.Hkv + hk) << a.ps_log2), a.page_size * 4, full_v);
+        } else {
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-          tma_load_4d(smem + L::oV + c * L::kRows + off * 128, &mv, full_v, c * 64, 0, hk, page);
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(smem + L::oV + c * L::kRows + off * 128, &mv, full_v, c * 64, 0, hk, page);
+        }
+      }
     }
     if (!ok) {                         // nothing may still be writing shared memory
       mbar_wait_drain(full_k, i & 1);
@@ -1172,7 +1078,7 @@ __global__ void __launch_bounds__(320, 2)
       for (int i = 0; i < units; ++i) {
         // (S's columns are free: they held P of the unit before, whose product
         // is ahead in the pipe)
-        if (!mbar_wait(full_k, i & 1, abort, 3)) break;
+        if (!mbar_wait(k_ready, i & 1, abort, 3)) break;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
@@ -1206,7 +1112,12 @@ __global__ void __launch_bounds__(320, 2)
     float m = -big, l = 0.0f;
     bool ok = true;
     for (int i = 0; i < units; ++i) {
-      ok = ok && mbar_wait(full_k, i & 1, abort, 6) && mbar_wait(s_ready, i & 1, abort, 7);
+      ok = ok && mbar_wait(full_k, i & 1, abort, 6);
+      if constexpr (FP8) {
+        widen<D>(smem + L::oK, pair, half, scales[pair], true);
+        mbar_arrive(k_ready);
+      }
+      ok = ok && mbar_wait(s_ready, i & 1, abort, 7);
       tc_fence_after();
       const int4* pages = info + (i & 1) * 8;
       // visible keys of each 32
@@ -1296,7 +1207,11 @@ __global__ void __launch_bounds__(320, 2)
       tmem_st16(tS + lanes + half * 32, p[0]);
       tmem_st16(tS + lanes + half * 32 + 16, p[1]);
       tmem_wait_st();
-      if (!whole) {
+      if constexpr (FP8) {
+        ok = ok && mbar_wait(full_v, i & 1, abort, 8);
+        const int4 w = pages[pair >> a.ps_log2];
+        widen<D>(smem + L::oV, pair, half, scales[128 + pair], (pair & (a.page_size - 1)) < w.z);
+      } else if (!whole) {
         // slots without a key hold anything: as zeros, P's zeros leave O alone
         ok = ok && mbar_wait(full_v, i & 1, abort, 8);
         const int key = half * 64 + (tid & 63);            // (two threads a key: half a row each)
@@ -1318,32 +1233,71 @@ __global__ void __launch_bounds__(320, 2)
     sums[half * 128 + pair] = l;
     meet();
     l += sums[(half ^ 1) * 128 + pair];
+    float o[D / 2];                                        // the thread's half of O's row
     if (__all_sync(0xffffffffu, ok)) {
       tc_fence_after();
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      bool fine = l < big && m < big;
-      __nv_bfloat16* out = a.o + (int64_t)(t0 + r) * a.so_t + (int64_t)h * a.so_h + half * (D / 2);
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
         uint32_t x[32];
         tmem_ld32(tO + lanes + half * (D / 2) + c * 32, x);
-        uint32_t y[16];
 #pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-          const float u = __uint_as_float(x[k]) * inv, v = __uint_as_float(x[k + 1]) * inv;
-          fine &= fabsf(u) < big && fabsf(v) < big;
-          y[k / 2] = pack_bf16(u, v);
+        for (int k = 0; k < 32; ++k) o[c * 32 + k] = __uint_as_float(x[k]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < D / 2; ++k) o[k] = 0.0f;
+    }
+    bool put = true;
+    if (parts > 1) {
+      // (thread-major: neighbouring threads' numbers stand next to each other)
+      float* mine = a.tile_parts + (int64_t)over * (256 * (D / 2 + 2)) + tid;
+#pragma unroll
+      for (int k = 0; k < D / 2; ++k) __stcg(mine + k * 256, o[k]);
+      __stcg(mine + (D / 2) * 256, m);
+      __stcg(mine + (D / 2 + 1) * 256, l);
+      __threadfence();
+      asm volatile("bar.sync 5, 256;" ::: "memory");
+      if (tid == 0)
+        flag[1] = atomicInc(reinterpret_cast<unsigned int*>(a.tile_arrived) + over / cuts, (unsigned)(parts - 1)) ==
+                  (unsigned)(parts - 1);
+      asm volatile("bar.sync 5, 256;" ::: "memory");
+      put = flag[1];
+      if (put) {
+        __threadfence();
+        const float* first = a.tile_parts + (int64_t)(over - cut) * (256 * (D / 2 + 2)) + tid;
+        m = -big;
+        l = 0.0f;
+        for (int q = 0; q < parts; ++q)
+          m = fmaxf(m, __ldcg(first + (int64_t)q * (256 * (D / 2 + 2)) + (D / 2) * 256));
+#pragma unroll
+        for (int k = 0; k < D / 2; ++k) o[k] = 0.0f;
+        for (int q = 0; q < parts; ++q) {
+          const float* part = first + (int64_t)q * (256 * (D / 2 + 2));
+          const float mq = __ldcg(part + (D / 2) * 256), f = mq == -big ? 0.0f : ex2(mq - m);
+          l += f * __ldcg(part + (D / 2 + 1) * 256);
+#pragma unroll
+          for (int k = 0; k < D / 2; ++k) o[k] += f * __ldcg(part + k * 256);
         }
-        if (pair < pairs)
+      }
+    }
+    if (put && pair < pairs) {
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      bool fine = l < big && m < big;
+      __nv_bfloat16* out = a.o + (int64_t)(t0 + r) * a.so_t + (int64_t)h * a.so_h + half * (D / 2);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<uint4*>(out + c * 32 + k * 8) = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+      for (int k = 0; k < D / 2; k += 8) {
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          y[e] = o[k + e] * inv;
+          fine &= fabsf(y[e]) < big;
+        }
+        *reinterpret_cast<uint4*>(out + k) =
+            make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
       }
-      if (pair < pairs) {
-        if (!fine) a.row_flags[t0 + r] = a.row_flags[a.T] = 1;
-        if (half == 0 && a.lse)
-          a.lse[(int64_t)(t0 + r) * a.H + h] = l == 0.0f ? -big : (m + log2f(l)) * 0.6931471805599453f;
-      }
+      if (!fine) a.row_flags[t0 + r] = a.row_flags[a.T] = 1;
+      if (half == 0 && a.lse)
+        a.lse[(int64_t)(t0 + r) * a.H + h] = l == 0.0f ? -big : (m + log2f(l)) * 0.6931471805599453f;
     }
   }
   tc_fence_before();
@@ -1395,26 +1349,20 @@ static cudaError_t run_lists(const CacheArgs& a, int64_t tiles, int dev, cudaStr
 }
 
 template <int D, bool FP8>
-static cudaError_t run_group(const CacheArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int64_t tiles,
-                             int sms, int dev, cudaStream_t s) {
-  using C = Cfg<D, FP8, 1, true>;
-  static_assert(C::kBytes <= 232448, "shared memory");
-  static OncePerDevice once;
-  auto k = cache_group_kernel<D, FP8>;
-  const cudaError_t e = once.allow(reinterpret_cast<const void*>(k), dev, C::kBytes);
-  if (e != cudaSuccess) return e;
-  k<<<(unsigned)(tiles * a.Hkv < sms ? tiles * a.Hkv : sms), C::kThreads, C::kBytes, s>>>(mk, mv, a, (int)tiles);
-  return cudaGetLastError();
-}
-
-template <int D>
 static cudaError_t run_tiles(const CacheArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int64_t tiles,
-                             int dev, cudaStream_t s) {
+                             int sms, int dev, cudaStream_t s) {
   static OncePerDevice once;
-  auto k = cache_tile_kernel<D>;
+  auto k = cache_tile_kernel<D, FP8>;
   const cudaError_t e = once.allow(reinterpret_cast<const void*>(k), dev, TileSmem<D>::kBytes);
   if (e != cudaSuccess) return e;
-  k<<<dim3((unsigned)tiles, a.Hkv), 320, TileSmem<D>::kBytes, s>>>(mk, mv, a);
+  // whole rounds of two blocks an SM; the items left are cut so that they fill
+  // one more (into 8 parts at most, of which a part has a few units)
+  const int64_t items = tiles * a.Hkv, places = 2 * sms < kMaxTileParts ? 2 * sms : kMaxTileParts;
+  const int64_t whole = items / places * places, left = items - whole;
+  int cuts = left ? (int)(places / left) : 1;
+  if (cuts > 8) cuts = 8;
+  k<<<(unsigned)(cuts > 1 ? whole + left * cuts : items), 320, TileSmem<D>::kBytes, s>>>(
+      mk, mv, a, (int)(cuts > 1 ? whole : items), cuts);
   return cudaGetLastError();
 }
 
@@ -1422,32 +1370,31 @@ cudaError_t launch_cache_attn(const CacheArgs& args, const CUtensorMap& mk, cons
                               bool sparse, cudaStream_t s) {
   CacheArgs a = args;
   a.row_flags = nullptr;
-  // rows together where there are tiles for every SM (fewer leave the GPU
-  // idle: the rows' own items split over it): bf16 in tiles of up to 128
-  // (row, query head) pairs and 32 rows, else in tiles of up to 32 pairs
+  // Rows together where there are enough for what the lists and the parts cost:
+  // bf16, 8 key heads of 4 query heads, 16 pages of 64 keys: 43 rows took 31 us
+  // either way, 75 rows 45 us on their own and 37 together, 183 rows 92 and 40.
+  // FP8's codes are widened, which 75 rows (40 and 42 us) do not earn back and
+  // 183 (81 and 45) do.
   if (sparse && a.cu) {
     int dev = 0, sms = 0;
     cudaError_t e = device_sms(dev, sms);
     if (e != cudaSuccess) return e;
-    int rows = a.fp8 ? 0 : tile_rows(a.G, a.T, a.S, a.max_pages);
-    const bool big = rows && (int64_t)a.T / rows * a.Hkv >= sms;
-    if (!big) rows = group_rows(a.G, a.T, a.S, a.max_pages);
-    const int64_t tiles = rows ? group_tiles(rows, a.T, a.S) : 0;
-    if (rows && (big || (int64_t)a.T / rows * a.Hkv >= 2 * sms) && tiles * a.Hkv < 0x7fffffff) {
+    const int rows = tile_rows(a.G, a.T, a.S, a.max_pages);
+    const int64_t tiles = rows ? tile_count(rows, a.T, a.S) : 0;
+    if (rows && (int64_t)a.T * a.Hkv >= (a.fp8 ? 4 : 2) * sms && tiles * a.Hkv < 0x7fffffff) {
       a.tile_rows = rows;
       a.list_cap = rows * a.n_select;
-      char* w = reinterpret_cast<char*>(a.scratch);
-      a.lists = reinterpret_cast<int2*>(w);
+      a.tile_parts = reinterpret_cast<float*>(a.scratch);
+      a.lists = reinterpret_cast<int2*>(reinterpret_cast<char*>(a.scratch) + kTilePartBytes);
       a.list_n = reinterpret_cast<int*>(a.lists + tiles * a.Hkv * a.list_cap);
-      a.row_flags = a.list_n + tiles * a.Hkv;
+      a.tile_arrived = a.list_n + tiles * a.Hkv;
+      a.row_flags = a.tile_arrived + kMaxTileParts;
       e = run_lists(a, tiles, dev, s);
       if (e == cudaSuccess) {
-        if (big)
-          e = a.d == 128 ? run_tiles<128>(a, mk, mv, tiles, dev, s) : run_tiles<64>(a, mk, mv, tiles, dev, s);
-        else if (a.d == 128)
-          e = a.fp8 ? run_group<128, true>(a, mk, mv, tiles, sms, dev, s) : run_group<128, false>(a, mk, mv, tiles, sms, dev, s);
+        if (a.d == 128)
+          e = a.fp8 ? run_tiles<128, true>(a, mk, mv, tiles, sms, dev, s) : run_tiles<128, false>(a, mk, mv, tiles, sms, dev, s);
         else
-          e = a.fp8 ? run_group<64, true>(a, mk, mv, tiles, sms, dev, s) : run_group<64, false>(a, mk, mv, tiles, sms, dev, s);
+          e = a.fp8 ? run_tiles<64, true>(a, mk, mv, tiles, sms, dev, s) : run_tiles<64, false>(a, mk, mv, tiles, sms, dev, s);
       }
       if (e != cudaSuccess) return e;
     }

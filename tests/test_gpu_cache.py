@@ -499,6 +499,10 @@ MANY = [
     ([700], [430], dict(H=64, Hkv=4, ps=128, n_select=3)),
     ([64, 3, 90], [310, 0, 333], dict(H=64, Hkv=8, ps=16, n_select=9, layout="nhd")),
     ([5000], [600], dict(H=24, Hkv=8, ps=32, n_select=40, scale=1.0)),
+    # tiles of one head; whole tiles and cut ones; every tile cut
+    ([0], [700], dict(H=40, Hkv=40, d=64, ps=16, n_select=4)),
+    ([2000, 9], [1300, 25], dict(H=32, Hkv=8, n_select=12)),
+    ([900], [40], dict(H=64, Hkv=8, ps=16, n_select=30)),
 ]
 
 
