@@ -851,8 +851,10 @@ struct Group {
 
 // Shared memory of a block's fp64 choice; reductions take turns on its halves,
 // so one barrier each is enough.
+constexpr int kExactHeads = 4;         // query heads taken at a time, at most
 struct ExactSmem {
-  double red[2][kSelThreads / 32];
+  double root[32];                     // 2^(k / 32)
+  double red[2][kExactHeads][kSelThreads / 32];
   int cnt[2][kSelThreads / 32][4];
   uint32_t keep[kMaxSelectPages / 32];
   int key[kSelThreads];                // upper words of the threads' greatest masses
@@ -863,17 +865,23 @@ struct ExactSmem {
 struct Block64 {
   ExactSmem& sm;
   int turn = 0;
-  template <typename Op>
-  __device__ __forceinline__ double reduce(double x, Op op) {
+  template <int N, typename Op>
+  __device__ __forceinline__ void reduce(double (&x)[N], Op op) {
+    double (*r)[kSelThreads / 32] = sm.red[turn ^= 1];
+#pragma unroll 1
+    for (int o = 16; o; o >>= 1)
 #pragma unroll
-    for (int o = 16; o; o >>= 1) x = op(x, __shfl_xor_sync(0xffffffffu, x, o));
-    double* r = sm.red[turn ^= 1];
-    if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = x;
+      for (int k = 0; k < N; ++k) x[k] = op(x[k], __shfl_xor_sync(0xffffffffu, x[k], o));
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if ((threadIdx.x & 31) == 0) r[k][threadIdx.x >> 5] = x[k];
     __syncthreads();
-    x = r[0];
 #pragma unroll
-    for (int w = 1; w < kSelThreads / 32; ++w) x = op(x, r[w]);
-    return x;
+    for (int k = 0; k < N; ++k) {
+      x[k] = r[k][0];
+#pragma unroll
+      for (int w = 1; w < kSelThreads / 32; ++w) x[k] = op(x[k], r[k][w]);
+    }
   }
   __device__ __forceinline__ void count(int (&x)[3]) {
     int (*r)[4] = sm.cnt[turn ^= 1];
@@ -891,77 +899,97 @@ struct Block64 {
   }
 };
 
-// The choice of one item from its fp64 logits, by the whole block; E pages a
-// thread (page r.c0 + tid + 256 i).
-template <int E>
-__device__ __noinline__ void choose64(const CacheArgs& a, int t, int hk, ExactSmem& sm) {
+// e^x for x <= 0, to about one unit in the last place: x = (32 e + k) ln2 / 32 + r,
+// 2^e 2^(k/32) (1 + r + r^2/2 + ... + r^6/720), with Cody and Waite's reduction
+// and Tang's table; the series' rest is 4e-18 of it.  Without a branch, so that
+// a thread's several run side by side (calls of exp took their turns).
+__device__ __forceinline__ double exp_down(const double* root, double x) {
+  const double magic = 6755399441055744.0;         // 1.5 * 2^52: the sum's low bits are the integer
+  const double y = fmax(x, -900.0);                // (0 below -745)
+  const double z = fma(y, 46.166241308446828384, magic), n = z - magic;
+  const int k = __double2loint(z), e = k >> 5;
+  double r = fma(n, -0x1.62e42feep-6, y);          // ln2 / 32 in two parts, the first of 32 bits
+  r = fma(n, -0x1.a39ef35793c76p-38, r);
+  double p = fma(r, 1.0 / 720.0, 1.0 / 120.0);
+  p = fma(r, p, 1.0 / 24.0);
+  p = fma(r, p, 1.0 / 6.0);
+  p = fma(r, p, 0.5);
+  p = fma(r, p, 1.0);
+  const double t = root[k & 31], v = fma(t * r, p, t);
+  const int e1 = e >> 1;                           // (two steps: the result may be subnormal)
+  return v * __hiloint2double((1023 + e1) << 20, 0) * __hiloint2double((1023 + e - e1) << 20, 0);
+}
+
+// The choice of one item from its fp64 logits, by the whole block.  x: room for
+// the logits of HN query heads, which hold those of all of them already
+// (`there`) or come from the item's scratch rows; the masses take the first one's
+// place.  The code runs once or twice in a block's life, so its loops stay rolled:
+// unrolled over a thread's pages, fetching instructions took half the time.
+template <int HN>
+__device__ __forceinline__ void choose64(const CacheArgs& a, int t, int hk, const RowPages r, ExactSmem& sm,
+                                      double* x, bool there) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const RowPages r = row_pages(a, t, row_seq(a, t));
   int* sel = a.sel + ((int64_t)t * a.Hkv + hk) * a.n_select;
-  const int nc = r.c1 - r.c0;
+  const int nc = r.c1 - r.c0, pitch = (int)select_pitch(a.max_pages);
   const int want = a.n_select - a.n_first - a.n_recent;
   Block64 blk{sm};
   auto larger = [](double x, double y) { return fmax(x, y); };
   auto plus = [](double x, double y) { return x + y; };
 
-  // ---- masses ----
-  double mass[E];
+  // ---- masses: a thread has pages tid + 256 i ----
+  if (tid < 32) sm.root[tid] = exp2(tid * 0.03125);        // (read behind the first reduction's barrier)
+  double top = -1.0;
+  double* all = logit_row(a, t, hk * a.G) + r.c0;          // masses between two sets of heads
+  for (int g0 = 0; g0 < a.G; g0 += HN) {
+    const int nh = min(HN, a.G - g0);
+    if (!there) {
+      const double* l = logit_row(a, t, hk * a.G + g0) + r.c0;
+#pragma unroll 4
+      for (int j = tid; j < nc; j += kSelThreads)
 #pragma unroll
-  for (int i = 0; i < E; ++i) mass[i] = 0.0;
-  constexpr int R = E <= 8 ? E : 1;                // logits kept in registers, the next head's too
-  double nx[R];
-  if (E <= 8) {
-    const double* l = logit_row(a, t, hk * a.G) + r.c0;
+        for (int h = 0; h < HN; ++h)
+          if (h < nh) cp_async8(x + h * pitch + j, l + (int64_t)h * pitch + j);
+      cp_async_wait_all();
+    }
+    double mx[HN], sum[HN], inv[HN];
 #pragma unroll
-    for (int i = 0; i < R; ++i) nx[i] = tid + kSelThreads * i < nc ? l[tid + kSelThreads * i] : -kInf64();
-  }
-  for (int gq = 0; gq < a.G; ++gq) {
-    const double* l = logit_row(a, t, hk * a.G + gq) + r.c0;
-    double x[R], mx = -kInf64();
-    if (E <= 8) {
+    for (int h = 0; h < HN; ++h) mx[h] = -kInf64(), sum[h] = 0.0;
+    // (a head behind the last one: x holds anything there, which nothing uses)
+#pragma unroll 2
+    for (int j = tid; j < nc; j += kSelThreads)
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        x[i] = nx[i];
-        if (gq + 1 < a.G && tid + kSelThreads * i < nc)
-          nx[i] = l[select_pitch(a.max_pages) + tid + kSelThreads * i];
+      for (int h = 0; h < HN; ++h) {
+        const double y = x[h * pitch + j];
+        mx[h] = isfinite(y) && y > mx[h] ? y : mx[h];
       }
-    }
-#pragma unroll(E <= 8 ? E : 4)
-    for (int i = 0; i < E; ++i) {
-      const int j = tid + kSelThreads * i;
-      const double y = E <= 8 ? x[i % R] : (j < nc ? l[j] : -kInf64());
-      if (isfinite(y)) mx = fmax(mx, y);
-    }
-    mx = blk.reduce(mx, larger);
-    if (mx == -kInf64()) continue;                 // (a head without a finite logit)
-    double sum = 0.0;
-#pragma unroll(E <= 8 ? E : 4)
-    for (int i = 0; i < E; ++i) {
-      const int j = tid + kSelThreads * i;
-      double y = E <= 8 ? x[i % R] : (j < nc ? l[j] : -kInf64());
-      y = isfinite(y) ? exp(y - mx) : 0.0;
-      if (E <= 8) x[i % R] = y;
-      sum += y;
-    }
-    const double inv = 1.0 / blk.reduce(sum, plus);
+    blk.reduce(mx, larger);                        // (-inf: a head without a finite logit)
+#pragma unroll(4 / HN)
+    for (int j = tid; j < nc; j += kSelThreads)
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const int j = tid + kSelThreads * i;
-      if (E <= 8) {
-        mass[i] += x[i % R] * inv;
+      for (int h = 0; h < HN; ++h) {
+        const double y = x[h * pitch + j], e = exp_down(sm.root, y - mx[h]), z = isfinite(y) ? e : 0.0;
+        x[h * pitch + j] = z;
+        sum[h] += z;
+      }
+    blk.reduce(sum, plus);
+#pragma unroll
+    for (int h = 0; h < HN; ++h) inv[h] = h < nh && sum[h] > 0.0 ? 1.0 / sum[h] : 0.0;
+    const bool last = g0 + HN >= a.G;
+#pragma unroll 2
+    for (int j = tid; j < nc; j += kSelThreads) {
+      double m = g0 ? all[j] : 0.0;
+#pragma unroll
+      for (int h = 0; h < HN; ++h)
+        if (h < nh) m = fma(x[h * pitch + j], inv[h], m);
+      if (last) {
+        x[j] = m;
+        top = m > top ? m : top;
       } else {
-        const double y = j < nc ? l[j] : -kInf64();
-        if (isfinite(y)) mass[i] += exp(y - mx) * inv;
+        all[j] = m;
       }
     }
   }
 
-  double top = -1.0;
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    if (tid + kSelThreads * i >= nc) mass[i] = -1.0;
-    top = fmax(top, mass[i]);
-  }
   const int words = (nc + 31) / 32;
   for (int w = tid; w < words; w += kSelThreads) sm.keep[w] = 0;
   // ---- candidates: a value that `want` of the threads' greatest masses reach
@@ -978,32 +1006,35 @@ __device__ __noinline__ void choose64(const CacheArgs& a, int t, int hk, ExactSm
 #pragma unroll
     for (int i = 1; i < 8; ++i) hi = max(hi, k[i]);
     hi = __reduce_max_sync(0xffffffffu, hi) + 1;
-    int lo = 0;
+    int lo = 0;                                    // count(>= lo) >= want > count(>= hi)
     while (hi - lo > 1) {
-      const int mid = lo + ((hi - lo) >> 1);
+      // three cuts a pass, their counts (256 at most) in one sum
+      const int step = max((hi - lo) >> 2, 1), c1 = lo + step, c2 = c1 + step, c3 = c2 + step;
       int n = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) n += k[i] >= mid;
+      for (int i = 0; i < 8; ++i) n += (k[i] >= c1) + ((k[i] >= c2) << 10) + ((k[i] >= c3) << 20);
       n = __reduce_add_sync(0xffffffffu, n);
-      if (n >= want) lo = mid; else hi = mid;
-      if (n >= want && n <= want + 16) break;
+      const int n1 = n & 1023, n2 = n >> 10 & 1023, n3 = n >> 20;
+      if (n1 < want) {
+        hi = c1;
+        continue;
+      }
+      lo = n3 >= want ? c3 : n2 >= want ? c2 : c1;
+      hi = n3 >= want ? hi : min(hi, lo + step);
+      if ((n3 >= want ? n3 : n2 >= want ? n2 : n1) <= want + 16) break;
     }
     if (lane == 0) sm.cut = lo;
   }
   __syncthreads();
   const int cut = sm.cut;
-#pragma unroll 8
-  for (int i = 0; i < E; ++i) {
-    const bool in = __double2hiint(mass[i]) >= cut;
-    const uint32_t b = __ballot_sync(0xffffffffu, in);
-    if (b) {
-      int at = 0;
-      if (lane == 0) at = atomicAdd(&sm.n_cand, __popc(b));
-      at = __shfl_sync(0xffffffffu, at, 0) + __popc(b & ((1u << lane) - 1));
-      if (in && at < kSelThreads) {
-        sm.cand[at] = mass[i];
-        sm.cand_j[at] = tid + kSelThreads * i;
-      }
+#pragma unroll 1
+  for (int j = tid; j < nc; j += kSelThreads) {
+    const double m = x[j];
+    if (__double2hiint(m) < cut) continue;
+    const int at = atomicAdd(&sm.n_cand, 1);
+    if (at < kSelThreads) {
+      sm.cand[at] = m;
+      sm.cand_j[at] = j;
     }
   }
   __syncthreads();
@@ -1012,25 +1043,32 @@ __device__ __noinline__ void choose64(const CacheArgs& a, int t, int hk, ExactSm
     // a candidate's rank by (-mass, page) settles it (whatever the order in
     // which the candidates came)
     if (tid < n_cand) {
-      const double m = sm.cand[tid];
+      // (as bits, which order as the masses do)
+      const long long m = __double_as_longlong(sm.cand[tid]);
       const int j = sm.cand_j[tid];
       int rank = 0;
-      for (int k = 0; k < n_cand; ++k) rank += sm.cand[k] > m || (sm.cand[k] == m && sm.cand_j[k] < j);
+#pragma unroll 8
+      for (int k = 0; k < n_cand; ++k) {
+        const long long o = __double_as_longlong(sm.cand[k]);
+        const int oj = sm.cand_j[k];
+        rank += (int)(o > m) | ((int)(o == m) & (int)(oj < j));
+      }
       if (rank < want) atomicOr(&sm.keep[j >> 5], 1u << (j & 31));
     }
   } else {
     // too many to rank (more than 256 places, or many equal masses): the
     // want-th greatest mass, by bisection on the bits
-    top = blk.reduce(top, larger);
-    long long lo = 0, hi = __double_as_longlong(top) + 1;   // count(>= lo) > want > count(>= hi)
+    double all_top[1] = {top};
+    blk.reduce(all_top, larger);
+    long long lo = 0, hi = __double_as_longlong(all_top[0]) + 1;   // count(>= lo) > want > count(>= hi)
     int above = 0;                                          // count(>= hi)
     while (hi - lo > 1) {
       // three cuts a pass: a barrier costs more than the comparisons
       const long long step = max((hi - lo) >> 2, 1ll);
       int n[3] = {0, 0, 0};
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const long long b = __double_as_longlong(mass[i]);
+#pragma unroll 1
+      for (int j = tid; j < nc; j += kSelThreads) {
+        const long long b = __double_as_longlong(x[j]);
 #pragma unroll
         for (int k = 0; k < 3; ++k) n[k] += b >= lo + (k + 1) * step;
       }
@@ -1058,13 +1096,8 @@ __device__ __noinline__ void choose64(const CacheArgs& a, int t, int hk, ExactSm
     // kept: every mass >= hi, and of those equal to lo (ties) the first ones
     int ties = want - above;
 #pragma unroll 1
-    for (int i = 0; i < E; ++i) {
-      const int first = kSelThreads * i;
-      if (first >= nc) break;
-      long long b = -1;
-#pragma unroll
-      for (int k = 0; k < E; ++k)
-        if (k == i) b = __double_as_longlong(mass[k]);
+    for (int first = 0; first < nc; first += kSelThreads) {
+      const long long b = first + tid < nc ? __double_as_longlong(x[first + tid]) : -1;
       bool keep = b >= hi;
       if (ties > 0) {                                       // uniform
         const bool eq = b == lo && b < hi;
@@ -1082,7 +1115,7 @@ __device__ __noinline__ void choose64(const CacheArgs& a, int t, int hk, ExactSm
         ties -= min(ties, all);
       }
       const uint32_t bk = __ballot_sync(0xffffffffu, keep);
-      if (lane == 0) sm.keep[i * (kSelThreads / 32) + warp] = bk;
+      if (lane == 0) sm.keep[first / 32 + warp] = bk;
     }
   }
   __syncthreads();
@@ -1125,22 +1158,26 @@ __device__ __forceinline__ bool fixed_pages(const CacheArgs& a, const RowPages& 
   return a.n_select > a.n_first + a.n_recent;
 }
 
-template <int E>
-__global__ void __launch_bounds__(kSelThreads) cache_choose64_kernel(const CacheArgs a) {
+template <int HN>
+__global__ void __launch_bounds__(kSelThreads, 3) cache_choose64_kernel(const CacheArgs a) {
   __shared__ ExactSmem sm;
+  extern __shared__ __align__(16) unsigned char sel_smem[];
   const int t = blockIdx.x, hk = blockIdx.y;
   if (t >= rows_used(a)) return;
   const RowPages r = row_pages(a, t, row_seq(a, t));
-  if (fixed_pages(a, r, (int64_t)t * a.Hkv + hk, threadIdx.x, kSelThreads)) choose64<E>(a, t, hk, sm);
+  if (fixed_pages(a, r, (int64_t)t * a.Hkv + hk, threadIdx.x, kSelThreads))
+    choose64<HN>(a, t, hk, r, sm, reinterpret_cast<double*>(sel_smem), false);
 }
 
-// fp64 logits of one item by the whole block, into the item's scratch rows.
+// fp64 logits of one item by the whole block: into x, or without it into the
+// item's scratch rows.
 template <int D>
-__device__ __noinline__ void logits64_item(const CacheArgs& a, int t, int hk, double* qs) {
+__device__ __forceinline__ void logits64_item(const CacheArgs& a, int t, int hk, int s, const RowPages r, double* qs,
+                                           double* x) {
   constexpr int QP = D + 8;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tg = lane & 3;
-  const int s = row_seq(a, t);
-  const RowPages r = row_pages(a, t, s);
+  const int64_t pitch = select_pitch(a.max_pages);
+  double* out = x ? x - r.c0 : logit_row(a, t, hk * a.G);
   for (int g0 = 0; g0 < a.G; g0 += 8) {
     __syncthreads();
     for (int i = tid; i < 8 * D; i += kSelThreads) {
@@ -1169,7 +1206,7 @@ __device__ __noinline__ void logits64_item(const CacheArgs& a, int t, int hk, do
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           if (g0 + 2 * tg + e < a.G)
-            logit_row(a, t, hk * a.G + g0 + 2 * tg + e)[j + g] = page < 0 ? -kInf64() : ((c0[e] + c1[e]) + (c2[e] + c3[e])) * a.scale;
+            out[(g0 + 2 * tg + e) * pitch + j + g] = page < 0 ? -kInf64() : ((c0[e] + c1[e]) + (c2[e] + c3[e])) * a.scale;
       }
     }
   }
@@ -1368,15 +1405,22 @@ __global__ void __launch_bounds__(kSelThreads, WPI == 1 && E == 16 ? 4 : 1) cach
 }
 
 // The items that the fast choice left, a block each at a time.
-template <int D, int E>
-__global__ void __launch_bounds__(kSelThreads) cache_again_kernel(const CacheArgs a) {
+template <int D, int HN>
+__global__ void __launch_bounds__(kSelThreads, 3) cache_again_kernel(const CacheArgs a) {
   __shared__ __align__(16) double qs[8 * (D + 8)];
   __shared__ ExactSmem sm;
+  extern __shared__ __align__(16) unsigned char sel_smem[];
+  double* x = reinterpret_cast<double*>(sel_smem);
   const int n = *again_count(a);
   for (int i = blockIdx.x; i < n; i += gridDim.x) {
-    const int2 it = again_list(a)[i];
-    logits64_item<D>(a, it.x, it.y, qs);
-    choose64<E>(a, it.x, it.y, sm);
+    const int2 it = again_list(a)[i], info = row_info(a)[it.x];
+    RowPages r;
+    r.n = info.y;
+    r.c0 = min(a.n_first, r.n);
+    r.c1 = max(r.c0, r.n - a.n_recent);
+    const bool fits = a.G <= HN;
+    logits64_item<D>(a, it.x, it.y, info.x, r, qs, fits ? x : nullptr);
+    choose64<HN>(a, it.x, it.y, r, sm, x, fits);
     __syncthreads();
   }
 }
@@ -1406,6 +1450,16 @@ cudaError_t launch_cache_append(const CacheArgs& a, cudaStream_t s) {
   return a.fp8 ? go(cache_append_kernel<64, true>) : go(cache_append_kernel<64, false>);
 }
 
+// A kernel of the fp64 choice (ID: one for each, for its shared-memory limit).
+template <int ID, typename Kernel>
+static cudaError_t run_exact(Kernel k, dim3 grid, int bytes, int dev, const CacheArgs& a, cudaStream_t s) {
+  static OncePerDevice once;
+  const cudaError_t e = once.allow(reinterpret_cast<const void*>(k), dev, kMaxSelectPages * 8);
+  if (e != cudaSuccess) return e;
+  k<<<grid, kSelThreads, bytes, s>>>(a);
+  return cudaGetLastError();
+}
+
 template <int D>
 static cudaError_t select_d(const CacheArgs& a, cudaStream_t s) {
   int dev = 0, sms = 0;
@@ -1429,7 +1483,7 @@ static cudaError_t select_d(const CacheArgs& a, cudaStream_t s) {
     // multiple of what a block's warps take at a time
     const int step = 64, groups = (tile_rows * a.G + 3) / 4;
     int pages = (a.max_pages + step - 1) / step * step;
-    while (pages > 2 * step && tiles * a.Hkv * ((a.max_pages + pages - 1) / pages) < 4ll * sms)
+    while (pages > 2 * step && tiles * a.Hkv * ((a.max_pages + pages - 1) / pages) < 8ll * sms)
       pages = (pages / 2 + step - 1) / step * step;
     const int bytes = groups * 4 * D * 8 + kSelThreads / 32 * 16 * D * 4;
     e = once_d.allow(reinterpret_cast<const void*>(cache_logits64_kernel<D>), dev, 232448);
@@ -1439,28 +1493,31 @@ static cudaError_t select_d(const CacheArgs& a, cudaStream_t s) {
   }
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int64_t items = (int64_t)a.T * a.Hkv;
+  // the fp64 choice: so many heads' logits in shared memory that three blocks
+  // share an SM
+  int heads = kExactHeads;
+  while (heads > 1 && (heads / 2 >= a.G || heads * select_pitch(a.max_pages) * 8 > 65536)) heads /= 2;
+  const int exact = heads * (int)select_pitch(a.max_pages) * 8;
   if (!fast) {
     const dim3 all(a.T, a.Hkv);
-    if (a.max_pages <= 512) cache_choose64_kernel<2><<<all, kSelThreads, 0, s>>>(a);
-    else if (a.max_pages <= 2048) cache_choose64_kernel<8><<<all, kSelThreads, 0, s>>>(a);
-    else cache_choose64_kernel<64><<<all, kSelThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return heads == 4   ? run_exact<4>(cache_choose64_kernel<4>, all, exact, dev, a, s)
+           : heads == 2 ? run_exact<2>(cache_choose64_kernel<2>, all, exact, dev, a, s)
+                        : run_exact<1>(cache_choose64_kernel<1>, all, exact, dev, a, s);
   }
   const int again = (int)(items < 4ll * sms ? items : 4ll * sms);
   if (a.max_pages <= 512) {
     cache_choose_kernel<1, 16><<<(unsigned)((items + 7) / 8), kSelThreads, 0, s>>>(a);
-    cache_again_kernel<D, 2><<<again, kSelThreads, 0, s>>>(a);
   } else if (a.max_pages <= 1024) {
     cache_choose_kernel<1, 32><<<(unsigned)((items + 7) / 8), kSelThreads, 0, s>>>(a);
-    cache_again_kernel<D, 4><<<again, kSelThreads, 0, s>>>(a);
   } else if (a.max_pages <= 8192) {
     cache_choose_kernel<8, 32><<<(unsigned)items, kSelThreads, 0, s>>>(a);
-    cache_again_kernel<D, 32><<<again, kSelThreads, 0, s>>>(a);
   } else {
     cache_choose_kernel<8, 64><<<(unsigned)items, kSelThreads, 0, s>>>(a);
-    cache_again_kernel<D, 64><<<again, kSelThreads, 0, s>>>(a);
   }
-  return cudaGetLastError();
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return heads == 4   ? run_exact<10 * D + 4>(cache_again_kernel<D, 4>, dim3(again), exact, dev, a, s)
+         : heads == 2 ? run_exact<10 * D + 2>(cache_again_kernel<D, 2>, dim3(again), exact, dev, a, s)
+                      : run_exact<10 * D + 1>(cache_again_kernel<D, 1>, dim3(again), exact, dev, a, s);
 }
 
 cudaError_t launch_cache_select(const CacheArgs& a, cudaStream_t s) {

@@ -110,6 +110,11 @@ __device__ __forceinline__ void report_bad_index(int* status) {
     status[ST_BLOCK] = (int)(blockIdx.x + gridDim.x * blockIdx.y);
 }
 
+// 8-byte asynchronous copy global -> shared.
+__device__ __forceinline__ void cp_async8(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
 // Length of sequence s, clamped to what its table row can hold.
 __device__ __forceinline__ int seq_len(const CacheArgs& a, int s) {
   const int n = a.lens[s];

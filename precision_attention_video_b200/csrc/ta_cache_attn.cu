@@ -902,10 +902,10 @@ __global__ void __launch_bounds__(256) cache_lists_kernel(const CacheArgs a) {
 // their keys, so that the last round is full too: their parts meet in the
 // workspace, and the block that arrives last joins them in order.
 //
-// 1332 rows of 32 query heads, 1024 keys each, bf16: 115 us with the lists (107
-// without), FP8 143; 131 without the cut, 145 with one thread a pair.  A tile's
+// 1332 rows of 32 query heads, 1024 keys each, bf16: 115 us with the lists,
+// FP8 143; 131 without the cut, 145 with one thread a pair.  A tile's
 // blocks wait for one another's steps (S, softmax, O) and two blocks an SM
-// cover a part of it: the tensor pipe is busy a third of the time.  Units of 64
+// cover a part of it: the tensor pipe is busy a quarter of the time.  Units of 64
 // keys with a second S, multiplied ahead of the softmax, took 13 us more.
 //
 // A row's greatest weight is exactly 1, so P's rounding spares it (letting the
