@@ -422,8 +422,13 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
 // Power of two that brings a largest magnitude x to [1, 2); 1 where x is zero,
 // or not finite, or tiny: such a column's logits are made NaN, which sends
 // the row to fp64.
+// (unit_size is its reciprocal.)
+__device__ __forceinline__ float unit_size(float x) {
+  return x >= 1e-35f && x < kInf ? __uint_as_float(__float_as_uint(x) & 0x7F800000u) : 1.0f;
+}
 __device__ __forceinline__ float unit_scale(float x) {
-  return x >= 1e-35f && x < kInf ? 1.0f / __uint_as_float(__float_as_uint(x) & 0x7F800000u) : 1.0f;
+  const uint32_t w = 0x7F000000u - __float_as_uint(unit_size(x));
+  return __uint_as_float(w ? w : 0x00400000u);     // (2^-127 is subnormal)
 }
 
 __device__ __forceinline__ double kInf64() { return __longlong_as_double(0x7ff0000000000000ll); }
@@ -601,8 +606,8 @@ __global__ void __launch_bounds__(kSelThreads) cache_split_kernel(const CacheArg
 #pragma unroll
     for (int o = 16; o; o >>= 1) n2 += __shfl_xor_sync(0xffffffffu, n2, o);
     if (lane == 0) {
-      down[row] = tiny(am) ? __int_as_float(0x7fffffff) : 1.0f / up;
-      norm[row] = sqrtf(n2) / up;
+      down[row] = tiny(am) ? __int_as_float(0x7fffffff) : unit_size(am);
+      norm[row] = sqrtf(n2) * unit_size(am);
     }
     const int d = E * lane, half = d / 64, chunk = (d % 64) / 8;
     unsigned char* at = tile + half * T::kHalf + row * 128 + ((chunk ^ (row & 7)) << 4) + (d % 8) * 2;
@@ -724,14 +729,20 @@ __global__ void __launch_bounds__(288, 2) cache_logits_kernel(const CacheArgs a,
       }
       *reinterpret_cast<uint4*>(smem + L::oB + (part / 8) * T::kHalf + c * 128 + (((part % 8) ^ (c & 7)) << 4)) =
           make_uint4(y[0], y[1], y[2], y[3]);
-      if (part == 0) {
-        const int r = c / a.G, row = c < cols ? r * a.H + c - r * a.G : -1;
-        col[c] = make_float2(tiny(am) ? __int_as_float(0x7fffffff) : (float)(a.scale * 1.4426950408889634) / up,
-                             __int_as_float(row));
-        if (row >= 0) qnorm_row(a)[(int64_t)t0 * a.H + hk * a.G + row] = sqrtf(n2);
-      }
+      if (part == 0) col[c] = make_float2(am, n2);
     }
     fence_proxy_async_smem();
+    // what is left of a column is one thread's (in the loop above, unrolled, it
+    // was a fifth of the kernel's time, most of it in fetching instructions)
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    const int c = threadIdx.x;
+    if (c < kSelCols) {
+      const float am = col[c].x, n2 = col[c].y;
+      const int r = c / a.G, row = c < cols ? r * a.H + c - r * a.G : -1;
+      col[c] = make_float2(tiny(am) ? __int_as_float(0x7fffffff) : (float)(a.scale * 1.4426950408889634) * unit_size(am),
+                           __int_as_float(row));
+      if (row >= 0) qnorm_row(a)[(int64_t)t0 * a.H + hk * a.G + row] = sqrtf(n2);
+    }
   }
   tc_fence_before();
   __syncthreads();
