@@ -1476,9 +1476,13 @@ static cudaError_t select_d(const CacheArgs& a, cudaStream_t s) {
   int dev = 0, sms = 0;
   cudaError_t e = device_sms(dev, sms);
   if (e != cudaSuccess) return e;
-  // two rows of a sequence or more on average (and a key head's queries fit a
-  // tile): the fast logits
-  const bool fast = a.cu && a.T >= 2 * (int64_t)a.S && a.G <= kSelCols;
+  // The fast logits (a key head's queries have to fit a tile) take four kernels,
+  // 28 us for a row and for a hundred; fp64 takes two, whose time grows with the
+  // rows: 8 key heads of 4 query heads over 160 pages, 63 rows: 35 us fast and
+  // 24 in fp64, 158 rows: 36 and 45; 4 key heads of 1 over 140 pages, 158 rows:
+  // 29 and 20, 904 rows: 38 and 63.
+  const bool fast = a.cu && a.T >= 2 * (int64_t)a.S && a.G <= kSelCols &&
+                    (int64_t)a.T * a.Hkv * (a.G > 1 ? a.G : 2) >= 20ll * sms;
   const int most = fast ? kSelCols : 8;
   const int tile_rows = !a.cu || a.G >= most ? 1 : most / a.G;
   const int64_t tiles = a.cu ? (int64_t)(a.T / tile_rows) + a.S : a.S;

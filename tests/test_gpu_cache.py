@@ -460,6 +460,70 @@ def test_select_values_that_are_not_finite(cuda_ok):
     np.testing.assert_array_equal(st.select().cpu().numpy(), want)
 
 
+# rows enough for the logits in f16 parts
+SELECT_MANY = [
+    ([600, 64, 0, 10], [90, 200, 1, 300], dict()),
+    ([100, 700], [400, 150], dict(ps=16, n_select=9, n_first=2, n_recent=3, pad=2)),
+    ([2000], [700], dict(ps=16, H=10, Hkv=2, d=64, n_select=40)),
+    ([300, 900], [700, 0], dict(ps=32, H=3, Hkv=3, n_select=3, n_first=0, n_recent=3)),
+    ([900, 40, 0, 2000], [200, 0, 1, 300], dict(ps=32, d=64, H=20, Hkv=1, n_select=8)),
+    ([30000], [200], dict(ps=16, H=16, Hkv=2, n_select=64)),
+]
+
+
+@pytest.mark.parametrize("tie", [False, True])
+@pytest.mark.parametrize("case", range(len(SELECT_MANY)))
+def test_select_many_rows(cuda_ok, case, tie):
+    old, new, kw = SELECT_MANY[case]
+    st = Step(old, new, seed=500 + case, **kw)
+    means_of(st, tie)
+    sel = st.select()
+    assert st.status() == 0
+    want = OC.select(np64(st.Q), np64(st.cache.k_mean), st.lens, st.cu, st.table, st.G, st.ps,
+                     st.p.n_select, st.p.n_first, st.p.n_recent, st.scale)
+    np.testing.assert_array_equal(sel.cpu().numpy(), want)
+
+
+def test_select_many_rows_extreme_magnitudes(cuda_ok):
+    for ek, eq in ((30, -20), (-40, 30), (-140, 0), (100, -90), (0, -135), (60, 60)):
+        st = Step([900], [800], H=4, Hkv=2, n_select=5, ps=32, seed=3)
+        means_of(st)
+        st.cache.k_mean *= 2.0 ** ek if ek > -126 else 2.0 ** (ek + 40) * 2.0 ** -40
+        st.Q *= 2.0 ** eq if eq > -126 else 2.0 ** (eq + 40)
+        if eq <= -126:
+            st.Q *= 2.0 ** -40
+        want = OC.select(np64(st.Q), np64(st.cache.k_mean), st.lens, st.cu, st.table, st.G, st.ps, 5, 1, 1,
+                         st.scale)
+        np.testing.assert_array_equal(st.select().cpu().numpy(), want, err_msg=str((ek, eq)))
+
+
+def test_select_many_rows_values_that_are_not_finite(cuda_ok):
+    st = Step([700], [800], H=4, Hkv=2, n_select=5, seed=1)
+    means_of(st)
+    st.cache.k_mean[st.table[0][3], 0, 5] = float("nan")
+    st.cache.k_mean[st.table[0][4], 1, :] = float("inf")
+    want = OC.select(np64(st.Q), np64(st.cache.k_mean), st.lens, st.cu, st.table, st.G, st.ps, 5, 1, 1,
+                     st.scale)
+    np.testing.assert_array_equal(st.select().cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("rows", [1, 800])
+def test_select_masses_of_every_size(cuda_ok, rows):
+    # logits 18 apart, down to exp(-724), which only a subnormal holds: the
+    # order of the masses is theirs to the last
+    st = Step([640 + 16], [rows], H=4, Hkv=4, d=64, ps=16, n_select=38, seed=2)
+    mean = torch.zeros(st.P, st.Hkv, st.d)
+    order = torch.randperm(40, generator=st.g)
+    for j in range(40):
+        mean[st.table[0][j], :, 0] = -18.1 * float(order[j]) / st.scale
+    st.cache.k_mean.copy_(mean)
+    st.Q.zero_()
+    st.Q[..., 0] = 1.0
+    want = OC.select(np64(st.Q), np64(st.cache.k_mean), st.lens, st.cu, st.table, st.G, st.ps, 38, 1, 1,
+                     st.scale)
+    np.testing.assert_array_equal(st.select().cpu().numpy(), want)
+
+
 # ---------------------------------------------------------------------------
 # sparse attention
 # ---------------------------------------------------------------------------
