@@ -1224,194 +1224,208 @@ __device__ __forceinline__ void logits64_item(const CacheArgs& a, int t, int hk,
   __syncthreads();
 }
 
-// WPI warps choose for one (row, key head), each thread holding E of its
-// pages; a block has 8 / WPI items.
+// Shared memory of the fast choice.
 template <int WPI, int E>
-__global__ void __launch_bounds__(kSelThreads, WPI == 1 && E == 16 ? 4 : 1) cache_choose_kernel(const CacheArgs a) {
-  __shared__ float red[kSelThreads / 32];
-  __shared__ uint32_t bits[WPI > 1 ? WPI * E : 1];
-  __shared__ float few_mass[WPI == 1 ? 8 : 1][64];
-  constexpr int IPB = 8 / WPI, GS = 32 * WPI;
+struct FastSmem {
+  float red[kSelThreads / 32];
+  uint32_t bits[WPI > 1 ? WPI * E : 1];
+  float few_mass[WPI == 1 ? 8 : 1][64];
+};
+
+// WPI warps choose for one (row, key head) of sequence s, each thread holding
+// E of its pages; true where fp64 has to decide.
+template <int WPI, int E, class Smem>
+__device__ __forceinline__ bool fast_choice(const CacheArgs& a, Smem& sm, int t, int hk, int s, const RowPages& r,
+                                            int* sel) {
+  constexpr int GS = 32 * WPI;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int lid = WPI == 1 ? lane : threadIdx.x;           // thread of the item
-  const int64_t item = (int64_t)blockIdx.x * IPB + (WPI == 1 ? warp : 0);
-  const int t = (int)(item / a.Hkv), hk = (int)(item - (int64_t)t * a.Hkv);
-  const Group<WPI> grp{red};
-  bool again = false;                                      // the item needs fp64
-
-  if (t < rows_used(a)) {
-    const int2 info = row_info(a)[t];
-    // (a row that a malformed cu gives to no tile has none: no pages)
-    const bool known = (unsigned)info.x < (unsigned)a.S && (unsigned)info.y <= (unsigned)a.max_pages;
-    const int s = known ? info.x : 0;
-    RowPages r;
-    r.n = known ? info.y : 0;
-    r.c0 = min(a.n_first, r.n);
-    r.c1 = max(r.c0, r.n - a.n_recent);
-    int* sel = a.sel + item * a.n_select;
-    const int nc = r.c1 - r.c0, want = a.n_select - a.n_first - a.n_recent;
-    if (fixed_pages(a, r, item, lid, GS)) {                // 0 < want < nc
-      float mass[E];
+  const Group<WPI> grp{sm.red};
+  const int nc = r.c1 - r.c0, want = a.n_select - a.n_first - a.n_recent;
+  bool again = false;
+  float mass[E];
 #pragma unroll
-      for (int i = 0; i < E; ++i) mass[i] = 0.0f;
-      // thread's pages lid + GS i, i < mine
-      const int mine_n = lid < nc ? (nc - lid + GS - 1) / GS : 0;
-      float kn = 0.0f, qn = 0.0f;
-      const float* nr = norm_row(a, s, hk) + r.c0 + lid;
+  for (int i = 0; i < E; ++i) mass[i] = 0.0f;
+  // thread's pages lid + GS i, i < mine
+  const int mine_n = lid < nc ? (nc - lid + GS - 1) / GS : 0;
+  float kn = 0.0f, qn = 0.0f;
+  const float* nr = norm_row(a, s, hk) + r.c0 + lid;
 #pragma unroll
-      for (int i = 0; i < E; ++i)
-        if (i < mine_n) kn = fmaxf(kn, nr[GS * i]);
-      kn = grp.max(kn);
-      bool bad = false;
-      const int64_t lstep = select_pitch(a.max_pages) * 2;
-      const float* l = reinterpret_cast<const float*>(logit_row(a, t, hk * a.G)) + r.c0 + lid;
-      float nx[E];                                         // the next head's logits
+  for (int i = 0; i < E; ++i)
+    if (i < mine_n) kn = fmaxf(kn, nr[GS * i]);
+  kn = grp.max(kn);
+  bool bad = false;
+  const int64_t lstep = select_pitch(a.max_pages) * 2;
+  const float* l = reinterpret_cast<const float*>(logit_row(a, t, hk * a.G)) + r.c0 + lid;
+  float nx[E];                                         // the next head's logits
+#pragma unroll
+  for (int i = 0; i < E; ++i) nx[i] = i < mine_n ? l[GS * i] : -kInf;
+  for (int gq = 0; gq < a.G; ++gq) {
+    qn = fmaxf(qn, qnorm_row(a)[(int64_t)t * a.H + hk * a.G + gq]);
+    float x[E], mx = -kInf;
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] = nx[i];
+    if (gq + 1 < a.G) {
+      l += lstep;
 #pragma unroll
       for (int i = 0; i < E; ++i) nx[i] = i < mine_n ? l[GS * i] : -kInf;
-      for (int gq = 0; gq < a.G; ++gq) {
-        qn = fmaxf(qn, qnorm_row(a)[(int64_t)t * a.H + hk * a.G + gq]);
-        float x[E], mx = -kInf;
+    }
 #pragma unroll
-        for (int i = 0; i < E; ++i) x[i] = nx[i];
-        if (gq + 1 < a.G) {
-          l += lstep;
+    for (int i = 0; i < E; ++i) mx = fmaxf(mx, x[i]);
+    mx = grp.max(mx);
+    float sum = 0.0f;
 #pragma unroll
-          for (int i = 0; i < E; ++i) nx[i] = i < mine_n ? l[GS * i] : -kInf;
-        }
+    for (int i = 0; i < E; ++i) {
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x[i]) : "f"(x[i] - mx));
+      sum += x[i];
+    }
+    sum = grp.sum(sum);
+    bad |= !(sum >= 0.5f && mx < kInf);                // a logit that is not finite
+    const float inv = 1.0f / sum;
 #pragma unroll
-        for (int i = 0; i < E; ++i) mx = fmaxf(mx, x[i]);
-        mx = grp.max(mx);
-        float sum = 0.0f;
+    for (int i = 0; i < E; ++i) mass[i] = fmaf(x[i], inv, mass[i]);
+  }
+  bad |= !(kn * qn < kInf);                            // (all of these uniform)
+  float top = -1.0f;
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-          asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x[i]) : "f"(x[i] - mx));
-          sum += x[i];
-        }
-        sum = grp.sum(sum);
-        bad |= !(sum >= 0.5f && mx < kInf);                // a logit that is not finite
-        const float inv = 1.0f / sum;
-#pragma unroll
-        for (int i = 0; i < E; ++i) mass[i] = fmaf(x[i], inv, mass[i]);
+  for (int i = 0; i < E; ++i) {
+    if (i >= mine_n) mass[i] = -1.0f;
+    top = fmaxf(top, mass[i]);
+  }
+  // a float that `want` masses reach and the others do not: by bisection
+  // on the bits; count(>= lo) >= want >= count(>= hi)
+  int cut = -1;
+  if (!bad) {
+    int lo = 0, hi;
+    bool few = false;                                  // only few masses lie above lo
+    if (WPI == 1 && want <= 32) {
+      // the want-th greatest of the lanes' greatest: it and everything
+      // above it are `want` masses or more, and hardly more
+      int up = __float_as_int(__uint_as_float(__reduce_max_sync(0xffffffffu, max(__float_as_int(top), 0)))) + 1;
+      hi = up;
+      while (up - lo > 1) {
+        const int mid = lo + ((up - lo) >> 1);
+        const int n = __popc(__ballot_sync(0xffffffffu, __float_as_int(top) >= mid));
+        if (n >= want) lo = mid; else up = mid;
+        if (n == want) break;
       }
-      bad |= !(kn * qn < kInf);                            // (all of these uniform)
-      float top = -1.0f;
+      // its survivors, up to two a lane
+      int n = 0;
 #pragma unroll
       for (int i = 0; i < E; ++i) {
-        if (i >= mine_n) mass[i] = -1.0f;
-        top = fmaxf(top, mass[i]);
+        const uint32_t b = __ballot_sync(0xffffffffu, __float_as_int(mass[i]) >= lo);
+        const int at = n + __popc(b & ((1u << lane) - 1));
+        if (__float_as_int(mass[i]) >= lo && at < 64) sm.few_mass[warp][at] = mass[i];
+        n += __popc(b);
       }
-      // a float that `want` masses reach and the others do not: by bisection
-      // on the bits; count(>= lo) >= want >= count(>= hi)
-      int cut = -1;
-      if (!bad) {
-        int lo = 0, hi;
-        bool few = false;                                  // only few masses lie above lo
-        if (WPI == 1 && want <= 32) {
-          // the want-th greatest of the lanes' greatest: it and everything
-          // above it are `want` masses or more, and hardly more
-          int up = __float_as_int(__uint_as_float(__reduce_max_sync(0xffffffffu, max(__float_as_int(top), 0)))) + 1;
-          hi = up;
-          while (up - lo > 1) {
-            const int mid = lo + ((up - lo) >> 1);
-            const int n = __popc(__ballot_sync(0xffffffffu, __float_as_int(top) >= mid));
-            if (n >= want) lo = mid; else up = mid;
-            if (n == want) break;
-          }
-          // its survivors, up to two a lane
-          int n = 0;
-#pragma unroll
-          for (int i = 0; i < E; ++i) {
-            const uint32_t b = __ballot_sync(0xffffffffu, __float_as_int(mass[i]) >= lo);
-            const int at = n + __popc(b & ((1u << lane) - 1));
-            if (__float_as_int(mass[i]) >= lo && at < 64) few_mass[warp][at] = mass[i];
-            n += __popc(b);
-          }
-          few = n <= 64;
-          if (few) {
-            __syncwarp();
-            const int m0 = lane < n ? __float_as_int(few_mass[warp][lane]) : -1;
-            const int m1 = lane + 32 < n ? __float_as_int(few_mass[warp][lane + 32]) : -1;
-            if (n == want) cut = lo;
-            while (cut < 0 && hi - lo > 1) {
-              const int mid = lo + ((hi - lo) >> 1);
-              const int k = __popc(__ballot_sync(0xffffffffu, m0 >= mid)) + __popc(__ballot_sync(0xffffffffu, m1 >= mid));
-              if (k == want) cut = mid;
-              if (k > want) lo = mid; else hi = mid;
-            }
-          }
-        } else {
-          hi = __float_as_int(grp.max(top)) + 1;
-        }
-        while (!few && hi - lo > 1) {
+      few = n <= 64;
+      if (few) {
+        __syncwarp();
+        const int m0 = lane < n ? __float_as_int(sm.few_mass[warp][lane]) : -1;
+        const int m1 = lane + 32 < n ? __float_as_int(sm.few_mass[warp][lane + 32]) : -1;
+        if (n == want) cut = lo;
+        while (cut < 0 && hi - lo > 1) {
           const int mid = lo + ((hi - lo) >> 1);
-          int n = 0;
-#pragma unroll
-          for (int i = 0; i < E; ++i) n += __float_as_int(mass[i]) >= mid;
-          n = grp.count(n);
-          if (n == want) {
-            cut = mid;
-            break;
-          }
-          if (n > want) lo = mid; else hi = mid;
+          const int k = __popc(__ballot_sync(0xffffffffu, m0 >= mid)) + __popc(__ballot_sync(0xffffffffu, m1 >= mid));
+          if (k == want) cut = mid;
+          if (k > want) lo = mid; else hi = mid;
         }
       }
-      if (cut < 0) {
-        again = true;                                      // equal floats, or values not finite
-      } else {
-        const float c = __int_as_float(cut);
-        float in = kInf, out = 0.0f;
+    } else {
+      hi = __float_as_int(grp.max(top)) + 1;
+    }
+    while (!few && hi - lo > 1) {
+      const int mid = lo + ((hi - lo) >> 1);
+      int n = 0;
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-          if (mass[i] >= c) in = fminf(in, mass[i]); else out = fmaxf(out, mass[i]);
+      for (int i = 0; i < E; ++i) n += __float_as_int(mass[i]) >= mid;
+      n = grp.count(n);
+      if (n == want) {
+        cut = mid;
+        break;
+      }
+      if (n > want) lo = mid; else hi = mid;
+    }
+  }
+  if (cut < 0) {
+    again = true;                                      // equal floats, or values not finite
+  } else {
+    const float c = __int_as_float(cut);
+    float in = kInf, out = 0.0f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      if (mass[i] >= c) in = fminf(in, mass[i]); else out = fmaxf(out, mass[i]);
+    }
+    in = -grp.max(-in);
+    out = grp.max(out);
+    // relative error of a mass: the logits' error in the exponent of the
+    // term and of the sum, ex2 and its argument (near the border up to
+    // ln(1 / mass) below the maximum), and the sums' roundings
+    const float delta = kLogitErr * (float)a.scale * qn * kn;
+    const float err = 2.0f * delta + 1.2e-7f * (float)(E + 26 + a.G) + 4.8e-7f * (8.0f - logf(fmaxf(out, 1e-37f)));
+    again = !(delta < 0.05f) || !(in * (1.0f - 1.1f * err) > out * (1.0f + 1.1f * err));
+    if (!again) {
+      uint32_t mine = 0;                               // WPI = 1: word `lane`
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const uint32_t b = __ballot_sync(0xffffffffu, mass[i] >= c);
+        if constexpr (WPI == 1) {
+          if (lane == i) mine = b;
+        } else {
+          if (lane == 0) sm.bits[i * WPI + warp] = b;
         }
-        in = -grp.max(-in);
-        out = grp.max(out);
-        // relative error of a mass: the logits' error in the exponent of the
-        // term and of the sum, ex2 and its argument (near the border up to
-        // ln(1 / mass) below the maximum), and the sums' roundings
-        const float delta = kLogitErr * (float)a.scale * qn * kn;
-        const float err = 2.0f * delta + 1.2e-7f * (float)(E + 26 + a.G) + 4.8e-7f * (8.0f - logf(fmaxf(out, 1e-37f)));
-        again = !(delta < 0.05f) || !(in * (1.0f - 1.1f * err) > out * (1.0f + 1.1f * err));
-        if (!again) {
-          uint32_t mine = 0;                               // WPI = 1: word `lane`
+      }
+      constexpr int WPL = WPI == 1 ? 1 : (WPI * E + 31) / 32;   // words of a lane
+      if constexpr (WPI > 1) __syncthreads();
+      if (WPI == 1 || warp == 0) {
+        uint32_t w[WPL];
+        int n = 0;
 #pragma unroll
-          for (int i = 0; i < E; ++i) {
-            const uint32_t b = __ballot_sync(0xffffffffu, mass[i] >= c);
-            if constexpr (WPI == 1) {
-              if (lane == i) mine = b;
-            } else {
-              if (lane == 0) bits[i * WPI + warp] = b;
-            }
-          }
-          constexpr int WPL = WPI == 1 ? 1 : (WPI * E + 31) / 32;   // words of a lane
-          if constexpr (WPI > 1) __syncthreads();
-          if (WPI == 1 || warp == 0) {
-            uint32_t w[WPL];
-            int n = 0;
-#pragma unroll
-            for (int k = 0; k < WPL; ++k) {
-              w[k] = WPI == 1 ? mine : (lane * WPL + k < WPI * E ? bits[lane * WPL + k] : 0u);
-              n += __popc(w[k]);
-            }
-            int inc = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-              const int y = __shfl_up_sync(0xffffffffu, inc, o);
-              if (lane >= o) inc += y;
-            }
-            int at = a.n_first + inc - n;
-#pragma unroll
-            for (int k = 0; k < WPL; ++k)
-              while (w[k]) {
-                const int b = __ffs(w[k]) - 1;
-                w[k] &= w[k] - 1;
-                sel[at++] = r.c0 + (lane * WPL + k) * 32 + b;
-              }
-          }
+        for (int k = 0; k < WPL; ++k) {
+          w[k] = WPI == 1 ? mine : (lane * WPL + k < WPI * E ? sm.bits[lane * WPL + k] : 0u);
+          n += __popc(w[k]);
         }
+        int inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += y;
+        }
+        int at = a.n_first + inc - n;
+#pragma unroll
+        for (int k = 0; k < WPL; ++k)
+          while (w[k]) {
+            const int b = __ffs(w[k]) - 1;
+            w[k] &= w[k] - 1;
+            sel[at++] = r.c0 + (lane * WPL + k) * 32 + b;
+          }
       }
     }
   }
+  return again;
+}
+
+// A block has 8 / WPI items.  Rows with half the pages or fewer take half the
+// registers' steps.
+template <int WPI, int E>
+__global__ void __launch_bounds__(kSelThreads, E == 16 ? 4 : E == 32 ? 2 : 1) cache_choose_kernel(const CacheArgs a) {
+  __shared__ FastSmem<WPI, E> sm;
+  constexpr int IPB = 8 / WPI, GS = 32 * WPI;
+  const int warp = threadIdx.x >> 5, lid = WPI == 1 ? threadIdx.x & 31 : threadIdx.x;
+  const int64_t item = (int64_t)blockIdx.x * IPB + (WPI == 1 ? warp : 0);
+  const int t = (int)(item / a.Hkv), hk = (int)(item - (int64_t)t * a.Hkv);
+  if (t >= rows_used(a)) return;
+  const int2 info = row_info(a)[t];
+  // (a row that a malformed cu gives to no tile has none: no pages)
+  const bool known = (unsigned)info.x < (unsigned)a.S && (unsigned)info.y <= (unsigned)a.max_pages;
+  RowPages r;
+  r.n = known ? info.y : 0;
+  r.c0 = min(a.n_first, r.n);
+  r.c1 = max(r.c0, r.n - a.n_recent);
+  if (!fixed_pages(a, r, item, lid, GS)) return;           // 0 < want < nc
+  int* sel = a.sel + item * a.n_select;
+  const bool again = r.c1 - r.c0 <= GS * E / 2 ? fast_choice<WPI, E / 2>(a, sm, t, hk, info.x, r, sel)
+                                               : fast_choice<WPI, E>(a, sm, t, hk, info.x, r, sel);
   if (again && lid == 0) again_list(a)[atomicAdd(again_count(a), 1)] = make_int2(t, hk);
 }
 
