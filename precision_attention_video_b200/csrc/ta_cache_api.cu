@@ -162,6 +162,10 @@ EncodeTiledFn encode_fn() {
 
 // Codes [n_pages, Hkv, page_size, d]: a box is one page of one head, 128 bytes
 // of each row at most (64 for FP8 with d = 64), swizzled by the row's width.
+// L2 fetches no more than a row at a time: behind it, in token-major pages,
+// stands another head's, which comes too early for the block that wants it
+// (551 MB of 128-byte rows: 106 us, with 256 bytes at a time 132; whole rows of
+// 256 bytes gain by it, 107 us against 113 for 673 MB).
 bool make_cache_map(CUtensorMap* m, const ta_cache_params* p, void* base) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
@@ -178,7 +182,8 @@ bool make_cache_map(CUtensorMap* m, const ta_cache_params* p, void* base) {
   return fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims,
             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            p->d * esz < 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 ta_status attend(const ta_cache_params* p, const ta_cache* cache, const void* Q, const int32_t* sel,
