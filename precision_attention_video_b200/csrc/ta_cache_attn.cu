@@ -1331,9 +1331,20 @@ cudaError_t run(const CacheArgs& a, const CUtensorMap& mk, const CUtensorMap& mv
 template <int D, bool FP8>
 cudaError_t pick(const CacheArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, bool sparse,
                  cudaStream_t s) {
-  // groups of more than 8 query heads take two column tiles, so that each key
-  // is read once for up to 16 of them
-  if (a.G <= 8)
+  // Groups of more than 8 query heads take two column tiles where the cache's
+  // bytes bound, so that each key is read once for up to 16 of them; with fewer
+  // units than that a second tile only lengthens an item's chain.  16 heads a
+  // key head: 12 units 13.7 us with two tiles and 9.5 with one, 1000 units 34
+  // and 26, 4000 units 50 and 53, 16000 units 123 and 211; FP8 2000 units 49
+  // and 42, 4000 units 66 and 62, 8000 units 118 and 125.
+  int dev = 0, sms = 0;
+  const cudaError_t e = device_sms(dev, sms);
+  if (e != cudaSuccess) return e;
+  constexpr int kUnit = Cfg<D, FP8, 1>::kUnit;
+  static_assert(kUnit == Cfg<D, FP8, 2>::kUnit, "units are counted alike");
+  const int64_t pages = !sparse ? a.max_pages : a.n_select < a.max_pages ? a.n_select : a.max_pages;
+  const int64_t units = (sparse ? a.T : a.S) * (int64_t)a.Hkv * ((pages * a.page_size + kUnit - 1) / kUnit);
+  if (a.G <= 8 || units <= (FP8 ? 32 : 16) * sms)
     return sparse ? run<D, FP8, 1, true>(a, mk, mv, s) : run<D, FP8, 1, false>(a, mk, mv, s);
   return sparse ? run<D, FP8, 2, true>(a, mk, mv, s) : run<D, FP8, 2, false>(a, mk, mv, s);
 }

@@ -335,6 +335,38 @@ def test_decode(cuda_ok, case, fp8):
     assert torch.equal(big[:, 1], O) and (big[:, 0] == 5).all()
 
 
+# groups of more than 8 query heads where the cache may be long (its table is)
+WIDE = [
+    ([400, 90, 700], dict(H=16, Hkv=1, ps=128)),
+    ([1000, 17, 3], dict(H=40, Hkv=2, ps=128)),
+    ([700, 65, 0, 300], dict(H=24, Hkv=1, d=64, ps=128)),
+]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("case", range(len(WIDE)))
+def test_decode_wide_groups(cuda_ok, case, fp8):
+    lens, kw = WIDE[case]
+    st = Step(lens, [0] * len(lens), fp8=fp8, seed=150 + case, cu=False, spare=5000, **kw)
+    O, lse = st.decode()
+    assert st.status() == 0
+    st.check(O, lse)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("case", range(len(WIDE)))
+def test_sparse_wide_groups(cuda_ok, case, fp8):
+    lens, kw = WIDE[case]
+    lens = [n + 37 * i for i in range(4) for n in lens]
+    st = Step(lens, [1] * len(lens), fp8=fp8, seed=160 + case, spare=1000, n_select=1000, **kw)
+    st.append()
+    lists = torch.full((st.T, st.Hkv, 1000), -1, dtype=torch.int32)
+    lists[..., 3:12] = torch.randint(-1, 10, (st.T, st.Hkv, 9), generator=st.g, dtype=torch.int32)
+    O, lse = st.sparse(lists.to(DEV))
+    assert st.status() == 0
+    st.check(O, lse, lists.tolist())
+
+
 def test_decode_long_and_split_over_the_gpu(cuda_ok):
     st = Step([20000, 3, 7777], [0] * 3, H=4, Hkv=1, seed=9, cu=False)
     a, la = st.decode()
