@@ -73,7 +73,10 @@ inline int tile_rows(int G, int64_t T, int64_t S, int max_pages) {
   return 128 / G < 32 ? 128 / G : 32;
 }
 constexpr int kMaxTileParts = 512;                // parts of cut tiles: 256 threads' 64 + 2 numbers each
-constexpr size_t kTilePartBytes = (size_t)kMaxTileParts * 256 * 66 * 4;
+// (a tile is cut into 8 parts at most)
+inline size_t tile_part_bytes(int64_t items) {
+  return (size_t)(items * 8 < kMaxTileParts ? items * 8 : kMaxTileParts) * (256 * 66 * 4);
+}
 inline int64_t tile_count(int rows, int64_t T, int64_t S) { return T / rows + S; }
 
 // Doubles of a row of the choice's scratch: whole tiles of 128 pages.

@@ -48,7 +48,7 @@ size_t sparse_bytes(const ta_cache_params* p) {
   const int rows = ta::tile_rows(p->H / p->Hkv, p->T, p->S, p->max_pages);
   if (!rows) return 0;
   const size_t items = (size_t)ta::tile_count(rows, p->T, p->S) * p->Hkv;
-  return ta::kTilePartBytes + items * ((size_t)rows * p->n_select * 8 + 4) +
+  return ta::tile_part_bytes(items) + items * ((size_t)rows * p->n_select * 8 + 4) +
          ((size_t)p->T + 1 + ta::kMaxTileParts) * 4;
 }
 size_t scratch_bytes(const ta_cache_params* p) {

@@ -1396,7 +1396,7 @@ cudaError_t launch_cache_attn(const CacheArgs& args, const CUtensorMap& mk, cons
       a.tile_rows = rows;
       a.list_cap = rows * a.n_select;
       a.tile_parts = reinterpret_cast<float*>(a.scratch);
-      a.lists = reinterpret_cast<int2*>(reinterpret_cast<char*>(a.scratch) + kTilePartBytes);
+      a.lists = reinterpret_cast<int2*>(reinterpret_cast<char*>(a.scratch) + tile_part_bytes(tiles * a.Hkv));
       a.list_n = reinterpret_cast<int*>(a.lists + tiles * a.Hkv * a.list_cap);
       a.tile_arrived = a.list_n + tiles * a.Hkv;
       a.row_flags = a.tile_arrived + kMaxTileParts;
