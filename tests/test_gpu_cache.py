@@ -789,6 +789,64 @@ def test_captured_steps_share_a_workspace(cuda_ok):
     assert st.status() == 0
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_prompt_captured_and_replayed_between_other_calls(cuda_ok, fp8):
+    # the fast choice and cut tiles in a graph, other calls of other sizes on
+    # the same workspace between its replays: the same bits every time
+    st = Step([900, 300], [500, 330], H=16, Hkv=4, fp8=fp8, n_select=6, seed=45)
+    st.append()
+    O, lse = st.out()
+    sel = torch.zeros((st.T, st.Hkv, 6), dtype=torch.int32, device=DEV)
+    m = pav()
+    p1 = m.make_cache_params(n_pages=st.P, page_size=st.ps, H=16, Hkv=4, d=128, S=2, T=2, max_pages=st.W,
+                             format=int(fp8), n_select=6, n_recent=1)
+    O1 = torch.empty(2, 16, 128, dtype=BF, device=DEV)
+    sel1 = torch.zeros((2, 4, 6), dtype=torch.int32, device=DEV)
+
+    def prompt():
+        m.cache_select(st.p, st.cache, st.Q, st.t_table, st.t_lens, st.ws, sel, cu=st.t_cu)
+        m.cache_sparse(st.p, st.cache, st.Q, sel, st.t_table, st.t_lens, st.ws, O, cu=st.t_cu, lse=lse)
+
+    def token():
+        m.cache_decode(p1, st.cache, st.Q[:2], st.t_table, st.t_lens, st.ws, O1)
+        m.cache_select(p1, st.cache, st.Q[:2], st.t_table, st.t_lens, st.ws, sel1)
+        m.cache_sparse(p1, st.cache, st.Q[:2], sel1, st.t_table, st.t_lens, st.ws, O1)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        prompt()
+        s.synchronize()
+        first = [x.clone() for x in (O, lse, sel)]
+        check_some(st, O, lse, sel.tolist(), every=23)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            prompt()
+        for _ in range(3):
+            token()
+            O.fill_(7), lse.fill_(7), sel.fill_(0)
+            g.replay()
+            s.synchronize()
+            assert all(torch.equal(x, y) for x, y in zip(first, (O, lse, sel)))
+    assert st.status() == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_prompt_with_a_page_outside_the_cache(cuda_ok, fp8):
+    # reported, and its keys are nobody's
+    st = Step([0, 100], [700, 300], H=16, Hkv=4, fp8=fp8, n_select=5, seed=46)
+    st.append()
+    st.t_table[0, 3] = st.P
+    st.t_table[1, 1] = -7
+    lists = torch.randint(-1, 11, (st.T, 4, 5), generator=st.g, dtype=torch.int32)
+    O, lse = st.sparse(lists.to(DEV))
+    torch.cuda.synchronize()
+    assert st.status() == pav().TA_ERR_BAD_INDEX
+    lists[:700][lists[:700] == 3] = -1
+    lists[700:][lists[700:] == 1] = -1
+    check_some(st, O, lse, lists.tolist(), every=13)
+
+
 def test_another_stream_and_two_workspaces_at_once(cuda_ok):
     a = Step([4000], [0], H=8, Hkv=1, seed=41, cu=False)
     b = Step([3000], [0], H=8, Hkv=1, seed=42, cu=False)
