@@ -1363,7 +1363,11 @@ __device__ __forceinline__ bool fast_choice(const CacheArgs& a, Smem& sm, int t,
     // ln(1 / mass) below the maximum), and the sums' roundings
     const float delta = kLogitErr * (float)a.scale * qn * kn;
     const float err = 2.0f * delta + 1.2e-7f * (float)(E + 26 + a.G) + 4.8e-7f * (8.0f - logf(fmaxf(out, 1e-37f)));
-    again = !(delta < 0.05f) || !(in * (1.0f - 1.1f * err) > out * (1.0f + 1.1f * err));
+    // and what a mass may lack outright: a head's term below 2^-126 counts as
+    // 0 (a head's sum is 1 at least, so its share of the mass is no larger), and
+    // sums down there round by 2^-150
+    const float lost = 2.36e-38f * (float)a.G;             // 2^-125 a head
+    again = !(delta < 0.05f) || !(in * (1.0f - 1.1f * err) > out * (1.0f + 1.1f * err) + lost);
     if (!again) {
       uint32_t mine = 0;                               // WPI = 1: word `lane`
 #pragma unroll

@@ -1,0 +1,56 @@
+"""Cached attention where its numbers leave the ordinary range: page choices
+whose border masses no float holds."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache as OC
+from test_gpu_cache import BF, Step, np64
+
+pytestmark = pytest.mark.gpu
+
+
+def same_choice(st):
+    """The lists of `st` are fp64's."""
+    want = OC.select(np64(st.Q), np64(st.cache.k_mean), st.lens, st.cu, st.table, st.G, st.ps,
+                     st.p.n_select, st.p.n_first, st.p.n_recent, st.scale)
+    np.testing.assert_array_equal(st.select().cpu().numpy(), want)
+    assert st.status() == 0
+
+
+def set_logits(st, logits):
+    """Page j's logit for query head g of each key head is logits[j][g] (nats),
+    for a query of ones: head g reads element g alone."""
+    mean = torch.zeros(st.P, st.Hkv, st.d, dtype=torch.float64)
+    for j, row in enumerate(logits):
+        mean[st.table[0][j], :, :st.G] = torch.as_tensor(row, dtype=torch.float64) / st.scale
+    st.cache.k_mean.copy_(mean)
+    st.Q.zero_()
+    for h in range(st.H):
+        st.Q[:, h, h % st.G] = 1.0
+
+
+# ---- masses at the border that a float holds as 0, or in few bits ----
+@pytest.mark.parametrize("d", [64, 128])
+def test_select_masses_that_no_float_holds(cuda_ok, d):
+    # in log2: page 3's two terms lie below the smallest normal float and their
+    # sum above page 2's one term, which does not
+    st = Step([(4 + 12) * 16], [800], H=4, Hkv=2, d=d, ps=16, n_select=5, n_first=1, n_recent=1)
+    rows = [(-300.0, -300.0)] * (st.W + 1)
+    rows[1:5] = (0.0, 0.0), (-100.0, -100.0), (-125.8, -400.0), (-126.2, -126.2)
+    set_logits(st, np.array(rows[:st.W]) * np.log(2.0))
+    same_choice(st)
+
+
+@pytest.mark.parametrize("pages", [60, 900, 3000])
+@pytest.mark.parametrize("G", [2, 8])
+def test_select_borders_far_below_the_greatest_page(cuda_ok, G, pages):
+    # one page far above all others, whose heads' logits differ by nats around
+    # where a float's terms vanish, and rows whose queries differ in length
+    st = Step([pages * 16], [300], H=8 * G, Hkv=8, d=64, ps=16, n_select=12, seed=pages + G)
+    logits = -75.0 - 20.0 * torch.rand(st.W, G, generator=st.g, dtype=torch.float64)
+    logits[7] = 0.0
+    set_logits(st, logits)
+    st.Q *= (1.0 + torch.randint(-16, 17, (st.T, 1, 1), generator=st.g) / 128.0).to(BF).to(st.Q.device)
+    same_choice(st)
