@@ -710,23 +710,21 @@ __global__ void __launch_bounds__(288, 2) cache_logits_kernel(const CacheArgs a,
       const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
       float am = 0.0f, n2 = 0.0f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float x = bf_lo(u[k]), y = bf_hi(u[k]);
-        am = fmax3(am, fabsf(x), fabsf(y));
-        n2 += x * x + y * y;
-      }
+      for (int k = 0; k < 4; ++k) am = fmax3(am, fabsf(bf_lo(u[k])), fabsf(bf_hi(u[k])));
 #pragma unroll
-      for (int o = 1; o < LPC; o <<= 1) {
-        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-        n2 += __shfl_xor_sync(0xffffffffu, n2, o);
-      }
+      for (int o = 1; o < LPC; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
       const float up = unit_scale(am);
       uint32_t y[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const __half2 z = __floats2half2_rn(bf_lo(u[k]) * up, bf_hi(u[k]) * up);
+        // (the norm of the scaled elements: a tiny query's own squares underflow)
+        const float lo = bf_lo(u[k]) * up, hi = bf_hi(u[k]) * up;
+        n2 += lo * lo + hi * hi;
+        const __half2 z = __floats2half2_rn(lo, hi);
         y[k] = *reinterpret_cast<const uint32_t*>(&z);
       }
+#pragma unroll
+      for (int o = 1; o < LPC; o <<= 1) n2 += __shfl_xor_sync(0xffffffffu, n2, o);
       *reinterpret_cast<uint4*>(smem + L::oB + (part / 8) * T::kHalf + c * 128 + (((part % 8) ^ (c & 7)) << 4)) =
           make_uint4(y[0], y[1], y[2], y[3]);
       if (part == 0) col[c] = make_float2(am, n2);
@@ -741,7 +739,7 @@ __global__ void __launch_bounds__(288, 2) cache_logits_kernel(const CacheArgs a,
       const int r = c / a.G, row = c < cols ? r * a.H + c - r * a.G : -1;
       col[c] = make_float2(tiny(am) ? __int_as_float(0x7fffffff) : (float)(a.scale * 1.4426950408889634) * unit_size(am),
                            __int_as_float(row));
-      if (row >= 0) qnorm_row(a)[(int64_t)t0 * a.H + hk * a.G + row] = sqrtf(n2);
+      if (row >= 0) qnorm_row(a)[(int64_t)t0 * a.H + hk * a.G + row] = sqrtf(n2) * unit_size(am);
     }
   }
   tc_fence_before();

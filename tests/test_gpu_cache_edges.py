@@ -1,5 +1,5 @@
 """Cached attention where its numbers leave the ordinary range: page choices
-whose border masses no float holds."""
+whose border masses no float holds, queries whose squares underflow."""
 
 import numpy as np
 import pytest
@@ -53,4 +53,19 @@ def test_select_borders_far_below_the_greatest_page(cuda_ok, G, pages):
     logits[7] = 0.0
     set_logits(st, logits)
     st.Q *= (1.0 + torch.randint(-16, 17, (st.T, 1, 1), generator=st.g) / 128.0).to(BF).to(st.Q.device)
+    same_choice(st)
+
+
+# ---- queries whose squares underflow ----
+@pytest.mark.parametrize("ek,eq", [(90, -90), (100, -100)])
+@pytest.mark.parametrize("near", [1e-6, 1e-5])
+def test_select_near_ties_of_tiny_queries(cuda_ok, near, ek, eq):
+    # logits of hundreds as the product of tiny queries and huge means, with
+    # pages that differ by no more than the fast sums' error
+    st = Step([3000], [800], H=8, Hkv=4, ps=16, n_select=12, seed=19)
+    base = torch.randn(3, 1, st.Hkv, st.d, generator=st.g)
+    mean = base[torch.randint(0, 3, (st.P,), generator=st.g), 0]
+    mean = mean + near * torch.randn(st.P, st.Hkv, st.d, generator=st.g)
+    st.cache.k_mean.copy_(8 * mean * 2.0 ** ek)
+    st.Q *= 8 * 2.0 ** eq
     same_choice(st)
