@@ -979,7 +979,8 @@ __global__ void __launch_bounds__(320, 2)
   int4* info = reinterpret_cast<int4*>(smem + L::oInfo);   // first position, rows' bits, keys that exist
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::oBar);
   uint64_t *full_k = bars, *full_v = bars + 1, *s_ready = bars + 2, *p_ready = bars + 3, *o_done = bars + 4,
-           *k_ready = FP8 ? bars + 5 : full_k;             // K in bf16
+           *k_ready = FP8 ? bars + 5 : full_k,             // K in bf16
+           *seen = bars + 5;                               // bf16: the softmax warps know that K is there
   uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 6);
   int* flag = reinterpret_cast<int*>(bars + 7);            // [0]: a wait gave up, [1]: the last part
   float* scales = reinterpret_cast<float*>(smem + L::oScale);
@@ -990,7 +991,7 @@ __global__ void __launch_bounds__(320, 2)
     mbar_init(s_ready, 1);
     mbar_init(p_ready, 256);
     mbar_init(o_done, 1);
-    if (FP8) mbar_init(k_ready, 256);
+    mbar_init(bars + 5, FP8 ? 256 : 8);
     *flag = 0;
     fence_mbar_init();
   }
@@ -1034,7 +1035,9 @@ __global__ void __launch_bounds__(320, 2)
         if (page < 0) vc = 0;
       }
       const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, vc > 0)) * a.page_size * (FP8 ? D + 4 : 2 * D);
-      if (i > 0) ok = mbar_wait(s_ready, (i - 1) & 1, abort, 1);       // K is free
+      // K is free; and (FP8: as S tells) no softmax warp still waits for full_k's
+      // last phase, which a next one, done early, would hide from it
+      if (i > 0) ok = mbar_wait(s_ready, (i - 1) & 1, abort, 1) && (FP8 || mbar_wait(seen, (i - 1) & 1, abort, 10));
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
       if (lane < ppu) info[(i & 1) * 8 + lane] = make_int4(e.x << a.ps_log2, e.y, vc, 0);
       __syncwarp();
@@ -1116,6 +1119,9 @@ __global__ void __launch_bounds__(320, 2)
       if constexpr (FP8) {
         widen<D>(smem + L::oK, pair, half, scales[pair], true);
         mbar_arrive(k_ready);
+      } else {
+        __syncwarp();                                      // (every lane has waited)
+        if (lane == 0) mbar_arrive(seen);
       }
       ok = ok && mbar_wait(s_ready, i & 1, abort, 7);
       tc_fence_after();
