@@ -672,11 +672,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT>::kThreads, 1)
       ++issued;
       if (i + 1 < n_units) cur.next(a, pre, HX);
     }
-    if (*abort.abort) {
-      // nothing may still be writing shared memory when the CTA ends
-      for (int i = max(0, issued - C::kStages); i < issued; ++i)
-        mbar_wait_drain(&full[i % C::kStages], (i / C::kStages) & 1);
-    }
+    // nothing may still be writing shared memory when the CTA ends, whoever's
+    // wait ran out (the flag may rise after this warp has looked)
+    for (int i = max(0, issued - C::kStages); i < issued; ++i)
+      mbar_wait_drain(&full[i % C::kStages], (i / C::kStages) & 1);
     return;
   }
 
@@ -1025,8 +1024,8 @@ __global__ void __launch_bounds__(320, 2)
     // ---- loads: lane i brings page i of the unit ----
     const int2* list = a.lists + item * a.list_cap;
     bool ok = true;
-    int i = 0;
-    for (; i < units && ok; ++i) {
+    int nk = 0, nv = 0;                // phases that full_k and full_v were given
+    for (int i = 0; i < units; ++i) {
       const int at = (unit0 + i) * ppu + lane;
       const int2 e = lane < ppu && at < n ? list[at] : make_int2(0, 0);
       int vc = e.y ? min(a.page_size, max(0, len - (e.x << a.ps_log2))) : 0, page = 0;
@@ -1038,10 +1037,11 @@ __global__ void __launch_bounds__(320, 2)
       // K is free; and (FP8: as S tells) no softmax warp still waits for full_k's
       // last phase, which a next one, done early, would hide from it
       if (i > 0) ok = mbar_wait(s_ready, (i - 1) & 1, abort, 1) && (FP8 || mbar_wait(seen, (i - 1) & 1, abort, 10));
-      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      if (!__all_sync(0xffffffffu, ok)) break;
       if (lane < ppu) info[(i & 1) * 8 + lane] = make_int4(e.x << a.ps_log2, e.y, vc, 0);
       __syncwarp();
       if (lane == 0) mbar_arrive_expect_tx(full_k, bytes);
+      ++nk;
       __syncwarp();
       const int off = lane << a.ps_log2;
       if (vc > 0) {
@@ -1055,8 +1055,9 @@ __global__ void __launch_bounds__(320, 2)
         }
       }
       if (i > 0) ok = mbar_wait(o_done, (i - 1) & 1, abort, 2);        // V is free
-      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      if (!__all_sync(0xffffffffu, ok)) break;
       if (lane == 0) mbar_arrive_expect_tx(full_v, bytes);
+      ++nv;
       __syncwarp();
       if (vc > 0) {
         if constexpr (FP8) {
@@ -1069,15 +1070,16 @@ __global__ void __launch_bounds__(320, 2)
         }
       }
     }
-    if (!ok) {                         // nothing may still be writing shared memory
-      mbar_wait_drain(full_k, i & 1);
-      if (i > 0) mbar_wait_drain(full_v, (i - 1) & 1);
-    }
+    // nothing may still be writing shared memory when the block ends, whatever
+    // wait of whichever role ran out
+    if (nk) mbar_wait_drain(full_k, (nk - 1) & 1);
+    if (nv) mbar_wait_drain(full_v, (nv - 1) & 1);
   } else if (warp == 9) {
     // ---- products ----
     if (lane == 0) {
       const uint32_t sq = smem_u32(smem + L::oQ), sk = smem_u32(smem + L::oK), sv = smem_u32(smem + L::oV);
       constexpr uint32_t idesc_s = idesc_bf16(128, 128, false), idesc_o = idesc_bf16(128, D, true);
+      int ns = 0, no = 0;              // products committed to s_ready and o_done
       for (int i = 0; i < units; ++i) {
         // (S's columns are free: they held P of the unit before, whose product
         // is ahead in the pipe)
@@ -1088,17 +1090,19 @@ __global__ void __launch_bounds__(320, 2)
           mma_f16_ss(tS, smem_desc_sw128(sq + (kk >> 2) * L::kRows + (kk & 3) * 32, 16, 1024),
                      smem_desc_sw128(sk + (kk >> 2) * L::kRows + (kk & 3) * 32, 16, 1024), idesc_s, kk > 0 ? 1u : 0u);
         tc_commit(s_ready);
-        if (!mbar_wait(p_ready, i & 1, abort, 4) || !mbar_wait(full_v, i & 1, abort, 5)) {
-          mbar_wait_drain(s_ready, i & 1);
-          break;
-        }
+        ++ns;
+        if (!mbar_wait(p_ready, i & 1, abort, 4) || !mbar_wait(full_v, i & 1, abort, 5)) break;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
           mma_f16_ts(tO, tS + kk * 8, smem_desc_sw128(sv + kk * 16 * 128, L::kRows, 1024), idesc_o,
                      (i > 0 || kk > 0) ? 1u : 0u);
         tc_commit(o_done);
+        ++no;
       }
+      // nor may a product read that memory, or write the columns given back
+      if (ns) mbar_wait_drain(s_ready, (ns - 1) & 1);
+      if (no) mbar_wait_drain(o_done, (no - 1) & 1);
     }
   } else {
     // ---- softmax: two threads have a pair, 64 keys of a unit each ----
@@ -1118,7 +1122,7 @@ __global__ void __launch_bounds__(320, 2)
       ok = ok && mbar_wait(full_k, i & 1, abort, 6);
       if constexpr (FP8) {
         widen<D>(smem + L::oK, pair, half, scales[pair], true);
-        mbar_arrive(k_ready);
+        if (ok) mbar_arrive(k_ready);                      // (else no product may start on it)
       } else {
         __syncwarp();                                      // (every lane has waited)
         if (lane == 0) mbar_arrive(seen);
