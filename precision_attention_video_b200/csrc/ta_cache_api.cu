@@ -33,10 +33,16 @@ ta_status validate(const ta_cache_params* p) {
   return TA_OK;
 }
 
-// The choice's scratch: logits; split means, their norms and scales; the
+// Sizes that the choice takes: a row's masses, and the queries of a key head,
+// stand in shared memory; sequences and (row, key head) items are grid dimensions.
+bool select_fits(const ta_cache_params* p) {
+  return p->max_pages <= ta::kMaxSelectPages && p->H / p->Hkv <= 128 && p->S <= 65535 &&
+         (int64_t)p->T * p->Hkv <= 0x7fffffff;
+}
+// The choice's scratch (none where it refuses the sizes): logits; split means, their norms and scales; the
 // queries' norms; the rows; the list of items to do again.
 size_t select_bytes(const ta_cache_params* p) {
-  if (p->n_select <= 0) return 0;
+  if (p->n_select <= 0 || !select_fits(p)) return 0;
   const size_t pitch = (size_t)ta::select_pitch(p->max_pages), T = (size_t)p->T + (p->T & 1);
   return pitch * ((size_t)p->T * p->H * 8 + (size_t)p->S * p->Hkv * (4 * p->d + 8)) + T * p->H * 4 + (T + 2) * 8 +
          (size_t)p->T * p->Hkv * 8;
@@ -274,11 +280,7 @@ ta_status tiered_attn_cache_select(const ta_cache_params* p, const ta_cache* cac
   ta_status st = validate(p);
   if (st != TA_OK) return st;
   if (p->n_select < 1) return TA_ERR_INVALID_ARG;
-  // a row's masses, and the queries of a key head, stand in shared memory;
-  // sequences and (row, key head) items are grid dimensions
-  if (p->max_pages > ta::kMaxSelectPages || p->H / p->Hkv > 128 || p->S > 65535 ||
-      (int64_t)p->T * p->Hkv > 0x7fffffff)
-    return TA_ERR_UNSUPPORTED;
+  if (!select_fits(p)) return TA_ERR_UNSUPPORTED;
   if ((st = check_cache(p, cache, false, true)) != TA_OK) return st;
   if ((st = check_index(p, cu, lens, table)) != TA_OK) return st;
   if (!rows_ok(Q, p->stride_q_t, p->stride_q_h) || !aligned(sel, 4)) return TA_ERR_INVALID_ARG;
