@@ -155,8 +155,11 @@ ta_status tiered_attn_cache_decode(const ta_cache_params* p, const ta_cache* cac
  * sel_dev: int32 [T, Hkv, n_select], a row's page indices (in its sequence)
  * in ascending order, then -1.  Only k_mean of the cache is read.  At most
  * 16384 pages of a sequence, 128 query heads of a key head, 65535 sequences and
- * 2^31 - 1 (row, key head) pairs (else TA_ERR_UNSUPPORTED).  Two to four
- * launches. */
+ * 2^31 - 1 (row, key head) pairs (else TA_ERR_UNSUPPORTED).  The workspace
+ * holds 8 bytes for each page of the table's width (rounded up to 128) and query
+ * head of as many rows as 4 GiB take (one at least), and where T >= 2 S some
+ * 4 d for each such page and key head of each sequence.  Two launches for so many
+ * rows; where rows share their means, three for so many and one more. */
 ta_status tiered_attn_cache_select(const ta_cache_params* p, const ta_cache* cache,
                                    const void* Q_dev, const int32_t* cu_dev,
                                    const int32_t* seq_lens_dev, const int32_t* table_dev,

@@ -378,17 +378,18 @@ __device__ __forceinline__ RowPages row_pages(const CacheArgs& a, int t, int s) 
   return r;
 }
 
-// Scratch.  For each (row, query head) `pitch` doubles, of which the fp32
-// logits (in log2 units) take the first half until the row is done in fp64.
+// Scratch.  For each (row, query head), of the rows that choose at a time,
+// `pitch` doubles, of which the fp32 logits (in log2 units) take the first half
+// until the row is done in fp64.
 // For the fast logits also: for each (sequence, key head) the split tiles, the
 // pages' norms and the powers of two that undo their scaling; the queries'
 // norms; for each row its sequence and number of pages; the list of items that
 // fp64 has to decide.
 __device__ __forceinline__ double* logit_row(const CacheArgs& a, int t, int h) {
-  return a.scratch + ((int64_t)t * a.H + h) * select_pitch(a.max_pages);
+  return a.scratch + ((int64_t)(t - a.row0) * a.H + h) * select_pitch(a.max_pages);
 }
 __device__ __forceinline__ unsigned char* split_tile(const CacheArgs& a, int s, int hk, int jb, int bytes) {
-  return reinterpret_cast<unsigned char*>(a.scratch + (int64_t)a.T * a.H * select_pitch(a.max_pages)) +
+  return reinterpret_cast<unsigned char*>(a.scratch + (int64_t)a.logit_rows * a.H * select_pitch(a.max_pages)) +
          (((int64_t)s * a.Hkv + hk) * (select_pitch(a.max_pages) / 128) + jb) * bytes;
 }
 __device__ __forceinline__ float* norm_row(const CacheArgs& a, int s, int hk) {
@@ -405,6 +406,14 @@ __device__ __forceinline__ int2* row_info(const CacheArgs& a) {
 // Items (row, key head) that fp64 has to decide, and how many.
 __device__ __forceinline__ int2* again_list(const CacheArgs& a) { return row_info(a) + a.T + (a.T & 1) + 2; }
 __device__ __forceinline__ int* again_count(const CacheArgs& a) { return reinterpret_cast<int*>(again_list(a) - 1); }
+
+// A tile's rows among those that choose now.
+__device__ __forceinline__ RowTile choosing_tile(const CacheArgs& a, int tile_rows) {
+  RowTile r = row_tile(a, (a.cu ? a.row0 / tile_rows : a.row0) + blockIdx.x, tile_rows);
+  r.t0 = max(r.t0, a.row0);
+  r.t1 = min(r.t1, a.row0 + a.row_n);
+  return r;
+}
 
 __device__ __forceinline__ void dmma(double (&c)[2], double a, double b) {
   asm volatile("mma.sync.aligned.m8n8k4.row.col.f64.f64.f64.f64 {%0, %1}, {%2}, {%3}, {%0, %1};"
@@ -452,7 +461,7 @@ __global__ void __launch_bounds__(kSelThreads, 3) cache_logits64_kernel(const Ca
   constexpr int K = D / 32, STEP = kSelThreads / 32 * 8;   // 16-byte chunks of a lane; pages of a step
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane >> 3, li = lane & 7;
   const int hk = blockIdx.y;
-  const RowTile tile = row_tile(a, blockIdx.x, tile_rows);
+  const RowTile tile = choosing_tile(a, tile_rows);
   const int s = tile.s, t0 = tile.t0, t1 = tile.t1;
   if (t0 >= t1) return;
   const RowPages last = row_pages(a, t1 - 1, s);   // the tile's longest row
@@ -572,7 +581,6 @@ __global__ void __launch_bounds__(kSelThreads) cache_split_kernel(const CacheArg
   constexpr int E = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int jb = blockIdx.x / 4, hk = blockIdx.y, s = blockIdx.z;
-  if (blockIdx.x == 0 && hk == 0 && s == 0 && threadIdx.x == 0) *again_count(a) = 0;
   const int end = pages_competing(a, s);
   if ((int)blockIdx.x * 32 >= end) return;
   unsigned char* tile = split_tile(a, s, hk, jb, T::kBytes);
@@ -648,7 +656,8 @@ __global__ void __launch_bounds__(288, 2) cache_logits_kernel(const CacheArgs a,
   unsigned char* smem = sel_raw + ((1024 - (smem_u32(sel_raw) & 1023)) & 1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hk = blockIdx.y;
-  const RowTile tile = row_tile(a, blockIdx.x, tile_rows);
+  if (blockIdx.x == 0 && hk == 0 && threadIdx.x == 0) *again_count(a) = 0;
+  const RowTile tile = choosing_tile(a, tile_rows);
   const int s = tile.s, t0 = tile.t0, t1 = tile.t1;
   if (t0 >= t1) return;
   if (hk == 0)
@@ -1171,7 +1180,7 @@ template <int HN>
 __global__ void __launch_bounds__(kSelThreads, 3) cache_choose64_kernel(const CacheArgs a) {
   __shared__ ExactSmem sm;
   extern __shared__ __align__(16) unsigned char sel_smem[];
-  const int t = blockIdx.x, hk = blockIdx.y;
+  const int t = a.row0 + blockIdx.x, hk = blockIdx.y;
   if (t >= rows_used(a)) return;
   const RowPages r = row_pages(a, t, row_seq(a, t));
   if (fixed_pages(a, r, (int64_t)t * a.Hkv + hk, threadIdx.x, kSelThreads))
@@ -1414,9 +1423,9 @@ __global__ void __launch_bounds__(kSelThreads, E == 16 ? 4 : E == 32 ? 2 : 1) ca
   __shared__ FastSmem<WPI, E> sm;
   constexpr int IPB = 8 / WPI, GS = 32 * WPI;
   const int warp = threadIdx.x >> 5, lid = WPI == 1 ? threadIdx.x & 31 : threadIdx.x;
-  const int64_t item = (int64_t)blockIdx.x * IPB + (WPI == 1 ? warp : 0);
+  const int64_t item = (int64_t)a.row0 * a.Hkv + (int64_t)blockIdx.x * IPB + (WPI == 1 ? warp : 0);
   const int t = (int)(item / a.Hkv), hk = (int)(item - (int64_t)t * a.Hkv);
-  if (t >= rows_used(a)) return;
+  if (t >= min(rows_used(a), a.row0 + a.row_n)) return;
   const int2 info = row_info(a)[t];
   // (a row that a malformed cu gives to no tile has none: no pages)
   const bool known = (unsigned)info.x < (unsigned)a.S && (unsigned)info.y <= (unsigned)a.max_pages;
@@ -1488,67 +1497,76 @@ static cudaError_t run_exact(Kernel k, dim3 grid, int bytes, int dev, const Cach
 }
 
 template <int D>
-static cudaError_t select_d(const CacheArgs& a, cudaStream_t s) {
+static cudaError_t select_d(CacheArgs a, cudaStream_t s) {
   int dev = 0, sms = 0;
   cudaError_t e = device_sms(dev, sms);
   if (e != cudaSuccess) return e;
+  a.logit_rows = select_rows(a.H, a.T, a.max_pages);
   // The fast logits (a key head's queries have to fit a tile) take four kernels,
   // 28 us for a row and for a hundred; fp64 takes two, whose time grows with the
   // rows: 8 key heads of 4 query heads over 160 pages, 63 rows: 35 us fast and
   // 24 in fp64, 158 rows: 36 and 45; 4 key heads of 1 over 140 pages, 158 rows:
   // 29 and 20, 904 rows: 38 and 63.
-  const bool fast = a.cu && a.T >= 2 * (int64_t)a.S && a.G <= kSelCols &&
+  const bool fast = a.cu && rows_share_means(a.T, a.S) && a.G <= kSelCols &&
                     (int64_t)a.T * a.Hkv * (a.G > 1 ? a.G : 2) >= 20ll * sms;
   const int most = fast ? kSelCols : 8;
   const int tile_rows = !a.cu || a.G >= most ? 1 : most / a.G;
-  const int64_t tiles = a.cu ? (int64_t)(a.T / tile_rows) + a.S : a.S;
   static OncePerDevice once_f, once_d;
   if (fast) {
     cache_split_kernel<D><<<dim3((unsigned)(select_pitch(a.max_pages) / 32), a.Hkv, a.S), kSelThreads, 0, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     e = once_f.allow(reinterpret_cast<const void*>(cache_logits_kernel<D>), dev, LogitsSmem<D>::kBytes);
-    if (e != cudaSuccess) return e;
-    cache_logits_kernel<D><<<dim3((unsigned)tiles, a.Hkv), 288, LogitsSmem<D>::kBytes, s>>>(a, tile_rows);
   } else {
-    // pages of a block: all of them, or so few that every SM has blocks, a
-    // multiple of what a block's warps take at a time
-    const int step = 64, groups = (tile_rows * a.G + 3) / 4;
-    int pages = (a.max_pages + step - 1) / step * step;
-    while (pages > 2 * step && tiles * a.Hkv * ((a.max_pages + pages - 1) / pages) < 8ll * sms)
-      pages = (pages / 2 + step - 1) / step * step;
-    const int bytes = groups * 4 * D * 8 + kSelThreads / 32 * 16 * D * 4;
     e = once_d.allow(reinterpret_cast<const void*>(cache_logits64_kernel<D>), dev, 232448);
-    if (e != cudaSuccess) return e;
-    cache_logits64_kernel<D><<<dim3((unsigned)tiles, a.Hkv, (a.max_pages + pages - 1) / pages), kSelThreads,
-                               bytes, s>>>(a, tile_rows, pages);
   }
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int64_t items = (int64_t)a.T * a.Hkv;
+  if (e != cudaSuccess) return e;
   // the fp64 choice: so many heads' logits in shared memory that three blocks
   // share an SM
   int heads = kExactHeads;
   while (heads > 1 && (heads / 2 >= a.G || heads * select_pitch(a.max_pages) * 8 > 65536)) heads /= 2;
   const int exact = heads * (int)select_pitch(a.max_pages) * 8;
-  if (!fast) {
-    const dim3 all(a.T, a.Hkv);
-    return heads == 4   ? run_exact<4>(cache_choose64_kernel<4>, all, exact, dev, a, s)
-           : heads == 2 ? run_exact<2>(cache_choose64_kernel<2>, all, exact, dev, a, s)
-                        : run_exact<1>(cache_choose64_kernel<1>, all, exact, dev, a, s);
+  for (a.row0 = 0; a.row0 < a.T; a.row0 += a.logit_rows) {
+    a.row_n = a.logit_rows < a.T - a.row0 ? a.logit_rows : a.T - a.row0;
+    // tiles that hold these rows: row t of sequence s > 0 lies in tile
+    // t / tile_rows + s or in the one before, of sequence 0 in t / tile_rows
+    const int64_t tiles = a.cu ? (int64_t)((a.row0 + a.row_n - 1) / tile_rows - a.row0 / tile_rows) + a.S : a.row_n;
+    const int64_t items = (int64_t)a.row_n * a.Hkv;
+    if (fast) {
+      cache_logits_kernel<D><<<dim3((unsigned)tiles, a.Hkv), 288, LogitsSmem<D>::kBytes, s>>>(a, tile_rows);
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      if (a.max_pages <= 512) {
+        cache_choose_kernel<1, 16><<<(unsigned)((items + 7) / 8), kSelThreads, 0, s>>>(a);
+      } else if (a.max_pages <= 1024) {
+        cache_choose_kernel<1, 32><<<(unsigned)((items + 7) / 8), kSelThreads, 0, s>>>(a);
+      } else if (a.max_pages <= 8192) {
+        cache_choose_kernel<8, 32><<<(unsigned)items, kSelThreads, 0, s>>>(a);
+      } else {
+        cache_choose_kernel<8, 64><<<(unsigned)items, kSelThreads, 0, s>>>(a);
+      }
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      const dim3 again((unsigned)(items < 4ll * sms ? items : 4ll * sms));
+      e = heads == 4   ? run_exact<10 * D + 4>(cache_again_kernel<D, 4>, again, exact, dev, a, s)
+          : heads == 2 ? run_exact<10 * D + 2>(cache_again_kernel<D, 2>, again, exact, dev, a, s)
+                       : run_exact<10 * D + 1>(cache_again_kernel<D, 1>, again, exact, dev, a, s);
+    } else {
+      // pages of a block: all of them, or so few that every SM has blocks, a
+      // multiple of what a block's warps take at a time
+      const int step = 64, groups = (tile_rows * a.G + 3) / 4;
+      int pages = (a.max_pages + step - 1) / step * step;
+      while (pages > 2 * step && tiles * a.Hkv * ((a.max_pages + pages - 1) / pages) < 8ll * sms)
+        pages = (pages / 2 + step - 1) / step * step;
+      const int bytes = groups * 4 * D * 8 + kSelThreads / 32 * 16 * D * 4;
+      cache_logits64_kernel<D><<<dim3((unsigned)tiles, a.Hkv, (a.max_pages + pages - 1) / pages), kSelThreads,
+                                 bytes, s>>>(a, tile_rows, pages);
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      const dim3 all(a.row_n, a.Hkv);
+      e = heads == 4   ? run_exact<4>(cache_choose64_kernel<4>, all, exact, dev, a, s)
+          : heads == 2 ? run_exact<2>(cache_choose64_kernel<2>, all, exact, dev, a, s)
+                       : run_exact<1>(cache_choose64_kernel<1>, all, exact, dev, a, s);
+    }
+    if (e != cudaSuccess) return e;
   }
-  const int again = (int)(items < 4ll * sms ? items : 4ll * sms);
-  if (a.max_pages <= 512) {
-    cache_choose_kernel<1, 16><<<(unsigned)((items + 7) / 8), kSelThreads, 0, s>>>(a);
-  } else if (a.max_pages <= 1024) {
-    cache_choose_kernel<1, 32><<<(unsigned)((items + 7) / 8), kSelThreads, 0, s>>>(a);
-  } else if (a.max_pages <= 8192) {
-    cache_choose_kernel<8, 32><<<(unsigned)items, kSelThreads, 0, s>>>(a);
-  } else {
-    cache_choose_kernel<8, 64><<<(unsigned)items, kSelThreads, 0, s>>>(a);
-  }
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return heads == 4   ? run_exact<10 * D + 4>(cache_again_kernel<D, 4>, dim3(again), exact, dev, a, s)
-         : heads == 2 ? run_exact<10 * D + 2>(cache_again_kernel<D, 2>, dim3(again), exact, dev, a, s)
-                      : run_exact<10 * D + 1>(cache_again_kernel<D, 1>, dim3(again), exact, dev, a, s);
+  return cudaSuccess;
 }
 
 cudaError_t launch_cache_select(const CacheArgs& a, cudaStream_t s) {

@@ -55,6 +55,8 @@ struct CacheArgs {
   float* part_ml;
   float* part_o;
   double* scratch;
+  // page choice: rows that scratch has logits for, and those whose stand there
+  int logit_rows, row0, row_n;
   // sparse attention of many rows (parts of scratch)
   int tile_rows;                  // rows that share their pages' loads
   int list_cap;                   // entries of a tile's page list
@@ -81,6 +83,18 @@ inline int64_t tile_count(int rows, int64_t T, int64_t S) { return T / rows + S;
 
 // Doubles of a row of the choice's scratch: whole tiles of 128 pages.
 __host__ __device__ inline int64_t select_pitch(int max_pages) { return ((int64_t)max_pages + 127) / 128 * 128; }
+// Whether the logits of many rows may come from split means (given by cu).
+inline bool rows_share_means(int64_t T, int64_t S) { return T >= 2 * S; }
+// Rows that choose at a time: as many as have their logits in 4 GiB, so that a
+// long prompt, or a table far wider than its sequences, does not ask for more.
+// 32 query heads, 8 key heads, 1 GiB at a time, 4, and all at once: 8000 rows of
+// tables of 8192 pages (16.9 GB) 3981, 2817 and 2682 us, 4680 rows (9.9 GB) 1640,
+// 1374 and 1303, 32768 rows of 512 pages (4.3 GB) 1248, 1157 and 1188.
+constexpr int64_t kMaxLogitBytes = (int64_t)1 << 32;
+inline int select_rows(int H, int T, int max_pages) {
+  const int64_t n = kMaxLogitBytes / (select_pitch(max_pages) * H * 8);
+  return n < 1 ? 1 : n < T ? (int)n : T;
+}
 
 cudaError_t launch_cache_append(const CacheArgs& a, cudaStream_t s);
 cudaError_t launch_cache_select(const CacheArgs& a, cudaStream_t s);

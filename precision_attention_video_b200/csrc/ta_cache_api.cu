@@ -39,13 +39,15 @@ bool select_fits(const ta_cache_params* p) {
   return p->max_pages <= ta::kMaxSelectPages && p->H / p->Hkv <= 128 && p->S <= 65535 &&
          (int64_t)p->T * p->Hkv <= 0x7fffffff;
 }
-// The choice's scratch (none where it refuses the sizes): logits; split means, their norms and scales; the
-// queries' norms; the rows; the list of items to do again.
+// The choice's scratch (none where it refuses the sizes): logits; and where rows
+// may share their means, split means, their norms and scales, the queries'
+// norms, the rows, and the list of items to do again.
 size_t select_bytes(const ta_cache_params* p) {
   if (p->n_select <= 0 || !select_fits(p)) return 0;
   const size_t pitch = (size_t)ta::select_pitch(p->max_pages), T = (size_t)p->T + (p->T & 1);
-  return pitch * ((size_t)p->T * p->H * 8 + (size_t)p->S * p->Hkv * (4 * p->d + 8)) + T * p->H * 4 + (T + 2) * 8 +
-         (size_t)p->T * p->Hkv * 8;
+  const size_t logits = pitch * p->H * 8 * ta::select_rows(p->H, p->T, p->max_pages);
+  if (!ta::rows_share_means(p->T, p->S)) return logits;
+  return logits + pitch * p->S * p->Hkv * (4 * p->d + 8) + T * p->H * 4 + (T + 2) * 8 + (size_t)p->T * p->Hkv * 8;
 }
 // Sparse attention's: parts of cut tiles, joint page lists and their lengths,
 // the rows' flags.

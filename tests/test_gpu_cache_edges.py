@@ -1,12 +1,13 @@
 """Cached attention where its numbers leave the ordinary range: page choices
-whose border masses no float holds, queries whose squares underflow."""
+whose border masses no float holds, queries whose squares underflow, more
+rows than have their logits in the workspace at a time."""
 
 import numpy as np
 import pytest
 import torch
 
 from oracle import cache as OC
-from test_gpu_cache import BF, Step, np64
+from test_gpu_cache import BF, DEV, Step, np64, pav
 
 pytestmark = pytest.mark.gpu
 
@@ -68,4 +69,35 @@ def test_select_near_ties_of_tiny_queries(cuda_ok, near, ek, eq):
     mean = mean + near * torch.randn(st.P, st.Hkv, st.d, generator=st.g)
     st.cache.k_mean.copy_(8 * mean * 2.0 ** ek)
     st.Q *= 8 * 2.0 ** eq
+    same_choice(st)
+
+
+# ---- more rows than have their logits in the workspace at a time ----
+@pytest.mark.parametrize("old,new,kw", [
+    # the fast choice: 256 rows at a time, tiles of 8 rows
+    ([900, 0, 40, 3, 500], [130, 300, 0, 1, 270], dict(H=128, Hkv=8, d=64, n_select=5)),
+    # fp64, two rows a tile, single rows among them
+    ([150] * 400, [2] * 200 + [1] * 200, dict(H=128, Hkv=32, d=64, n_select=6, pad=2)),
+    # fp64, a row a sequence
+    (list(range(300)), [1] * 300, dict(H=128, Hkv=32, d=64, n_select=4)),
+])
+def test_select_in_parts(cuda_ok, old, new, kw):
+    st = Step(old, new, ps=16, spare=16384 - 100, seed=23, **kw)
+    assert 16256 < st.W <= 16384 and st.T * st.H * 16384 * 8 > 1 << 32
+    mean = torch.randn(st.P, st.Hkv, st.d, generator=st.g)
+    st.cache.k_mean.copy_(mean)
+    n = pav().cache_workspace_bytes(st.p)
+    assert n < 5 << 30
+    same_choice(st)
+    # and a captured call of them, other lengths in the same buffers
+    sel = torch.full((st.T, st.Hkv, st.p.n_select), -2, dtype=torch.int32, device=DEV)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        pav().cache_select(st.p, st.cache, st.Q, st.t_table, st.t_lens, st.ws, sel, cu=st.t_cu)
+    st.lens = [max(n, a - 7) for a, n in zip(st.lens, st.new)]
+    st.t_lens.copy_(torch.tensor(st.lens, dtype=torch.int32))
+    sel.fill_(-2)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(sel, st.select())
     same_choice(st)
