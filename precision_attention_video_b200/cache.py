@@ -4,8 +4,9 @@ choice and sparse attention (the C ABI of include/tiered_attn_cache.h).
 Argument marshalling only, as in ``binding``: the operators run in the
 library's CUDA kernels, the caller owns every buffer.  A call goes through
 ``_cache_call`` (csrc/ta_cache_py.cpp), which checks and marshals in C++; what
-it refuses is checked again here, for the reason.  Strides come from the
-tensors of each call, sizes from the parameters::
+it refuses is checked again here, for the reason.  Where that module could not
+be built, all calls are checked and marshalled here (a warning says so once).
+Strides come from the tensors of each call, sizes from the parameters::
 
     p = pav.make_cache_params(n_pages=P, page_size=64, H=32, Hkv=8, d=128, S=S, T=T,
                               max_pages=W, n_select=16, rot_dim=128)
@@ -19,6 +20,7 @@ tensors of each call, sizes from the parameters::
 from __future__ import annotations
 
 import ctypes
+import warnings
 from typing import Optional
 
 import torch
@@ -77,15 +79,29 @@ def _fn(name):
 _call = None
 
 
+class _NoNative:
+    """In place of a C++ entry that is not there: refuses every call."""
+
+    @staticmethod
+    def append(*args):
+        return None
+
+    decode = select = sparse = append
+
+
 def _native():
-    """The C++ entry, bound to the library on first use; a missing one raises."""
+    """The C++ entry, bound to the library on first use."""
     global _call
     if _call is None:
         try:
             from . import _cache_call as m
         except ImportError as e:
-            raise ImportError("_cache_call.so is missing or does not load: build it with "
-                              "`python -m precision_attention_video_b200.build`") from e
+            _b.lib()                     # (a missing library raises)
+            warnings.warn(f"_cache_call.so is missing or does not load ({e}): cached attention is called "
+                          "through ctypes, some 10 us a call slower; `python -m "
+                          "precision_attention_video_b200.build` builds it", RuntimeWarning, stacklevel=3)
+            _call = _NoNative
+            return _call
         m.init(*(ctypes.cast(_fn("tiered_attn_cache_" + n), _vp).value
                  for n in ("append", "decode", "select", "sparse")))
         _call = m

@@ -1,6 +1,14 @@
 """Cached attention without a GPU: sizes at the edge of what the calls take."""
 
+import os
+import sys
+
+import pytest
+import torch
+
 import precision_attention_video_b200 as pav
+from precision_attention_video_b200 import build as build_module
+from precision_attention_video_b200 import cache as C
 
 
 def params(**kw):
@@ -29,3 +37,37 @@ def test_workspace_of_a_long_prompt_is_bounded():
     assert pav.cache_workspace_bytes(wide) < (1 << 32) + 2 * 8 * 16384 * 520 + (1 << 26)
     # a token a sequence: no split means
     assert pav.cache_workspace_bytes(params(T=3000, S=3000, max_pages=16384)) < (1 << 32) + (1 << 26)
+
+
+# ---- without the C++ entry ----
+def without_entry(monkeypatch):
+    monkeypatch.setitem(sys.modules, "precision_attention_video_b200._cache_call", None)
+    monkeypatch.delattr(pav, "_cache_call", raising=False)
+    monkeypatch.setattr(C, "_call", None)
+
+
+def test_the_library_is_built_where_the_entry_is_not(monkeypatch, tmp_path, capfd):
+    # torch's C++ headers or Python's are missing: the library needs neither
+    def fails():
+        raise RuntimeError("compiler failed on ta_cache_py.cpp")
+
+    old = tmp_path / "_cache_call.so"
+    old.write_bytes(b"of another library")
+    os.utime(old, (1, 1))
+    monkeypatch.setattr(build_module, "CALL", str(old))
+    monkeypatch.setattr(build_module, "_build_call", fails)
+    assert build_module.build() == build_module.LIB and os.path.exists(build_module.LIB)
+    assert not old.exists() and "_cache_call.so is not built" in capfd.readouterr().err
+
+
+def test_calls_without_the_entry_are_checked_in_python(monkeypatch):
+    without_entry(monkeypatch)
+    p = params(T=2, max_pages=4)
+    c = pav.make_cache(p, "cpu")
+    Q, ws = torch.zeros(2, 32, 128, dtype=torch.bfloat16), torch.zeros(16, dtype=torch.uint8)
+    table, lens = torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    with pytest.warns(RuntimeWarning, match="through ctypes"):
+        with pytest.raises(ValueError, match="expected CUDA tensors"):
+            pav.cache_decode(p, c, Q, table, lens, ws, Q)
+    with pytest.raises(ValueError, match="expected CUDA tensors"):    # (and once only)
+        pav.cache_select(p, c, Q, table, lens, ws, table)

@@ -1,6 +1,7 @@
 """Cached attention where its numbers leave the ordinary range: page choices
 whose border masses no float holds, queries whose squares underflow, more
-rows than have their logits in the workspace at a time."""
+rows than have their logits in the workspace at a time; calls without the C++
+entry."""
 
 import numpy as np
 import pytest
@@ -101,3 +102,25 @@ def test_select_in_parts(cuda_ok, old, new, kw):
     torch.cuda.synchronize()
     assert torch.equal(sel, st.select())
     same_choice(st)
+
+
+# ---- without the C++ entry ----
+@pytest.mark.filterwarnings("ignore:_cache_call.so is missing")
+def test_calls_through_ctypes_give_the_same_bits(cuda_ok, monkeypatch):
+    from test_cache_edges import without_entry
+
+    def step():
+        st = Step([70, 0, 300], [30, 9, 1], rot=64, inter=True, fp8=True, seed=5, pad=2)
+        cos, sin = st.tables(400)
+        Qr = torch.full_like(st.Q, 7.0)
+        st.append(cos, sin, pos=torch.arange(st.T, dtype=torch.int32, device=DEV), Q_out=Qr)
+        sel = st.select()
+        one = Step([900, 0], [0, 0], seed=6, cu=False)
+        return (Qr, st.cache.k.view(torch.uint8), st.cache.k_scale, st.cache.k_mean, sel, *st.sparse(sel),
+                *one.decode())
+
+    with_entry = step()
+    without_entry(monkeypatch)
+    for a, b in zip(with_entry, step()):
+        assert torch.equal(a.nan_to_num(9) if a.is_floating_point() else a,
+                           b.nan_to_num(9) if b.is_floating_point() else b)
