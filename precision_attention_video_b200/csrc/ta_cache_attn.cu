@@ -324,8 +324,10 @@ __device__ __forceinline__ void fold_unit(Fold<D, NT>& f, const unsigned char* s
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float x = FP8 ? s[kt][nt][j] * ks[j >> 1] : s[kt][nt][j];
-        s[kt][nt][j] = seen(kt, j >> 1, nt, j & 1) ? x * sq[nt][j & 1] : kNegInf;
+        // (the two powers of two meet first: a product of a huge key's codes
+        // need not fit a float before a tiny query's size is back in it)
+        const float x = FP8 ? ks[j >> 1] * sq[nt][j & 1] : sq[nt][j & 1];
+        s[kt][nt][j] = seen(kt, j >> 1, nt, j & 1) ? s[kt][nt][j] * x : kNegInf;
       }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)

@@ -1,14 +1,14 @@
 """Cached attention where its numbers leave the ordinary range: page choices
 whose border masses no float holds, queries whose squares underflow, more
 rows than have their logits in the workspace at a time; calls without the C++
-entry."""
+entry; keys and queries of very different magnitudes."""
 
 import numpy as np
 import pytest
 import torch
 
 from oracle import cache as OC
-from test_gpu_cache import BF, DEV, Step, np64, pav
+from test_gpu_cache import BF, DEV, Step, check_some, np64, pav
 
 pytestmark = pytest.mark.gpu
 
@@ -124,3 +124,27 @@ def test_calls_through_ctypes_give_the_same_bits(cuda_ok, monkeypatch):
     for a, b in zip(with_entry, step()):
         assert torch.equal(a.nan_to_num(9) if a.is_floating_point() else a,
                            b.nan_to_num(9) if b.is_floating_point() else b)
+
+
+# ---- keys and queries of very different magnitudes ----
+@pytest.mark.parametrize("up", [-100, 100, 116])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_scores_of_huge_keys_and_tiny_queries(cuda_ok, fp8, up):
+    # the scores are ordinary; neither factor of theirs is
+    def scaled(st):
+        if fp8:
+            st.cache.k_scale *= 2.0 ** up
+        else:
+            st.cache.k *= 2.0 ** up
+        st.Q *= 2.0 ** -up
+        return st
+
+    st = scaled(Step([700, 65, 3000], [0, 0, 0], fp8=fp8, seed=81, cu=False))
+    st.check(*st.decode())
+    st = Step([100, 40], [300, 333], H=16, Hkv=4, fp8=fp8, n_select=5, seed=82)
+    st.append()
+    scaled(st)
+    lists = torch.randint(-1, 8, (st.T, 4, 5), generator=st.g, dtype=torch.int32)
+    O, lse = st.sparse(lists.to(DEV))
+    check_some(st, O, lse, lists.tolist(), every=7)
+    assert st.status() == 0
