@@ -53,8 +53,9 @@ typedef enum {
   TA_CACHE_FP8 = 1           /* e4m3 codes and one power-of-two scale for each
                                 token and head: the smallest 2^k, k >= -126,
                                 with amax <= 448 * 2^k (1 for a zero token).
-                                A token with a value that is not finite gets
-                                a NaN scale */
+                                A token with a value that is not finite (a
+                                key: in fp32, after its rotation) gets a NaN
+                                scale */
 } ta_cache_format;
 
 typedef struct {

@@ -60,8 +60,9 @@ def rotate64(x, cos, sin, inter):
 
 
 def token_scale(amax: float) -> float:
-    """Smallest power of two s >= 2^-126 with amax <= 448 s; 1 for 0."""
-    if not math.isfinite(amax):
+    """Smallest power of two s >= 2^-126 with amax <= 448 s; 1 for 0.  NaN for
+    what is not finite in fp32 (a rotated key may pass it)."""
+    if not amax < float(np.finfo(np.float32).max):
         return math.nan
     if amax == 0.0:
         return 1.0

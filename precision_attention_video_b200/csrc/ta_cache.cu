@@ -93,10 +93,11 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
 }
 
 // Smallest power of two s >= 2^-126 with amax <= 448 s; 1 for 0, NaN when
-// amax is not finite.
+// amax is not finite: a rotated key that passes fp32's range comes as its largest
+// value (narrow_odd), which no bf16 value is.
 __device__ __forceinline__ float token_scale(float amax) {
   if (amax == 0.0f) return 1.0f;
-  if (!(amax < __int_as_float(0x7f800000))) return __int_as_float(0x7fffffff);
+  if (!(amax < __int_as_float(0x7f7fffff))) return __int_as_float(0x7fffffff);
   int e;
   const float m = frexpf(amax, &e);   // amax = m * 2^e, m in [0.5, 1); 448 = 0.875 * 2^9
   return ldexpf(1.0f, max(m <= 0.875f ? e - 9 : e - 8, -126));

@@ -1,7 +1,8 @@
 """Cached attention where its numbers leave the ordinary range: page choices
 whose border masses no float holds, queries whose squares underflow, more
 rows than have their logits in the workspace at a time; calls without the C++
-entry; keys and queries of very different magnitudes."""
+entry; keys and queries of very different magnitudes; rotated keys that no
+float holds."""
 
 import numpy as np
 import pytest
@@ -148,3 +149,25 @@ def test_scores_of_huge_keys_and_tiny_queries(cuda_ok, fp8, up):
     O, lse = st.sparse(lists.to(DEV))
     check_some(st, O, lse, lists.tolist(), every=7)
     assert st.status() == 0
+
+
+# ---- rotated keys that fp32 does not hold ----
+@pytest.mark.parametrize("inter", [False, True])
+def test_append_fp8_keys_beyond_floats(cuda_ok, inter):
+    # bf16 holds 3e38, and a pair of them turned by 45 degrees is 4.2e38: a
+    # token that is not finite (its scale is NaN); 2.2e38 still is
+    st = Step([0], [6], fp8=True, H=2, Hkv=1, d=64, ps=16, rot=64, inter=inter, seed=12)
+    st.K[1], st.K[2], st.K[3] = 3e38, 2.2e38, -3e38
+    cos = torch.full((8, 32), 0.5 ** 0.5, device=DEV)
+    k, v, ks, vs = st.arrays()
+    OC.append(k, v, ks, vs, None, np64(st.K), np64(st.V), st.lens, st.cu, st.table, np64(cos), np64(cos),
+              inter, fp8=True)
+    st.append(cos, cos)
+    k2, v2, ks2, vs2 = st.arrays()
+    pg = st.table[0][0]
+    assert np.isnan(ks[pg, 0, [1, 3]]).all() and np.isfinite(ks[pg, 0, [0, 2, 4, 5]]).all()
+    np.testing.assert_array_equal(ks2, ks)
+    np.testing.assert_array_equal(vs2, vs)
+    np.testing.assert_array_equal(v2, v)
+    for r in (0, 2, 4, 5):
+        np.testing.assert_array_equal(k2[pg, 0, r], k[pg, 0, r])
