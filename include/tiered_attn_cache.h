@@ -172,7 +172,9 @@ ta_status tiered_attn_cache_select(const ta_cache_params* p, const ta_cache* cac
  * bf16 [T, H, d]; lse_dev: f32 [T, H], or NULL.  A row without keys gives 0
  * and -inf.  Where sequences have many rows, neighbouring rows share the loads
  * of the pages they have in common; a row's result does not depend on what
- * other rows hold but for its rounding.  One launch, or three with many rows. */
+ * other rows hold but for its rounding.  O may not overlap Q (the same pointer is
+ * refused): with many rows some are done again from their queries.  One launch,
+ * or three with many rows. */
 ta_status tiered_attn_cache_sparse(const ta_cache_params* p, const ta_cache* cache,
                                    const void* Q_dev, const int32_t* sel_dev,
                                    const int32_t* cu_dev, const int32_t* seq_lens_dev,

@@ -366,7 +366,7 @@ def cache_select(p: ta_cache_params, cache: PagedCache, Q, table, lens, ws, sel,
 def cache_sparse(p: ta_cache_params, cache: PagedCache, Q, sel, table, lens, ws, O, cu=None,
                  lse: Optional[torch.Tensor] = None, stream=None) -> None:
     """Attention of each row, Q bf16 [T, H, d], over the pages of its list
-    ``sel`` into O (and ``lse`` f32 [T, H])."""
+    ``sel`` into O (and ``lse`` f32 [T, H]).  O may not overlap Q."""
     st = _native().sparse(p, cache._view, Q, sel, table, lens, ws, O, cu, lse,
                           None if stream is None else _b._stream(stream))
     if st is not None:

@@ -204,6 +204,7 @@ ta_status attend(const ta_cache_params* p, const ta_cache* cache, const void* Q,
       (lse && !aligned(lse, 4)))
     return TA_ERR_INVALID_ARG;
   if ((st = check_ws(ws, ws_bytes, ta::kWsScratch + (sparse ? sparse_bytes(p) : 0))) != TA_OK) return st;
+  if (sparse && O == Q) return TA_ERR_INVALID_ARG;   // (a row may be done again from its queries)
   CacheArgs a;
   fill(p, cache, cu, lens, table, ws, a);
   a.q = static_cast<const __nv_bfloat16*>(Q);

@@ -2,7 +2,7 @@
 whose border masses no float holds, queries whose squares underflow, more
 rows than have their logits in the workspace at a time; calls without the C++
 entry; keys and queries of very different magnitudes; rotated keys that no
-float holds."""
+float holds; results over the queries."""
 
 import numpy as np
 import pytest
@@ -171,3 +171,14 @@ def test_append_fp8_keys_beyond_floats(cuda_ok, inter):
     np.testing.assert_array_equal(v2, v)
     for r in (0, 2, 4, 5):
         np.testing.assert_array_equal(k2[pg, 0, r], k[pg, 0, r])
+
+
+# ---- results over the queries ----
+def test_sparse_does_not_write_over_its_queries(cuda_ok):
+    # rows with a hidden value that is not finite are done again from their
+    # queries: O on top of them is refused
+    st = Step([0], [800], H=8, Hkv=8, d=64, ps=16, n_select=3, seed=7)
+    st.append()
+    lists = torch.randint(0, 50, (800, 8, 3), generator=st.g, dtype=torch.int32)
+    with pytest.raises(pav().TieredAttnError, match="invalid argument"):
+        pav().cache_sparse(st.p, st.cache, st.Q, lists.to(DEV), st.t_table, st.t_lens, st.ws, st.Q, cu=st.t_cu)
