@@ -127,7 +127,10 @@ class PagedCache:
     float8_e4m3fn [n_pages, Hkv, page_size, d] (any order of the outer three
     dimensions in memory), ``k_scale`` and ``v_scale`` f32 [n_pages, Hkv,
     page_size] for FP8, ``k_mean`` f32 [n_pages, Hkv, d] where pages are
-    chosen.  ``k`` and ``v`` may be None for a cache that is only chosen from."""
+    chosen.  ``k`` and ``v`` may be None for a cache that is only chosen from.
+    Calls read the tensors' places from here, so they cannot be exchanged for
+    others (nor may their memory be: ``set_``, ``resize_``); make a new
+    PagedCache instead."""
 
     __slots__ = ("k", "v", "k_scale", "v_scale", "k_mean", "_view", "_strides", "_shape", "_fmt",
                  "_dev")
@@ -137,8 +140,9 @@ class PagedCache:
         if some is None:
             raise ValueError("PagedCache: neither keys nor means")
         self._dev = some.get_device()
-        self._fmt, self._shape, self._strides = None, None, (0, 0, 0)
-        if k is not None:
+        if k is None:
+            self._fmt, self._shape, self._strides = None, None, (0, 0, 0)
+        else:
             if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
                 raise TypeError(f"k: expected torch.bfloat16 or torch.float8_e4m3fn, got {k.dtype}")
             if not isinstance(v, torch.Tensor) or v.dtype != k.dtype:
@@ -167,6 +171,11 @@ class PagedCache:
                        for t in (k, v, k_scale, v_scale, k_mean))),
             self._strides, (n, h, ps, d), -1 if self._fmt is None else self._fmt, self._dev,
             int(k_mean is not None))
+
+    def __setattr__(self, name, value):
+        if getattr(self, name, value) is not value:      # (cache.k *= 2 sets k itself)
+            raise AttributeError(f"PagedCache.{name} cannot be exchanged: make a new PagedCache")
+        object.__setattr__(self, name, value)
 
 
 def make_cache(p: ta_cache_params, device="cuda", layout: str = "hnd",

@@ -71,3 +71,15 @@ def test_calls_without_the_entry_are_checked_in_python(monkeypatch):
             pav.cache_decode(p, c, Q, table, lens, ws, Q)
     with pytest.raises(ValueError, match="expected CUDA tensors"):    # (and once only)
         pav.cache_select(p, c, Q, table, lens, ws, table)
+
+
+# ---- a cache's tensors ----
+def test_the_tensors_of_a_cache_cannot_be_exchanged():
+    # calls would go on reading the old ones, which nothing holds any more
+    c = pav.make_cache(params(), "cpu")
+    for name in ("k", "v", "k_scale", "v_scale", "k_mean"):
+        with pytest.raises(AttributeError, match="make a new PagedCache"):
+            setattr(c, name, torch.zeros(1))
+    c.k[0] = 1.0                                     # (their values may)
+    c.k *= 2
+    assert c.k[0, 0, 0, 0] == 2 and pav.PagedCache(None, None, k_mean=c.k_mean).k is None
