@@ -354,16 +354,18 @@ __global__ void __launch_bounds__(kAppendThreads, 4) cache_append_kernel(const C
 // (about one in a hundred on random means, and ties) are listed and done again
 // in fp64.
 //
-// The error: a page's mean is scaled by a power of two to f16's range and
-// split into two f16 parts (22 bits of each element), the query scaled the same
-// way (its 8 bits are exact down to 2^-14 of its largest element); what is cut
-// off is at most 2^-21 of |q| |kbar|.  64 products each go into a sum of their
-// own, 16 at a time with what the sum was, and an addend may lose 2^-24 of the
-// largest: 4 * 17 * 2^-24 < 2^-17.9 in all.  2^-17.7 scale |q| |kbar| covers
-// both with fp32's few roundings.
+// The error, in parts of |q| |kbar|, both scaled by powers of two to a largest
+// element in [1, 2).  Two f16 parts hold an element of the mean to 2^-22 of it or
+// half f16's smallest step, 2^-25; the query's 8 bits are exact down to 2^-17 and
+// below that to 2^-25; over d = 128 elements that is 2^-22 + 2 sqrt(d) 2^-25 at
+// most.  64 products each go into a sum of their own, 16 at a time with what the
+// sum was, and an addend may lose 2^-24 of the largest: 4 * 17 * 2^-24 (the rest
+// parts, which go first, are 2^-11 of that).  Joining the two sums and the two
+// scales round by 2^-24 each.  5.15e-6 in all; what is of second order, and the
+// norms' own roundings, the factor 1.1 at the decision covers.
 constexpr int kSelThreads = 256;
 constexpr int kSelCols = 128;          // (row, head) columns of a fast logits block
-constexpr float kLogitErr = 4.7e-6f;   // 2^-17.7
+constexpr float kLogitErr = 5.2e-6f;
 constexpr float kInf = 3.0e38f;        // a logit above is taken as not finite
 
 // Pages that row t sees, and the pages [c0, c1) that compete for it.

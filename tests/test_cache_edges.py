@@ -1,6 +1,7 @@
 """Cached attention without a GPU: sizes at the edge of what the calls take."""
 
 import os
+import re
 import sys
 
 import pytest
@@ -83,3 +84,17 @@ def test_the_tensors_of_a_cache_cannot_be_exchanged():
     c.k[0] = 1.0                                     # (their values may)
     c.k *= 2
     assert c.k[0, 0, 0, 0] == 2 and pav.PagedCache(None, None, k_mean=c.k_mean).k is None
+
+
+# ---- constants of the page choice ----
+CSRC = os.path.join(os.path.dirname(os.path.abspath(build_module.__file__)), "csrc")
+
+
+def test_the_bound_of_the_fast_logits_covers_its_parts():
+    # f16 parts of the means and the queries, fp32 sums of 64 products, the join
+    # of two sums and two scales (d = 128, the larger of the two)
+    with open(os.path.join(CSRC, "ta_cache.cu")) as f:
+        err = float(re.search(r"kLogitErr = ([0-9.e-]+)f;", f.read()).group(1))
+    u = 2.0 ** -24
+    parts = 2.0 ** -22 + 2 * 128 ** 0.5 * 2.0 ** -25 + 4 * 17 * u + 3 * u
+    assert parts <= err <= 1.05 * parts
