@@ -115,7 +115,8 @@ ta_status tiered_attn_cache_init(void* ws_dev, size_t ws_bytes, void* stream);
  *    cos_dev and sin_dev (f32 [rot_rows, rot_dim/2]; pos int32 [T], NULL: the
  *    row's position in its sequence): a pair (x, y) becomes
  *    (x cos - y sin, y cos + x sin).  A pos outside the table leaves the
- *    token unwritten and sets TA_ERR_BAD_INDEX.
+ *    token (and its rotated query) unwritten and sets TA_ERR_BAD_INDEX; its
+ *    page fills all the same, the mean counting what stood in its slot.
  *  - Q_dev, when not NULL, is rotated the same way into Q_out_dev (which may
  *    be Q_dev with equal strides).
  *  - k_mean of every page that these tokens fill up is written: the fp32 sum

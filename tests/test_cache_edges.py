@@ -1,8 +1,13 @@
 """Cached attention without a GPU: sizes at the edge of what the calls take."""
 
+import functools
+import math
 import os
+import random
 import re
 import sys
+from decimal import Decimal, getcontext
+from fractions import Fraction
 
 import pytest
 import torch
@@ -98,3 +103,52 @@ def test_the_bound_of_the_fast_logits_covers_its_parts():
     u = 2.0 ** -24
     parts = 2.0 ** -22 + 2 * 128 ** 0.5 * 2.0 ** -25 + 4 * 17 * u + 3 * u
     assert parts <= err <= 1.05 * parts
+
+
+@functools.cache
+def source(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return f.read()
+
+
+def exp_down(x):
+    """The fp64 exponential of the page choice, step by step, its constants read
+    from the source.  fma as the product's and the sum's exact value, rounded
+    once."""
+    body = source("ta_cache.cu")
+    body = body[body.index("double exp_down("):]
+    body = re.sub(r"//[^\n]*", "", body[:body.index("\n}\n")])
+    magic, low, inv = (float(re.search(p, body).group(1)) for p in (
+        r"magic = ([0-9.]+);", r"fmax\(x, (-[0-9.]+)\)", r"fma\(y, ([0-9.]+), magic\)"))
+    ln2 = [float.fromhex(h) for h in re.findall(r"fma\(n, (-0x[0-9a-f.]+p-?[0-9]+), \w\)", body)]
+    tail = [float(a) / float(b) for a, b in re.findall(r"([0-9.]+) / ([0-9.]+)", body)]
+    assert len(ln2) == 2 and tail == [1 / 720, 1 / 120, 1 / 24, 1 / 6]
+    fma = lambda a, b, c: float(Fraction(a) * Fraction(b) + Fraction(c))  # noqa: E731
+    y = max(x, low)
+    z = fma(y, inv, magic)
+    n = z - magic
+    k, e = int(n) & 31, int(n) >> 5
+    r = fma(n, ln2[1], fma(n, ln2[0], y))
+    p = fma(r, tail[0], tail[1])
+    for c in (*tail[2:], 0.5, 1.0):
+        p = fma(r, p, c)
+    t = math.exp2(k / 32)
+    v = fma(t * r, p, t)
+    return v * 2.0 ** (e >> 1) * 2.0 ** (e - (e >> 1))
+
+
+def test_the_fp64_exponential_is_right_to_about_a_unit():
+    # against e^x in 50 digits; below 2^-1022 half a subnormal step comes on top
+    getcontext().prec = 50
+    rng = random.Random(0)
+    xs = [-rng.uniform(0, 1) for _ in range(500)] + [-rng.uniform(0, 708) for _ in range(1500)] + \
+        [-j * math.log(2) / 32 for j in range(0, 2000, 7)] + [-2.0 ** -k for k in range(60)]
+    worst = 0.0
+    for x in xs:
+        want = Decimal(x).exp()
+        unit = Decimal(math.ulp(float(want)))
+        worst = max(worst, float(abs(Decimal(exp_down(x)) - want) / unit))
+    assert worst <= 1.25, worst
+    assert exp_down(0.0) == 1.0 and exp_down(-745.5) == exp_down(-900.0) == exp_down(-1e30) == 0.0
+    for x in (-710.0, -730.3, -744.0):
+        assert abs(exp_down(x) - math.exp(x)) <= 2 * 5e-324

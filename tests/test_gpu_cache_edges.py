@@ -2,7 +2,8 @@
 whose border masses no float holds, queries whose squares underflow, more
 rows than have their logits in the workspace at a time; calls without the C++
 entry; keys and queries of very different magnitudes; rotated keys that no
-float holds; results over the queries."""
+float holds; results over the queries; positions and lengths out
+of range."""
 
 import numpy as np
 import pytest
@@ -182,3 +183,88 @@ def test_sparse_does_not_write_over_its_queries(cuda_ok):
     lists = torch.randint(0, 50, (800, 8, 3), generator=st.g, dtype=torch.int32)
     with pytest.raises(pav().TieredAttnError, match="invalid argument"):
         pav().cache_sparse(st.p, st.cache, st.Q, lists.to(DEV), st.t_table, st.t_lens, st.ws, st.Q, cu=st.t_cu)
+
+
+# ---- the fast choice at every width of the table ----
+@pytest.mark.parametrize("W", [240, 700, 3000, 9000])
+@pytest.mark.parametrize("near", [1e-4, 1e-6])
+def test_select_near_ties_at_every_width(cuda_ok, near, W):
+    st = Step([3000, 500], [400, 100], ps=16, n_select=12, H=12, Hkv=3, seed=29, spare=W - 213)
+    assert st.W == W
+    base = torch.randn(3, 1, st.Hkv, st.d, generator=st.g)
+    mean = base[torch.randint(0, 3, (st.P,), generator=st.g), 0]
+    st.cache.k_mean.copy_(mean + near * torch.randn(st.P, st.Hkv, st.d, generator=st.g))
+    same_choice(st)
+
+
+def test_select_many_rows_of_more_than_8192_pages(cuda_ok):
+    st = Step([9000 * 16], [100], H=32, Hkv=8, d=64, ps=16, n_select=24, seed=30)
+    st.cache.k_mean.copy_(torch.randn(st.P, st.Hkv, st.d, generator=st.g))
+    same_choice(st)
+
+
+# ---- positions and lengths out of range ----
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("given", [False, True])
+def test_append_positions_outside_the_angles(cuda_ok, fp8, given):
+    # rows 3 and 20: their slots stay as they were, and their pages' means count that
+    st = Step([10], [60], ps=16, d=64, rot=64, fp8=fp8, seed=31)
+    cos, sin = st.tables(70)
+    pos = torch.arange(10, 70, dtype=torch.int32)
+    bad = [3, 20] if given else [58, 59]
+    if given:
+        pos[3], pos[20] = -1, 70
+    else:
+        cos, sin = cos[:68].contiguous(), sin[:68].contiguous()
+    if fp8:                                          # (something to count)
+        st.cache.k.view(torch.uint8).fill_(0x38)
+        st.cache.k_scale.fill_(0.25)
+    else:
+        st.cache.k.fill_(0.25)
+    k, v, ks, vs = st.arrays()
+    mean = np64(st.cache.k_mean)
+    before = [None if x is None else x.copy() for x in (k, v, ks, vs)]
+    clipped = [min(max(int(p), 0), len(cos) - 1) for p in pos]
+
+    def put_back():
+        for t in bad:
+            pg, slot = st.table[0][(10 + t) // 16], (10 + t) % 16
+            for x, b in zip((k, v, ks, vs), before):
+                if x is not None:
+                    x[pg, :, slot] = b[pg, :, slot]
+
+    OC.append(k, v, ks, vs, None, np64(st.K), np64(st.V), st.lens, st.cu, st.table, np64(cos), np64(sin),
+              fp8=fp8, pos=clipped)
+    put_back()
+    for j in range(4):                               # means of the pages as they now stand
+        pg, acc = st.table[0][j], np.zeros((st.Hkv, st.d), np.float32)
+        x = OC.decoded(k, ks, fp8)[pg].astype(np.float32)
+        for r in range(16):
+            acc = acc + x[:, r]
+        mean[pg] = acc * np.float32(1 / 16)
+    Qr = torch.full_like(st.Q, 7.0)
+    st.append(cos, sin, pos=pos.to(DEV) if given else None, Q_out=Qr)
+    torch.cuda.synchronize()
+    assert st.status() == pav().TA_ERR_BAD_INDEX
+    for a, b in zip(st.arrays(), (k, v, ks, vs)):
+        if a is not None:
+            np.testing.assert_array_equal(a, b)
+    np.testing.assert_array_equal(np64(st.cache.k_mean), mean)
+    for t in range(60):
+        want = OC.rotate32(np64(st.Q)[t], np64(cos)[clipped[t]], np64(sin)[clipped[t]], False)
+        np.testing.assert_array_equal(np64(Qr)[t], 7.0 if t in bad else OC.bf16_rne(np.float64(want)))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_lengths_are_clamped_to_the_table(cuda_ok, fp8):
+    # 10^9 tokens are the 256 of the table's four pages, -3 are none
+    st = Step([256, 0], [0, 0], seed=51, cu=False, H=4, Hkv=2, fp8=fp8)
+    assert st.W == 4
+    want, want_lse = st.decode()
+    st.check(want, want_lse)
+    st.t_lens.copy_(torch.tensor([10 ** 9, -3], dtype=torch.int32))
+    O, lse = st.decode()
+    torch.cuda.synchronize()
+    assert st.status() == pav().TA_ERR_BAD_INDEX
+    assert torch.equal(O, want) and torch.equal(lse, want_lse)
+    assert (O[1] == 0).all() and (lse[1] == -float("inf")).all()
