@@ -3,7 +3,7 @@ whose border masses no float holds, queries whose squares underflow, more
 rows than have their logits in the workspace at a time; calls without the C++
 entry; keys and queries of very different magnitudes; rotated keys that no
 float holds; results over the queries; positions and lengths out
-of range."""
+of range; sizes at the ends of their ranges."""
 
 import numpy as np
 import pytest
@@ -268,3 +268,104 @@ def test_lengths_are_clamped_to_the_table(cuda_ok, fp8):
     assert st.status() == pav().TA_ERR_BAD_INDEX
     assert torch.equal(O, want) and torch.equal(lse, want_lse)
     assert (O[1] == 0).all() and (lse[1] == -float("inf")).all()
+
+
+# ---- sizes at the ends of their ranges ----
+@pytest.mark.parametrize("G", [33, 48, 64, 65, 128])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_large_groups(cuda_ok, fp8, G):
+    # up to 128 query heads of a key head: decode, choice of few and many rows,
+    # sparse attention of few and many
+    kw = dict(H=2 * G, Hkv=2, d=64, ps=16, fp8=fp8, n_select=5)
+    st = Step([300, 0, 17], [0, 0, 0], seed=G, cu=False, **kw)
+    st.check(*st.decode())
+    for old, new in (([200, 90], [1, 2]), ([100, 30], [330, 290])):
+        st = Step(old, new, seed=G + 1, **kw)
+        st.append()
+        same_choice(st)
+        lists = torch.randint(-1, st.W + 1, (st.T, 2, 5), generator=st.g, dtype=torch.int32)
+        O, lse = st.sparse(lists.to(DEV))
+        check_some(st, O, lse, lists.tolist(), every=37)
+        assert st.status() == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_as_many_sequences_as_a_decode_takes(cuda_ok, fp8):
+    lens = [(7 * i) % 97 for i in range(2048)]
+    st = Step(lens, [0] * 2048, H=2, Hkv=1, d=64, ps=32, fp8=fp8, seed=91, cu=False)
+    O, lse = st.decode()
+    check_some(st, O, lse, None, every=11)
+    assert st.status() == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_one_page_one_head_one_slot(cuda_ok, fp8):
+    # a cache of one page (whose strides say nothing), and its first token
+    st = Step([0], [1], H=1, Hkv=1, d=64, ps=16, fp8=fp8, n_select=2, seed=92)
+    m = pav()
+    c = m.make_cache(m.make_cache_params(n_pages=1, page_size=16, H=1, Hkv=1, d=64, S=1, T=1, max_pages=1,
+                                         format=int(fp8)), DEV)
+    p = m.make_cache_params(n_pages=1, page_size=16, H=1, Hkv=1, d=64, S=1, T=1, max_pages=1,
+                            format=int(fp8), n_select=2)
+    table = torch.zeros(1, 1, dtype=torch.int32, device=DEV)
+    ws = m.alloc_cache_workspace(p, DEV)
+    O, lse = st.out()
+    sel = torch.full((1, 1, 2), -2, dtype=torch.int32, device=DEV)
+    m.cache_append(p, c, st.K, st.V, table, st.t_lens, ws)
+    m.cache_select(p, c, st.Q, table, st.t_lens, ws, sel)
+    m.cache_decode(p, c, st.Q, table, st.t_lens, ws, O, lse=lse)
+    assert sel.tolist() == [[[0, -1]]] and m.get_status(ws) == 0
+    st.cache, st.table = c, [[0]]
+    st.check(O, lse)
+    m.cache_sparse(p, c, st.Q, sel, table, st.t_lens, ws, O, lse=lse)
+    st.check(O, lse)
+
+
+def test_steps_without_rows_and_rows_without_pages(cuda_ok):
+    # every sequence empty and only padding; then a prompt of which no row lists a page
+    st = Step([40, 0], [0, 0], cu=True, pad=700, H=8, Hkv=4, seed=93)
+    k = [None if x is None else x.copy() for x in st.arrays()]
+    st.append()
+    lists = torch.zeros((700, 4, 4), dtype=torch.int32, device=DEV)
+    O, lse = st.sparse(lists)
+    assert (st.select() == -2).all() and (O == 7).all() and (lse == 7).all()
+    for a, b in zip(k, st.arrays()):
+        np.testing.assert_array_equal(a, b) if a is not None else None
+    st = Step([100, 0], [400, 350], H=16, Hkv=4, seed=94)
+    st.append()
+    O, lse = st.sparse(torch.full((750, 4, 4), -1, dtype=torch.int32, device=DEV))
+    assert (O == 0).all() and (lse == -float("inf")).all() and st.status() == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_fused_projections_and_a_fused_cache(cuda_ok, fp8):
+    # Q, K, V as parts of one row, rotated in place; keys and values of a page
+    # next to each other in one tensor
+    m = pav()
+    st = Step([50, 3], [300, 280], H=16, Hkv=4, d=64, ps=32, rot=64, fp8=fp8, n_select=6, seed=95)
+    cos, sin = st.tables(400)
+    qkv = torch.cat([x.flatten(1) for x in (st.Q, st.K, st.V)], 1)
+    q, k, v = (x.unflatten(1, (-1, 64)) for x in qkv.split([16 * 64, 4 * 64, 4 * 64], 1))
+    both = torch.empty((st.P, 2, *st.cache.k.shape[1:]), dtype=torch.uint8 if fp8 else BF, device=DEV)
+    both = both.view(st.cache.k.dtype)
+    raw = (lambda x: x.view(torch.uint8)) if fp8 else (lambda x: x)
+    raw(both)[:, 0], raw(both)[:, 1] = raw(st.cache.k), raw(st.cache.v)
+    c = m.PagedCache(both[:, 0], both[:, 1], st.cache.k_scale, st.cache.v_scale, st.cache.k_mean)
+    means = st.cache.k_mean.clone()
+    m.cache_append(st.p, c, k, v, st.t_table, st.t_lens, st.ws, cu=st.t_cu, cos=cos, sin=sin, Q=q, Q_out=q)
+    sel = torch.full((st.T, 4, 6), -2, dtype=torch.int32, device=DEV)
+    m.cache_select(st.p, c, q, st.t_table, st.t_lens, st.ws, sel, cu=st.t_cu)
+    O, lse = st.out()
+    m.cache_sparse(st.p, c, q, sel, st.t_table, st.t_lens, st.ws, O, cu=st.t_cu, lse=lse)
+    got = [raw(both[:, 0]).clone(), raw(both[:, 1]).clone(), c.k_mean.clone(), sel, O, lse, q.contiguous()]
+    # the same with tensors of their own
+    c.k_mean.copy_(means)
+    Qr = torch.empty_like(st.Q)
+    st.append(cos, sin, Q_out=Qr)
+    st.Q = Qr
+    want = [raw(st.cache.k), raw(st.cache.v), st.cache.k_mean, st.select()]
+    want += [*st.sparse(want[3]), Qr]
+    for a, b in zip(got, want):
+        a, b = (x.nan_to_num(9) if x.is_floating_point() else x for x in (a, b))
+        assert torch.equal(a, b)
+    check_some(st, O, lse, sel.tolist(), every=17)
