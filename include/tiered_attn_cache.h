@@ -15,7 +15,11 @@
  * cu[s] .. cu[s+1]-1 of K_new, V_new, Q and O, and row t stands at position
  * seq_lens[s] - (cu[s+1] - t).  cu = NULL means one row for each sequence
  * (row s is sequence s; T must equal S).  A row sees the keys at positions up
- * to its own.  Rows from cu[S] on are padding: neither read nor written.
+ * to its own, also among the new tokens of a step: the tokens of a frame do not
+ * see the ones behind them.  (For a frame whose tokens all see each other, append
+ * it, then attend with a sequence for each row: cu = NULL, the frame's end as
+ * every length, the table's row repeated.)  Rows from cu[S] on are padding:
+ * neither read nor written.
  * Sequences may be empty (cu[s] = cu[s+1]).  cu ascends from 0; with one that
  * does not, results are undefined, but nothing outside the buffers is read or
  * written.
@@ -137,7 +141,9 @@ ta_status tiered_attn_cache_append(const ta_cache_params* p, const ta_cache* cac
 /* Attention of one new token of each sequence (row s of Q) over its whole
  * cache: O[s, h] = sum_i softmax_i(scale * q . k_i) v_i, i < seq_lens[s].
  * The keys are split evenly over the GPU and the parts joined in a fixed
- * order; the result depends on the lengths and not on timing.  O_dev: bf16
+ * order; the result depends on the lengths and not on timing.  The softmax's
+ * weights multiply V rounded to bf16 (FP8 caches: to f16); maxima, sums and O are
+ * fp32 until O's one rounding.  O_dev: bf16
  * [S, H, d]; lse_dev: f32 [S, H] ln sum_i exp(scale * q . k_i), or NULL.  An
  * empty sequence gives O = 0 and lse = -inf.  At most 2048 sequences (else
  * TA_ERR_UNSUPPORTED).  One launch. */
@@ -173,7 +179,9 @@ ta_status tiered_attn_cache_select(const ta_cache_params* p, const ta_cache* cac
  * bf16 [T, H, d]; lse_dev: f32 [T, H], or NULL.  A row without keys gives 0
  * and -inf.  Where sequences have many rows, neighbouring rows share the loads
  * of the pages they have in common; a row's result does not depend on what
- * other rows hold but for its rounding.  O may not overlap Q (the same pointer is
+ * other rows hold but for its rounding.  Weights are rounded as for decode, but
+ * where FP8 caches meet many rows to bf16, which is coarser.  A list of every page
+ * (n_select of them at most) makes it dense attention.  O may not overlap Q (the same pointer is
  * refused): with many rows some are done again from their queries.  One launch,
  * or three with many rows. */
 ta_status tiered_attn_cache_sparse(const ta_cache_params* p, const ta_cache* cache,

@@ -15,6 +15,11 @@ Strides come from the tensors of each call, sizes from the parameters::
     pav.cache_append(p, cache, K, V, table, lens, ws, cu=cu, cos=cos, sin=sin, Q=Q, Q_out=Q)
     pav.cache_select(p, cache, Q, table, lens, ws, sel, cu=cu)
     pav.cache_sparse(p, cache, Q, sel, table, lens, ws, O, cu=cu)
+
+A row sees the keys at positions up to its own, also among the new tokens of a
+step: the tokens of one latent frame do not see the ones behind them.  Where they
+should, append the frame and attend with a sequence for each row: no ``cu``,
+``lens`` the frame's end in every entry, the sequence's table row repeated.
 """
 
 from __future__ import annotations
@@ -113,7 +118,8 @@ def make_cache_params(*, n_pages: int, page_size: int, H: int, Hkv: int, d: int,
                       n_first: int = 1, n_recent: int = 1, rot_dim: int = 0,
                       rot_interleaved: int = 0, softmax_scale: float = 0.0) -> ta_cache_params:
     """Sizes of a cache and of a step: S sequences with T new tokens in all
-    (the buffers' rows), at most max_pages pages each."""
+    (the buffers' rows), at most max_pages pages each.  Rows attend causally,
+    among the new tokens too."""
     p = ta_cache_params()
     p.n_pages, p.page_size, p.H, p.Hkv, p.d, p.format = n_pages, page_size, H, Hkv, d, format
     p.S, p.T, p.max_pages = S, T, max_pages

@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) cache_append_kernel(const C
 // products with an fp32 sum and a bound of their error; where the last page
 // that is in and the first that is out lie further apart than the bound, the
 // set is the one that fp64 would find, whatever the rounding.  The other rows
-// (about one in a hundred on random means, and ties) are listed and done again
+// (1.6 percent on random means, and ties) are listed and done again
 // in fp64.
 //
 // The error, in parts of |q| |kbar|, both scaled by powers of two to a largest

@@ -723,7 +723,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NT>::kThreads, 1)
     if (lane == 0) mbar_arrive(&empty[st]);
 
     if (cur.k + 1 == cur.units || i + 1 == n_units) {
-      // ---- join the four warps ----
+      // ---- join the computing warps ----
       join_warps<C, D, FP8, NT>(f, join, sm_m);
       auto joined = [&](int nn, int d) { return joined_at<C, D, FP8, NT>(join, nn, d); };
       auto state = [&](int nn, float& mm, float& ll) { joined_state<C, NT>(sm_m, nn, mm, ll); };
@@ -897,7 +897,8 @@ __global__ void __launch_bounds__(256) cache_lists_kernel(const CacheArgs a) {
 //
 // Codes of FP8 caches load into the upper half of their buffer, and the softmax
 // threads widen them in place to bf16 with the scale multiplied in, which is
-// exact (4 significant bits, scales are powers of two).
+// exact (4 significant bits, scales are powers of two).  Their weights are bf16
+// here, as V is; few rows' are f16 (cache_attn_kernel), which holds 3 bits more.
 //
 // The tiles that are left after whole rounds of the GPU's places are cut along
 // their keys, so that the last round is full too: their parts meet in the

@@ -3,7 +3,7 @@ whose border masses no float holds, queries whose squares underflow, more
 rows than have their logits in the workspace at a time; calls without the C++
 entry; keys and queries of very different magnitudes; rotated keys that no
 float holds; results over the queries; positions and lengths out
-of range; sizes at the ends of their ranges."""
+of range; sizes at the ends of their ranges; frames whose tokens see each other."""
 
 import numpy as np
 import pytest
@@ -369,3 +369,25 @@ def test_fused_projections_and_a_fused_cache(cuda_ok, fp8):
         a, b = (x.nan_to_num(9) if x.is_floating_point() else x for x in (a, b))
         assert torch.equal(a, b)
     check_some(st, O, lse, sel.tolist(), every=17)
+
+
+# ---- a frame whose tokens see each other ----
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_frame_whose_tokens_see_each_other(cuda_ok, fp8):
+    # appended as rows of its sequence, then a sequence for each row
+    m = pav()
+    st = Step([300], [90], H=8, Hkv=4, ps=32, rot=128, fp8=fp8, n_select=6, seed=96)
+    cos, sin = st.tables(400)
+    st.append(cos, sin, Q_out=st.Q)
+    st.p = m.make_cache_params(n_pages=st.P, page_size=32, H=8, Hkv=4, d=128, S=90, T=90, max_pages=st.W,
+                               format=int(fp8), n_select=6)
+    st.S, st.cu, st.t_cu = 90, None, None
+    st.lens, st.t_lens = st.lens * 90, st.t_lens.repeat(90)
+    st.table, st.t_table = st.table * 90, st.t_table.repeat(90, 1)
+    st.ws = m.alloc_cache_workspace(st.p, DEV)
+    st.check(*st.decode())
+    same_choice(st)
+    sel = st.select()
+    O, lse = st.sparse(sel)
+    st.check(O, lse, sel.tolist())
+    assert st.status() == 0
